@@ -65,6 +65,13 @@ extern "C" {
                           token, weights per output channel), everything else as
                           ALBERT_BF16; see albert_test_quant_e4m3               */
 
+/* ---- microscaled 4-bit formats (see albert_mx4_quantize) ---- */
+#define ALBERT_MXFP4 3 /* E2M1 values, blocks of 32, power-of-two scales (E8M0)  */
+#define ALBERT_NVFP4 4 /* E2M1 values, blocks of 16, E4M3 scales times one fp32
+                          factor per tensor                                      */
+/* ---- element types of the 4-bit entries' rows: ALBERT_BF16, ALBERT_FP32, or ---- */
+#define ALBERT_FP16 5
+
 /* Architecture and capacity.  The kernels support exactly: emb 128, hidden 768,
  * heads 12 (64 wide), ffn 2048, max_pos <= 512, out_dim 512 or 0 (0 = return the
  * [.., 768] hidden states).  n_exec >= 0 is free.  n_groups: distinct layer weight
@@ -315,6 +322,92 @@ int albert_length_regulate(const float *logits, int C, float speed, const void *
 
 /* Bytes of device scratch albert_length_regulate needs for n_tok tokens. */
 size_t albert_length_regulate_scratch_bytes(int n_tok);
+
+/* ---- microscaled 4-bit rows: quantization, LayerNorm, linear layers ----
+ * The pages evaluate a quantized build of the encoder against its FP32 outputs
+ * ("Kokoro-82M-encoder-hailo10h", section "Eval results"); these are this
+ * library's 4-bit forms of the same layers.
+ *
+ * A 4-bit tensor [rows, cols] is two device buffers the caller owns, each 16-byte
+ * aligned:
+ *   codes   albert_mx4_codes_bytes: rows x (cols rounded up to 32) / 2 bytes, two
+ *           E2M1 codes per byte (even column in the low nibble; sign, 2 exponent
+ *           bits, 1 mantissa bit: 0 .5 1 1.5 2 3 4 6); columns past cols hold 0;
+ *   scales  albert_mx4_scales_bytes: tiles of 128 rows x 4 blocks of a row, 512
+ *           bytes each, [ceil(rows / 128)][tiles per row]: the scale of row r,
+ *           block b is byte (r % 32) * 16 + (r % 128) / 32 * 4 + b % 4 of tile
+ *           [r / 128][b / 4].  Tiles per row cover cols rounded up to 256.
+ * and a format with, for ALBERT_NVFP4, a tensor scale ts (a host float, finite,
+ * 2^-100 <= ts <= 2^100; ignored for ALBERT_MXFP4).  For a block with largest
+ * magnitude amax:
+ *   ALBERT_MXFP4  byte = max(floor(log2 amax) - 2, -127) + 127, s = 2^(byte - 127),
+ *                 q = E2M1(x / s);                          value = q * s
+ *   ALBERT_NVFP4  byte = E4M3(fl(amax / fl(6 ts))) with value sb, saturating at 448,
+ *                 q = E2M1(fl(x * fl(1 / fl(sb ts))));      value = q * sb * ts
+ * with round to nearest, ties to even, and saturation at 6 (fl: fp32 rounding).
+ * A scale that rounds to 0 gives codes 0.  A block that holds an infinity or a
+ * NaN gets a NaN scale (255 / 127) and codes 0: all of it reads back as NaN.
+ *
+ * All entries below are asynchronous on `stream`, allocate nothing, and run on
+ * the current device, which must be the one the buffers are on.  Row strides
+ * (ld*) are in elements and at least the row length; rows of x, y, residual and
+ * out may have any alignment of their element type.  rows == 0 does nothing.
+ * Host errors: ALBERT_ERR_NULL; ALBERT_ERR_SHAPE (rows < 0, a width outside
+ * [1, 2^24], an ld below the row length); ALBERT_ERR_CONFIG (unknown format or
+ * type, a tensor scale out of range, unaligned codes or scales). */
+size_t albert_mx4_codes_bytes(int rows, int cols);
+size_t albert_mx4_scales_bytes(int rows, int cols, int fmt);
+
+/* x [rows, cols] of x_type -> codes, scales. */
+int albert_mx4_quantize(const void *x, int x_type, long long ld_x, int rows, int cols, int fmt, float tensor_scale,
+                        void *codes, void *scales, void *stream);
+
+/* The values of a 4-bit tensor, rounded once to out_type: out [rows, cols]. */
+int albert_mx4_dequantize(const void *codes, const void *scales, int rows, int cols, int fmt, float tensor_scale,
+                          void *out, int out_type, long long ld_out, void *stream);
+
+/* LayerNorm over each row of x (fp32 statistics; gamma, beta [cols] fp32):
+ * y [rows, cols] of x_type (may be NULL), and the 4-bit form of the fp32 result. */
+int albert_mx4_layer_norm(const void *x, int x_type, long long ld_x, const float *gamma, const float *beta, float eps,
+                          int rows, int cols, int fmt, float tensor_scale, void *y, long long ld_y, void *codes,
+                          void *scales, void *stream);
+
+/* A linear layer on 4-bit operands:
+ *   z = A W^T + bias (tcgen05, fp32 accumulation over the scaled products)
+ *   z = 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)))   if gelu
+ *   z = z + residual                                     if residual
+ * then out = z rounded once to out_type, or the 4-bit form of z (q_codes,
+ * q_scales).  A [rows, k] is either 4-bit (a_codes, a_scales) or x of x_type,
+ * which is quantized as albert_mx4_quantize does (same result as calling it).
+ * W [n, k] is 4-bit, as albert_mx4_quantize leaves a weight matrix. */
+typedef struct {
+    const void *x;             /* rows to quantize, or NULL                      */
+    const void *a_codes;       /* 4-bit rows (x == NULL)                         */
+    const void *a_scales;
+    const void *w_codes;
+    const void *w_scales;
+    const float *bias;         /* [n] or NULL                                    */
+    const void *residual;      /* [rows, n] of out_type, or NULL                 */
+    void *out;                 /* [rows, n], or NULL for a 4-bit result          */
+    void *q_codes;             /* 4-bit result [rows, n] (out == NULL)           */
+    void *q_scales;
+    void *workspace;           /* albert_mx4_linear_workspace_bytes, 16-byte aligned;
+                                  used when x is given; one call at a time       */
+    long long ld_x, ld_residual, ld_out;
+    float x_scale;             /* tensor scale of A                              */
+    float w_scale;             /* tensor scale of W                              */
+    float q_scale;             /* tensor scale of the 4-bit result               */
+    int x_type, out_type;
+    int rows, n, k, fmt;       /* one format for A, W and the 4-bit result       */
+    int gelu;
+} albert_mx4_linear_args;
+int albert_mx4_linear(const albert_mx4_linear_args *args, void *stream);
+size_t albert_mx4_linear_workspace_bytes(int rows, int k, int fmt);
+
+/* The kernels of albert_mx4_linear bound every wait (2 s); a wait that runs out
+ * is recorded in a status word of the current device that all these calls share.
+ * This call synchronizes `stream`, returns the word and clears it. */
+int albert_mx4_get_status(void *stream);
 
 /* ---- single-kernel entry points (parity tests of one kernel) ----
  * These run one kernel of the path in isolation, synchronously, and return its

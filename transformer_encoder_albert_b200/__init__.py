@@ -19,7 +19,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(PKG, "libalbert_b200.so")
 
 ALBERT_OK = 0
-ALBERT_BF16, ALBERT_FP32, ALBERT_FP8 = 0, 1, 2
+ALBERT_BF16, ALBERT_FP32, ALBERT_FP8, ALBERT_MXFP4, ALBERT_NVFP4, ALBERT_FP16 = 0, 1, 2, 3, 4, 5
 DTYPES = {"bf16": ALBERT_BF16, "fp32": ALBERT_FP32, "fp8": ALBERT_FP8}
 STATUS_NAMES = {
     0: "ALBERT_OK", 1: "ALBERT_ERR_NULL", 2: "ALBERT_ERR_CONFIG", 3: "ALBERT_ERR_SHAPE",
@@ -43,6 +43,8 @@ EXPORTS = (
     "albert_gemm_residual_ln_noalloc", "albert_length_regulate", "albert_length_regulate_scratch_bytes",
     "albert_set_wait_limit", "albert_test_stall", "albert_set_small_batch_kernel", "albert_last_forward_launches",
     "albert_test_quant_e4m3", "albert_forward_embedded", "albert_test_attention_groups",
+    "albert_mx4_codes_bytes", "albert_mx4_scales_bytes", "albert_mx4_quantize", "albert_mx4_dequantize",
+    "albert_mx4_layer_norm", "albert_mx4_linear", "albert_mx4_linear_workspace_bytes", "albert_mx4_get_status",
 )
 
 
@@ -61,6 +63,14 @@ class albert_config(C.Structure):
 
 class albert_weights(C.Structure):
     _fields_ = [(n, C.c_void_p) for n in WEIGHT_FIELDS]
+
+
+class albert_mx4_linear_args(C.Structure):
+    _fields_ = [(n, C.c_void_p) for n in ("x", "a_codes", "a_scales", "w_codes", "w_scales", "bias", "residual", "out",
+                                          "q_codes", "q_scales", "workspace")] \
+        + [(n, C.c_longlong) for n in ("ld_x", "ld_residual", "ld_out")] \
+        + [(n, C.c_float) for n in ("x_scale", "w_scale", "q_scale")] \
+        + [(n, C.c_int) for n in ("x_type", "out_type", "rows", "n", "k", "fmt", "gelu")]
 
 
 _lib = None
@@ -107,6 +117,18 @@ def lib() -> C.CDLL:
         L.albert_test_quant_e4m3.argtypes = [vp, i, i, vp, vp, vp]
         L.albert_forward_embedded.argtypes = [vp, vp, vp, i, i, vp, vp]
         L.albert_test_attention_groups.argtypes = [vp, i, i, vp, C.POINTER(C.c_int), vp]
+        ll, f = C.c_longlong, C.c_float
+        L.albert_mx4_codes_bytes.argtypes = [i, i]
+        L.albert_mx4_codes_bytes.restype = C.c_size_t
+        L.albert_mx4_scales_bytes.argtypes = [i, i, i]
+        L.albert_mx4_scales_bytes.restype = C.c_size_t
+        L.albert_mx4_quantize.argtypes = [vp, i, ll, i, i, i, f, vp, vp, vp]
+        L.albert_mx4_dequantize.argtypes = [vp, vp, i, i, i, f, vp, i, ll, vp]
+        L.albert_mx4_layer_norm.argtypes = [vp, i, ll, vp, vp, f, i, i, i, f, vp, ll, vp, vp, vp]
+        L.albert_mx4_linear.argtypes = [C.POINTER(albert_mx4_linear_args), vp]
+        L.albert_mx4_linear_workspace_bytes.argtypes = [i, i, i]
+        L.albert_mx4_linear_workspace_bytes.restype = C.c_size_t
+        L.albert_mx4_get_status.argtypes = [vp]
         _lib = L
     return _lib
 
@@ -436,3 +458,248 @@ def length_regulate(logits, feats, cu_seqlens, speed: float = 1.0, max_frames: i
         return rc, None, None, None, None
     torch.cuda.current_stream().synchronize() if stream is None else stream.synchronize()
     return int(status.item()), dur, start, cu_frames, frames
+
+
+# ------------------------------------------------------ microscaled 4-bit rows --
+
+MX4_FORMATS = {"mxfp4": ALBERT_MXFP4, "nvfp4": ALBERT_NVFP4}
+_MX4_BLOCK = {"mxfp4": 32, "nvfp4": 16}
+
+
+class Mx4Tensor:
+    """A [rows, cols] matrix in microscaled 4-bit form (layout: albert.h): E2M1 codes,
+    uint8 [rows, ceil(cols / 32) * 16], and scale bytes, uint8 [ceil(rows / 128),
+    tiles per row, 512].  ``fmt`` is "mxfp4" or "nvfp4"; ``tensor_scale`` multiplies
+    every value of an "nvfp4" tensor (ignored for "mxfp4")."""
+
+    __slots__ = ("codes", "scales", "rows", "cols", "fmt", "tensor_scale")
+
+    def __init__(self, codes, scales, rows: int, cols: int, fmt: str = "mxfp4", tensor_scale: float = 1.0):
+        import torch
+        shapes = mx4_shapes(rows, cols, fmt)
+        for name, t, shape in (("codes", codes, shapes[0]), ("scales", scales, shapes[1])):
+            if tuple(t.shape) != shape or t.dtype != torch.uint8 or not t.is_contiguous():
+                raise ValueError(f"Mx4Tensor: {name} must be a contiguous uint8 tensor of shape {shape}, "
+                                 f"got {tuple(t.shape)} {t.dtype}")
+        if codes.device != scales.device:
+            raise ValueError(f"Mx4Tensor: codes on {codes.device}, scales on {scales.device}")
+        if fmt == "nvfp4" and not 2.0 ** -100 <= tensor_scale <= 2.0 ** 100:
+            raise ValueError(f"Mx4Tensor: tensor_scale {tensor_scale} outside [2^-100, 2^100]")
+        self.codes, self.scales, self.rows, self.cols = codes, scales, rows, cols
+        self.fmt, self.tensor_scale = fmt, float(tensor_scale)
+
+    @property
+    def shape(self):
+        return (self.rows, self.cols)
+
+    @property
+    def device(self):
+        return self.codes.device
+
+
+def mx4_shapes(rows: int, cols: int, fmt: str):
+    """Shapes of the code and scale tensors of a [rows, cols] 4-bit matrix."""
+    if fmt not in MX4_FORMATS:
+        raise ValueError(f"format must be one of {sorted(MX4_FORMATS)}, got {fmt!r}")
+    if rows < 0 or not 1 <= cols <= 1 << 24:
+        raise ValueError(f"a 4-bit matrix has rows >= 0 and 1 <= cols <= 2^24, got [{rows}, {cols}]")
+    tiles = (cols + 255) // 256 * (256 // (4 * _MX4_BLOCK[fmt]))
+    return (rows, (cols + 31) // 32 * 16), ((rows + 127) // 128, tiles, 512)
+
+
+def mx4_empty(rows: int, cols: int, fmt: str = "mxfp4", tensor_scale: float = 1.0, device="cuda") -> Mx4Tensor:
+    """A 4-bit matrix with uninitialised contents."""
+    import torch
+    c, s = mx4_shapes(rows, cols, fmt)
+    return Mx4Tensor(torch.empty(c, dtype=torch.uint8, device=device),
+                     torch.empty(s, dtype=torch.uint8, device=device), rows, cols, fmt, tensor_scale)
+
+
+def _mx4_type(t, what: str) -> int:
+    import torch
+    code = {torch.bfloat16: ALBERT_BF16, torch.float32: ALBERT_FP32, torch.float16: ALBERT_FP16}.get(t)
+    if code is None:
+        raise ValueError(f"{what} must be bfloat16, float16 or float32, got {t}")
+    return code
+
+
+def _mx4_rows(t, what: str, shape=None) -> int:
+    """Check a matrix of rows (unit column stride, any row stride); its row stride."""
+    import torch
+    if not t.is_cuda or t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
+        want = "" if shape is None else f" of shape {tuple(shape)}"
+        raise ValueError(f"{what} must be a 2-D CUDA tensor{want}, got {tuple(t.shape)} on {t.device}")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what} must have unit stride along its columns, got strides {t.stride()}")
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{what} requires grad: the 4-bit operators have no backward pass (use torch.no_grad())")
+    ld = t.stride(0)
+    if rows > 1 and ld < cols:
+        raise ValueError(f"{what}: rows overlap (strides {t.stride()})")
+    return ld if rows > 1 else cols
+
+
+def _mx4_vector(t, n: int, what: str, device):
+    import torch
+    if tuple(t.shape) != (n,) or t.dtype != torch.float32 or not t.is_contiguous() or t.device != device:
+        raise ValueError(f"{what} must be a contiguous float32 tensor of shape ({n},) on {device}, "
+                         f"got {tuple(t.shape)} {t.dtype} on {t.device}")
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{what} requires grad: the 4-bit operators have no backward pass (use torch.no_grad())")
+    return t.data_ptr()
+
+
+def _mx4_same(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+class _Mx4On:
+    """Run allocations and launches on `device`, and on `stream` if one is given."""
+
+    __slots__ = ("ctx",)
+
+    def __init__(self, device, stream):
+        import torch
+        self.ctx = []
+        if stream is not None:
+            if stream.device != device:
+                raise ValueError(f"stream of {stream.device} for tensors on {device}")
+            self.ctx.append(torch.cuda.stream(stream))
+        elif torch.cuda.current_device() != device.index:
+            self.ctx.append(torch.cuda.device(device))
+
+    def __enter__(self):
+        for c in self.ctx:
+            c.__enter__()
+
+    def __exit__(self, *a):
+        for c in self.ctx:
+            c.__exit__(*a)
+
+
+def mx4_quantize(x, fmt: str = "mxfp4", tensor_scale: float = 1.0, out: Mx4Tensor | None = None, stream=None) -> Mx4Tensor:
+    """Rows of x [rows, cols] (bf16, fp16 or fp32, any row stride) in 4-bit form
+    (albert_mx4_quantize).  Asynchronous; outputs are allocated on the stream used."""
+    ld, typ = _mx4_rows(x, "x"), _mx4_type(x.dtype, "x")
+    rows, cols = x.shape
+    with _Mx4On(x.device, stream):
+        if out is None:
+            out = mx4_empty(rows, cols, fmt, tensor_scale, x.device)
+        elif out.shape != (rows, cols) or out.fmt != fmt or out.device != x.device:
+            raise ValueError(f"out must be a {fmt} matrix of shape {(rows, cols)} on {x.device}")
+        else:
+            out = Mx4Tensor(out.codes, out.scales, rows, cols, fmt, tensor_scale)
+        _check(lib().albert_mx4_quantize(_ptr(x), typ, ld, rows, cols, MX4_FORMATS[fmt], out.tensor_scale,
+                                         _ptr(out.codes), _ptr(out.scales), _stream_ptr()), "albert_mx4_quantize")
+    return out
+
+
+def mx4_dequantize(t: Mx4Tensor, dtype=None, out=None, stream=None):
+    """The values of a 4-bit matrix, rounded once to `dtype` (default bfloat16)."""
+    import torch
+    if not t.codes.is_cuda:
+        raise ValueError(f"the 4-bit matrix must be on a CUDA device, got {t.device}")
+    if out is not None and dtype is not None and out.dtype != dtype:
+        raise ValueError(f"out is {out.dtype}, dtype is {dtype}")
+    with _Mx4On(t.device, stream):
+        if out is None:
+            out = torch.empty(t.rows, t.cols, dtype=torch.bfloat16 if dtype is None else dtype, device=t.device)
+        ld, typ = _mx4_rows(out, "out", t.shape), _mx4_type(out.dtype, "out")
+        _mx4_same(t.device, out=out)
+        _check(lib().albert_mx4_dequantize(_ptr(t.codes), _ptr(t.scales), t.rows, t.cols, MX4_FORMATS[t.fmt],
+                                           t.tensor_scale, _ptr(out), typ, ld, _stream_ptr()), "albert_mx4_dequantize")
+    return out
+
+
+def mx4_layer_norm(x, gamma, beta, eps: float = 1e-12, fmt: str = "mxfp4", tensor_scale: float = 1.0,
+                   return_rows: bool = True, stream=None):
+    """LayerNorm over the rows of x: (y in x's dtype, or None if not return_rows;
+    the 4-bit form of the fp32 result) in one pass (albert_mx4_layer_norm)."""
+    import torch
+    ld, typ = _mx4_rows(x, "x"), _mx4_type(x.dtype, "x")
+    rows, cols = x.shape
+    g, b = _mx4_vector(gamma, cols, "gamma", x.device), _mx4_vector(beta, cols, "beta", x.device)
+    with _Mx4On(x.device, stream):
+        y = torch.empty(rows, cols, dtype=x.dtype, device=x.device) if return_rows else None
+        q = mx4_empty(rows, cols, fmt, tensor_scale, x.device)
+        _check(lib().albert_mx4_layer_norm(_ptr(x), typ, ld, g, b, float(eps), rows, cols, MX4_FORMATS[fmt],
+                                           q.tensor_scale, _ptr(y), cols, _ptr(q.codes), _ptr(q.scales),
+                                           _stream_ptr()), "albert_mx4_layer_norm")
+    return y, q
+
+
+def _mx4_linear(x, w: Mx4Tensor, bias, residual, gelu, x_scale, stream, out, out_dtype, q_scale):
+    import torch
+    a = albert_mx4_linear_args()
+    if isinstance(x, Mx4Tensor):
+        if x.fmt != w.fmt:
+            raise ValueError(f"x is {x.fmt}, w is {w.fmt}")
+        if not x.codes.is_cuda:
+            raise ValueError(f"x must be on a CUDA device, got {x.device}")
+        rows, k = x.shape
+        a.a_codes, a.a_scales, a.x_scale = _ptr(x.codes), _ptr(x.scales), x.tensor_scale
+    else:
+        a.ld_x, a.x_type = _mx4_rows(x, "x"), _mx4_type(x.dtype, "x")
+        rows, k = x.shape
+        a.x, a.x_scale = _ptr(x), float(x_scale)
+    device, n = x.device, w.rows
+    if w.cols != k or n < 1:
+        raise ValueError(f"x is [{rows}, {k}], w is {list(w.shape)}: w must be [n >= 1, {k}]")
+    _mx4_same(device, w=w)
+    a.w_codes, a.w_scales, a.w_scale = _ptr(w.codes), _ptr(w.scales), w.tensor_scale
+    a.rows, a.n, a.k, a.fmt, a.gelu = rows, n, k, MX4_FORMATS[w.fmt], 1 if gelu else 0
+    if bias is not None:
+        a.bias = _mx4_vector(bias, n, "bias", device)
+    with _Mx4On(device, stream):
+        if q_scale is None:
+            if out is None:
+                out = torch.empty(rows, n, dtype=out_dtype, device=device)
+            a.ld_out, a.out_type = _mx4_rows(out, "out", (rows, n)), _mx4_type(out.dtype, "out")
+            _mx4_same(device, out=out)
+            a.out = _ptr(out)
+        else:
+            out = mx4_empty(rows, n, w.fmt, q_scale, device)
+            a.q_codes, a.q_scales, a.q_scale = _ptr(out.codes), _ptr(out.scales), out.tensor_scale
+        if residual is not None:
+            a.ld_residual = _mx4_rows(residual, "residual", (rows, n))
+            if q_scale is not None or residual.dtype != out.dtype:
+                raise ValueError(f"residual must have the result's type ({out_dtype if q_scale is None else 'none'}), "
+                                 f"got {residual.dtype}")
+            _mx4_same(device, residual=residual)
+            a.residual = _ptr(residual)
+        if a.x:
+            ws = lib().albert_mx4_linear_workspace_bytes(rows, k, a.fmt)
+            if ws:
+                work = torch.empty(ws, dtype=torch.uint8, device=device)
+                a.workspace = _ptr(work)
+        _check(lib().albert_mx4_linear(C.byref(a), _stream_ptr()), "albert_mx4_linear")
+    return out
+
+
+def mx4_linear(x, w: Mx4Tensor, bias=None, residual=None, gelu: bool = False, dtype=None, x_scale: float = 1.0,
+               out=None, stream=None):
+    """x W^T + bias, tanh-GELU if `gelu`, + residual (albert_mx4_linear) -> [rows, n].
+
+    x: rows (bf16, fp16 or fp32), quantized in the call with tensor scale x_scale as
+    mx4_quantize does, or a 4-bit matrix of w's format.  w: [n, k] 4-bit weights.
+    bias [n] fp32; residual [rows, n] of the result's dtype (default bfloat16)."""
+    import torch
+    if out is not None and dtype is not None and out.dtype != dtype:
+        raise ValueError(f"out is {out.dtype}, dtype is {dtype}")
+    return _mx4_linear(x, w, bias, residual, gelu, x_scale, stream, out, torch.bfloat16 if dtype is None else dtype,
+                       None)
+
+
+def mx4_linear_quant(x, w: Mx4Tensor, bias=None, gelu: bool = False, x_scale: float = 1.0, out_scale: float = 1.0,
+                     stream=None) -> Mx4Tensor:
+    """mx4_linear whose fp32 result leaves in w's 4-bit format (tensor scale out_scale)."""
+    return _mx4_linear(x, w, bias, None, gelu, x_scale, stream, None, None, float(out_scale))
+
+
+def mx4_status(stream=None) -> int:
+    """Synchronize the stream; status of the 4-bit linear layers run on this device
+    since the last call (ALBERT_OK, or ALBERT_ERR_TIMEOUT after an expired wait)."""
+    return lib().albert_mx4_get_status(_stream_ptr(stream))

@@ -1,0 +1,198 @@
+// mx4.cuh -- microscaled 4-bit values on the device: E2M1 codes with one 8-bit
+// scale per block along a row ("mxfp4": blocks of 32, E8M0 scales; "nvfp4":
+// blocks of 16, E4M3 scales times one fp32 factor of the tensor).
+//
+// The decisions (scale byte, code) are taken in fp32 exactly as include/albert.h
+// states them, so that two kernels that quantize the same fp32 values agree bit
+// for bit:
+//   mxfp4: byte = max(biased exponent of amax - 2, 0); q = E2M1(x * 2^(127 - byte)),
+//          the power of two exact, so the only rounding is E2M1's;
+//   nvfp4: byte = E4M3(fl(amax / six_ts)), d = fl(E4M3 value * ts), q = E2M1(fl(x * fl(1 / d))).
+#pragma once
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+namespace albert {
+
+// Storage geometry.  A scale tile holds 128 rows x 4 blocks (512 bytes): byte
+// (r % 32) * 16 + (r % 128) / 32 * 4 + b % 4 -- the order in which tcgen05.cp
+// (32x128b, replicated to the four lane quadrants) brings a 128-row operand's
+// scales to tensor memory.  A row's tiles cover a multiple of 256 columns, one
+// stage of the products' main loop.
+constexpr int kMx4StageCols = 256;
+constexpr int kMx4TileBytes = 512;
+template <bool NV>
+struct Mx4 {
+    static constexpr int kBlock = NV ? 16 : 32;
+    static constexpr int kTileCols = 4 * kBlock;                   // columns of one scale tile
+    static constexpr int kStageTiles = kMx4StageCols / kTileCols;  // 4 (nvfp4) or 2 (mxfp4)
+};
+__host__ __device__ __forceinline__ int mx4_stages(int cols) { return (cols + kMx4StageCols - 1) / kMx4StageCols; }
+__host__ __device__ __forceinline__ int mx4_code_pitch(int cols) { return (cols + 31) / 32 * 16; }  // bytes per row
+
+// Eight fp32 -> eight E2M1 codes, value i in nibble i: nearest, ties to the even
+// code, saturating at 6.
+__device__ __forceinline__ uint32_t cvt_e2m1x8(const float (&v)[8]) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n\t"
+        "mov.b32 %0, {b0, b1, b2, b3};\n\t}"
+        : "=r"(r) : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+    return r;
+}
+
+// E2M1 code -> value: sign, 2 exponent bits (bias 1), 1 mantissa bit.
+__device__ __forceinline__ float e2m1_value(uint32_t c) {
+    const uint32_t e = (c >> 1) & 3u, m = c & 1u;
+    const float mag = e == 0 ? 0.5f * m : (1.0f + 0.5f * m) * (float)(1u << (e - 1));
+    return (c & 8u) ? -mag : mag;
+}
+
+__device__ __forceinline__ float e8m0_value(uint32_t byte) {
+    // 2^(byte - 127): byte 0 is below fp32's normals, byte 255 is NaN
+    return __uint_as_float(byte == 0 ? 0x00400000u : byte == 255u ? 0x7fffffffu : byte << 23);
+}
+__device__ __forceinline__ float e4m3_value(uint32_t byte) {
+    const uint32_t e = (byte >> 3) & 15u, m = byte & 7u;
+    if ((byte & 0x7fu) == 0x7fu) return __uint_as_float(0x7fffffffu);
+    // (1 + m/8) 2^(e-7), subnormals m/8 2^-6
+    const float mag = e == 0 ? (float)m * 0.001953125f : __uint_as_float(((e + 120u) << 23) | (m << 20));
+    return (byte & 0x80u) ? -mag : mag;
+}
+template <bool NV>
+__device__ __forceinline__ float mx4_scale_value(uint32_t byte) {
+    return NV ? e4m3_value(byte) : e8m0_value(byte);
+}
+
+// One block's scale byte, and the factor its values are multiplied by before the
+// rounding to E2M1.  amax_bits: the largest |x| of the block as bits (integer
+// order puts infinities and NaN above every finite value); a block that holds
+// one gets a NaN scale and zero codes (factor 0 with the values replaced by 0).
+struct Mx4Scale {
+    uint32_t byte;
+    float mul;
+    bool zero;  // codes are 0 whatever the values
+};
+template <bool NV>
+__device__ __forceinline__ Mx4Scale mx4_block_scale(uint32_t amax_bits, float ts, float six_ts) {
+    Mx4Scale s;
+    const bool bad = amax_bits >= 0x7f800000u;
+    if constexpr (!NV) {
+        const uint32_t e = amax_bits >> 23;
+        s.byte = bad ? 255u : (e > 2u ? e - 2u : 0u);
+        s.mul = __uint_as_float((254u - (bad ? 127u : s.byte)) << 23);
+        s.zero = bad;
+    } else {
+        const float t = __fdiv_rn(__uint_as_float(bad ? 0u : amax_bits), six_ts);
+        uint16_t c;
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(0.0f), "f"(t));
+        s.byte = bad ? 0x7fu : (uint32_t)(c & 0xffu);
+        s.zero = bad || s.byte == 0u;
+        const float d = __fmul_rn(e4m3_value(s.byte), ts);
+        s.mul = s.zero ? 0.0f : __fdiv_rn(1.0f, d);
+    }
+    return s;
+}
+
+template <typename T>
+__device__ __forceinline__ float to_f32(T x) {
+    if constexpr (sizeof(T) == 4) return x;
+    else return static_cast<float>(x);
+}
+template <typename T>
+__device__ __forceinline__ T from_f32(float x) {
+    if constexpr (sizeof(T) == 4) return x;
+    else if constexpr (std::is_same<T, __half>::value) return __float2half_rn(x);
+    else return __float2bfloat16_rn(x);
+}
+
+// Two floats as one 32-bit word of two 16-bit values.
+template <typename T>
+__device__ __forceinline__ uint32_t pack_x2(float lo, float hi) {
+    if constexpr (std::is_same<T, __half>::value) {
+        const __half2 v = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    } else {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&v);
+    }
+}
+template <typename T>
+__device__ __forceinline__ float2 unpack_x2(uint32_t u) {
+    if constexpr (std::is_same<T, __half>::value) return __half22float2(*reinterpret_cast<const __half2 *>(&u));
+    else return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u));
+}
+
+// Eight consecutive values of a row from p; only the first `n` (0..8) exist, the
+// rest read as 0.  vec: p is 16-byte aligned whenever all eight exist.
+template <typename T>
+__device__ __forceinline__ void load8(const T *p, int n, bool vec, float (&v)[8]) {
+    if (vec && n >= 8) {
+        if constexpr (sizeof(T) == 4) {
+            const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
+            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+        } else {
+            const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p));
+            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = unpack_x2<T>(w[i]);
+                v[2 * i] = f.x;
+                v[2 * i + 1] = f.y;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = i < n ? to_f32<T>(p[i]) : 0.0f;
+    }
+}
+template <typename T>
+__device__ __forceinline__ void store8(T *p, int n, bool vec, const float (&v)[8]) {
+    if (vec && n >= 8) {
+        if constexpr (sizeof(T) == 4) {
+            reinterpret_cast<float4 *>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+            reinterpret_cast<float4 *>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+            *reinterpret_cast<uint4 *>(p) = make_uint4(pack_x2<T>(v[0], v[1]), pack_x2<T>(v[2], v[3]),
+                                                       pack_x2<T>(v[4], v[5]), pack_x2<T>(v[6], v[7]));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (i < n) p[i] = from_f32<T>(v[i]);
+    }
+}
+
+__device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
+__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
+// A warp quantizes 256 consecutive columns of a row, eight per lane: the block's
+// lanes (four, or two) share its largest value by shuffles.  Returns the lane's
+// codes; `word` becomes the four scale bytes of the lane's tile (every lane of
+// the tile holds it).
+template <bool NV>
+__device__ __forceinline__ uint32_t mx4_warp_quant(const float (&v)[8], float ts, float six_ts, int lane, uint32_t &word) {
+    uint32_t m = abs_bits(v[0]);
+#pragma unroll
+    for (int i = 1; i < 8; ++i) m = umax(m, abs_bits(v[i]));
+    m = umax(m, __shfl_xor_sync(0xffffffffu, m, 1));
+    if constexpr (!NV) m = umax(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    const Mx4Scale s = mx4_block_scale<NV>(m, ts, six_ts);
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = __fmul_rn(v[i], s.mul);
+    uint32_t q = cvt_e2m1x8(y);
+    if (s.zero) q = 0;
+    constexpr int kLanes = NV ? 2 : 4;  // lanes of a block
+    uint32_t w = s.byte << (8 * ((lane / kLanes) & 3));
+    w |= __shfl_xor_sync(0xffffffffu, w, kLanes);
+    w |= __shfl_xor_sync(0xffffffffu, w, 2 * kLanes);
+    word = w;
+    return q;
+}
+
+}  // namespace albert
