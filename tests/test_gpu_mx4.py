@@ -200,6 +200,8 @@ LINEAR = [  # rows, n, k
     (1, 1, 1), (1, 16, 32), (1, 2304, 768), (2, 48, 100), (8, 130, 256), (16, 512, 2048), (17, 257, 320), (33, 96, 768),
     (64, 129, 1000), (127, 768, 768), (128, 128, 256), (129, 300, 288), (200, 1001, 1000), (257, 2304, 64),
     (300, 256, 2080), (513, 520, 520), (1025, 192, 256),
+    # enough 256x256 tiles for CTA pairs, with ragged last tiles, one and several tiles per pair
+    (2501, 2001, 544), (5000, 2304, 96), (9000, 1040, 1100),
 ]
 
 
@@ -242,7 +244,7 @@ def test_linear_against_the_oracle(rows, n, k, fmt):
 
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("rows,n,k", [(1, 32, 32), (1, 2048, 768), (5, 100, 96), (16, 33, 256), (40, 256, 300), (130, 320, 768),
-                                      (300, 2048, 256), (129, 1000, 64)])
+                                      (300, 2048, 256), (129, 1000, 64), (2600, 2020, 288), (10000, 1030, 96)])
 def test_linear_with_a_4_bit_result(rows, n, k, fmt):
     rng = np.random.default_rng(rows + n + k)
     x, t = _rows(rng, rows, k, "bf16")

@@ -1,7 +1,28 @@
-// mx4_gemm.cu -- the linear layer on microscaled 4-bit operands.
+// mx4_gemm.cu -- the linear layer on microscaled 4-bit operands, many rows.
 //
-// First form: 64x64 tiles, operands read back to fp32 in shared memory, fp32
-// products and sums on the CUDA cores.
+// z = alpha A W^T + bias, tanh-GELU, + residual; A [M, K] and W [N, K] as E2M1
+// codes with block scales (mx4.cuh), the products and the multiplication by both
+// scales on tcgen05 (kind::mxf4 / mxf4nvf4, block_scale), sums in fp32.
+//
+// Persistent, one CTA per SM, warp-specialized like the bf16 GEMM:
+//   warp 0     : TMA producer: per stage 256 columns of A and W (128-byte rows,
+//                128-byte swizzle) and their scale tiles (512 bytes per 128 rows and
+//                four blocks, plain);
+//   warp 1     : issues, per stage, the copies of the scale tiles to tensor memory
+//                and four products of K = 64;
+//   warps 2..9 : epilogue, a lane quadrant each, two warps per quadrant taking
+//                alternate 32-column chunks.
+// Two tile shapes:
+//   * a CTA pair per 256x256 tile (cta_group::2): each CTA stages 128 rows of A and of
+//     W and the scales of its A rows and of all W rows.  Two 256-column accumulators
+//     would fill tensor memory; they overlap by 96 columns, which leaves 96 for the
+//     scales (two stages).  The epilogue first reads the chunks that lie in the
+//     overlap into registers, so the next tile's products start after two loads.
+//   * one CTA per 128x128 tile, two separate accumulators, for work that would leave
+//     pairs idle.
+// Scale columns are written again only after the products that read them have
+// completed (their stage's empty barrier), two stages later.
+// Every wait is bounded; see the bf16 GEMM.
 #include <type_traits>
 
 #include "kernels.h"
@@ -11,103 +32,427 @@
 namespace albert {
 namespace {
 
-constexpr int TM = 64, TN = 64, TK = 32;
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = 32 * (2 + kEpiWarps);
+constexpr int kRowsBytes = 128 * 128;  // 128 rows x 256 columns of codes
 
-__device__ __forceinline__ float load_elem(const void *p, int type, size_t i) {
-    if (type == kElemF32) return static_cast<const float *>(p)[i];
-    if (type == kElemF16) return __half2float(static_cast<const __half *>(p)[i]);
-    return __bfloat162float(static_cast<const bf16 *>(p)[i]);
-}
-__device__ __forceinline__ void store_elem(void *p, int type, size_t i, float v) {
-    if (type == kElemF32) static_cast<float *>(p)[i] = v;
-    else if (type == kElemF16) static_cast<__half *>(p)[i] = __float2half_rn(v);
-    else static_cast<bf16 *>(p)[i] = __float2bfloat16_rn(v);
+template <bool NV, bool PAIR>
+struct Plan {
+    static constexpr int TN = PAIR ? 256 : 128;              // columns of a tile
+    static constexpr int UM = PAIR ? 256 : 128;              // rows of a tile
+    static constexpr int ST = Mx4<NV>::kStageTiles;          // scale tiles per 128 rows and stage
+    static constexpr int SFA = ST * kMx4TileBytes;
+    static constexpr int SFB = (TN / 128) * SFA;
+    static constexpr int STAGE = 2 * kRowsBytes + SFA + SFB;  // bytes per CTA and stage
+    static constexpr int NST = 5;
+    static constexpr int ACC1 = PAIR ? 160 : 128;            // first column of the second accumulator
+    static constexpr int SFCOL = PAIR ? 416 : 256;           // first scale column
+    static constexpr int SFBUF = 4 * ST * (1 + TN / 128);    // scale columns per stage
+    static constexpr int PER = TN / 64;                      // 32-column chunks per epilogue warp
+    static constexpr int SMEM = 1024 + NST * STAGE + kEpiWarps * PER * 128 + 1024;
+    static_assert(SFCOL + 2 * SFBUF <= 512, "tensor memory columns");
+    static_assert(SMEM <= 232448, "shared memory per CTA");
+};
+
+struct Ctrl {
+    uint64_t *full, *empty, *tfull, *tfree, *drain;
+    uint32_t *tmem_slot;
+    volatile int *abort_flag;
+    int *misc;
+};
+
+// GELU_tanh(x) = x / (1 + exp(-2u)), u = sqrt(2/pi) (x + 0.044715 x^3): relative
+// error a few 2^-23 plus 2^-23 |2u| of the exponential's argument.
+__device__ __forceinline__ float gelu_exact(float x) {
+    const float k = -2.0f * 0.7978845608028654f * 1.4426950408889634f;
+    const float e = ex2_approx(k * x * fmaf(0.044715f * x, x, 1.0f));
+    return __fdividef(x, 1.0f + e);
 }
 
-template <bool NV>
-__device__ __forceinline__ float read_value(const uint8_t *codes, const uint8_t *scales, int rows, int K, int row, int k) {
-    if (row >= rows || k >= K) return 0.f;
-    const uint8_t c = codes[(size_t)row * mx4_code_pitch(K) + k / 2];
-    const int blk = k / Mx4<NV>::kBlock, tiles = mx4_stages(K) * Mx4<NV>::kStageTiles;
-    const uint8_t sb = scales[((size_t)(row >> 7) * tiles + (blk >> 2)) * kMx4TileBytes + (row & 31) * 16 +
-                              ((row >> 5) & 3) * 4 + (blk & 3)];
-    return e2m1_value((k & 1) ? c >> 4 : c & 15) * mx4_scale_value<NV>(sb);
+template <typename T>
+__device__ __forceinline__ void add_row(const T *p, int n, bool vec, float (&v)[32]) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        float r[8];
+        const int left = n - 8 * q;
+        load8<T>(p + 8 * q, left > 0 ? left : 0, vec, r);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[8 * q + i] += r[i];
+    }
+}
+template <typename T>
+__device__ __forceinline__ void store_row(T *p, int n, bool vec, const float (&v)[32]) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        float r[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[i] = v[8 * q + i];
+        const int left = n - 8 * q;
+        store8<T>(p + 8 * q, left > 0 ? left : 0, vec, r);
+    }
 }
 
-template <bool NV>
-__global__ void __launch_bounds__(256) mx4_gemm_kernel(const Mx4GemmArgs p) {
-    __shared__ float sa[TM][TK + 1], sb[TN][TK + 1];
-    __shared__ float st[TM][TN + 1];
+template <bool NV, bool PAIR, bool QOUT>
+__global__ void __launch_bounds__(kThreads, 1)
+mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB, const Mx4GemmArgs p,
+                int n_sub, int vec_out, int vec_res) {
+    using P = Plan<NV, PAIR>;
+    constexpr int NST = P::NST, TN = P::TN, ST = P::ST;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *sA = base, *sB = sA + NST * kRowsBytes, *sSA = sB + NST * kRowsBytes, *sSB = sSA + NST * P::SFA;
+    float *sBias = reinterpret_cast<float *>(sSB + NST * P::SFB);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(reinterpret_cast<uint8_t *>(sBias) + kEpiWarps * P::PER * 128);
+    Ctrl c;
+    c.full = bars;
+    c.empty = bars + NST;
+    c.tfull = bars + 2 * NST;
+    c.tfree = bars + 2 * NST + 2;
+    c.drain = bars + 2 * NST + 4;
+    uint32_t *u32 = reinterpret_cast<uint32_t *>(bars + 2 * NST + 5);
+    c.tmem_slot = u32;
+    c.abort_flag = reinterpret_cast<volatile int *>(u32 + 1);
+    c.misc = reinterpret_cast<int *>(u32 + 2);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = PAIR ? cluster_ctarank() : 0;
+    const int slot = PAIR ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
+    const int nslots = PAIR ? (int)(gridDim.x >> 1) : (int)gridDim.x;
+
     if (p.trigger) griddep_launch_dependents();
+    if (threadIdx.x == 0) {
+        *c.abort_flag = 0;
+        wait_limit_init(p.wait_ns);
+        for (int i = 0; i < NST; ++i) {
+            mbar_init(smem_u32(&c.full[i]), 1);
+            mbar_init(smem_u32(&c.empty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&c.tfull[i]), 1);
+            mbar_init(smem_u32(&c.tfree[i]), (PAIR ? 2 : 1) * kEpiWarps);
+        }
+        mbar_init(smem_u32(c.drain), 1);
+        fence_mbar_init();
+    }
+    if (warp == 0 && lane == 0) {
+        prefetch_tmap(&tmA);
+        prefetch_tmap(&tmB);
+        prefetch_tmap(&tmSA);
+        prefetch_tmap(&tmSB);
+    }
+    if (warp == 1) {
+        if (PAIR) {
+            tmem_alloc_pair(smem_u32(c.tmem_slot), 512);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(smem_u32(c.tmem_slot), 512);
+            tmem_relinquish();
+        }
+    }
     griddep_wait();
-    if (p.check_status && *reinterpret_cast<const volatile int *>(p.status) != 0) return;
-    int nr = p.n_rows ? *reinterpret_cast<const volatile int *>(p.n_rows) : p.M;
-    nr = nr < p.M ? nr : p.M;
-    const int m0 = blockIdx.y * TM, n0 = blockIdx.x * TN, tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    if (m0 >= nr) return;
-    float acc[4][4] = {};
-    for (int k0 = 0; k0 < p.K; k0 += TK) {
-        for (int i = threadIdx.x; i < TM * TK; i += 256) {
-            sa[i / TK][i % TK] = read_value<NV>(p.a, p.a_scales, nr, p.K, m0 + i / TK, k0 + i % TK);
-            sb[i / TK][i % TK] = read_value<NV>(p.w, p.w_scales, p.N, p.K, n0 + i / TK, k0 + i % TK);
-        }
-        __syncthreads();
-        for (int k = 0; k < TK; ++k)
-            for (int i = 0; i < 4; ++i)
-                for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(sa[ty * 4 + i][k], sb[tx * 4 + j][k], acc[i][j]);
-        __syncthreads();
+    if (threadIdx.x == 0) {
+        c.misc[0] = p.n_rows ? *reinterpret_cast<const volatile int *>(p.n_rows) : p.M;
+        c.misc[1] = p.check_status ? *reinterpret_cast<const volatile int *>(p.status) : 0;
     }
-    for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) {
-            const int row = m0 + ty * 4 + i, col = n0 + tx * 4 + j;
-            float v = 0.f;
-            if (row < nr && col < p.N) {
-                v = p.alpha * acc[i][j] + (p.bias ? p.bias[col] : 0.f);
-                if (p.gelu) v = v / (1.0f + __expf(-1.5957691216057308f * (v + 0.044715f * v * v * v)));
-                if (p.res) v += load_elem(p.res, p.out_type, (size_t)row * p.ld_res + col);
-                if (p.out) store_elem(p.out, p.out_type, (size_t)row * p.ld_out + col, v);
+    tc_fence_before();
+    if (PAIR) cluster_sync();
+    else __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *c.tmem_slot;
+
+    const bool skip = c.misc[1] != 0 || c.misc[0] < 0 || c.misc[0] > p.M;
+    const int n_rows = skip ? 0 : c.misc[0];
+    const int m_blocks = (n_rows + P::UM - 1) / P::UM;
+    const long long units = (long long)m_blocks * n_sub;
+    const int kblocks = mx4_stages(p.K);
+
+    if (warp == 0) {
+        // ------------------------------------------------------ TMA producer --
+        if (lane == 0) {
+            int stage = 0, issued = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            const long long loaded = p.withhold_loads ? 0 : units;
+            for (long long u = slot; u < loaded && ok; u += nslots) {
+                const int m = (int)(u / n_sub), n = (int)(u % n_sub);
+                for (int kb = 0; kb < kblocks; ++kb) {
+                    if (!mbar_wait(smem_u32(&c.empty[stage]), phase ^ 1, c.abort_flag)) {
+                        ok = false;
+                        break;
+                    }
+                    const uint32_t fb = smem_u32(&c.full[stage]);
+                    const uint32_t a = smem_u32(sA + stage * kRowsBytes), b = smem_u32(sB + stage * kRowsBytes);
+                    const uint32_t fa = smem_u32(sSA + stage * P::SFA), fs = smem_u32(sSB + stage * P::SFB);
+                    // scale maps: rows of 256 bytes, a stage of one 128-row tile is 2 ST of them
+                    const int ma = m * (P::UM / 128) + (int)rank;
+                    const int ya = (ma * kblocks + kb) * 2 * ST;
+                    if (PAIR) {
+                        const uint32_t fb0 = mapa_shared(fb, 0);
+                        if (rank == 0) mbar_arrive_expect_tx(fb, 2 * P::STAGE);
+                        tma_load_2d_pair(a, &tmA, fb0, kb * 128, ma * 128);
+                        tma_load_2d_pair(b, &tmB, fb0, kb * 128, n * TN + (int)rank * 128);
+                        tma_load_2d_pair(fa, &tmSA, fb0, 0, ya);
+                        tma_load_2d_pair(fs, &tmSB, fb0, 0, ((n * 2) * kblocks + kb) * 2 * ST);
+                        tma_load_2d_pair(fs + P::SFA, &tmSB, fb0, 0, ((n * 2 + 1) * kblocks + kb) * 2 * ST);
+                    } else {
+                        mbar_arrive_expect_tx(fb, P::STAGE);
+                        tma_load_2d(a, &tmA, fb, kb * 128, m * 128);
+                        tma_load_2d(b, &tmB, fb, kb * 128, n * TN);
+                        tma_load_2d(fa, &tmSA, fb, 0, ya);
+                        tma_load_2d(fs, &tmSB, fb, 0, (n * kblocks + kb) * 2 * ST);
+                    }
+                    ++issued;
+                    if (++stage == NST) { stage = 0; phase ^= 1; }
+                }
             }
-            st[ty * 4 + i][tx * 4 + j] = v;
+            if (!ok && rank == 0) {
+                for (int i = 0; i < NST && i < issued; ++i) {
+                    if (--stage < 0) { stage = NST - 1; phase ^= 1; }
+                    mbar_wait_drain(smem_u32(&c.full[stage]), phase);
+                }
+            }
         }
-    if (!p.q) return;
-    __syncthreads();
-    constexpr int kB = Mx4<NV>::kBlock, kPer = TN / kB;
-    const int tiles = mx4_stages(p.N) * Mx4<NV>::kStageTiles, pitch = mx4_code_pitch(p.N);
-    for (int i = threadIdx.x; i < TM * kPer; i += 256) {
-        const int r = i / kPer, row = m0 + r, c0 = (i % kPer) * kB, blk = (n0 + c0) / kB;
-        if (row >= nr || (n0 + c0) / 2 >= pitch) continue;
-        uint32_t m = 0;
-        for (int j = 0; j < kB; ++j) m = umax(m, abs_bits(st[r][c0 + j]));
-        const Mx4Scale s = mx4_block_scale<NV>(m, p.q_ts, 6.0f * p.q_ts);
-        for (int j = 0; j < kB; j += 8) {
-            float y[8];
-            for (int e = 0; e < 8; ++e) y[e] = __fmul_rn(st[r][c0 + j + e], s.mul);
-            *reinterpret_cast<uint32_t *>(p.q + (size_t)row * pitch + (n0 + c0 + j) / 2) = s.zero ? 0u : cvt_e2m1x8(y);
+    } else if (warp == 1) {
+        // -------------------------------------------------------- MMA issuer --
+        if (lane == 0 && rank == 0) {
+            int stage = 0;
+            uint32_t phase = 0, t = 0;  // t: tiles issued by this CTA
+            long long it = 0;           // stages consumed
+            bool ok = true;
+            for (long long u = slot; u < units && ok; u += nslots, ++t) {
+                if (PAIR) {
+                    // the previous tile's columns of the overlap have been read
+                    if (t >= 1 && !mbar_wait(smem_u32(&c.tfree[(t - 1) & 1]), ((t - 1) >> 1) & 1, c.abort_flag)) break;
+                } else {
+                    if (t >= 2 && !mbar_wait(smem_u32(&c.tfree[t & 1]), ((t - 2) >> 1) & 1, c.abort_flag)) break;
+                }
+                tc_fence_after();
+                const uint32_t d = tmem + (t & 1) * P::ACC1;
+                for (int kb = 0; kb < kblocks; ++kb, ++it) {
+                    if (!mbar_wait(smem_u32(&c.full[stage]), phase, c.abort_flag)) { ok = false; break; }
+                    if (it >= 2) {
+                        // the products that read these scale columns two stages ago have completed
+                        const int es = (int)((it - 2) % NST);
+                        if (!mbar_wait(smem_u32(&c.empty[es]), (uint32_t)((it - 2) / NST) & 1, c.abort_flag)) { ok = false; break; }
+                    }
+                    tc_fence_after();
+                    const uint32_t a0 = smem_u32(sA + stage * kRowsBytes), b0 = smem_u32(sB + stage * kRowsBytes);
+                    const uint32_t fa = smem_u32(sSA + stage * P::SFA), fs = smem_u32(sSB + stage * P::SFB);
+                    const uint32_t ca = tmem + P::SFCOL + (uint32_t)(it & 1) * P::SFBUF, cb = ca + 4 * ST;
+#pragma unroll
+                    for (int g = 0; g < ST; ++g) {
+                        tmem_cp_scales<PAIR>(ca + 4 * g, scale_tile_desc(fa + g * kMx4TileBytes));
+#pragma unroll
+                        for (int h = 0; h < TN / 128; ++h)
+                            tmem_cp_scales<PAIR>(cb + (g * (TN / 128) + h) * 4,
+                                                 scale_tile_desc(fs + h * P::SFA + g * kMx4TileBytes));
+                    }
+                    const int left = p.K - kb * kMx4StageCols;  // products past the last column are left out
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (k * 64 >= left) break;
+                        const int g = NV ? k : k >> 1;
+                        umma_mx4<NV, PAIR>(d, sw128_kmajor_desc(a0 + k * 32), sw128_kmajor_desc(b0 + k * 32),
+                                           idesc_mx4<NV>(P::UM, TN, NV ? 0 : 2 * (k & 1)), ca + 4 * g,
+                                           cb + g * (TN / 128) * 4, (kb | k) != 0);
+                    }
+                    if (PAIR) umma_commit_pair(smem_u32(&c.empty[stage]), 3);
+                    else umma_commit(smem_u32(&c.empty[stage]));
+                    if (++stage == NST) { stage = 0; phase ^= 1; }
+                }
+                if (!ok) break;
+                if (PAIR) umma_commit_pair(smem_u32(&c.tfull[t & 1]), 3);
+                else umma_commit(smem_u32(&c.tfull[t & 1]));
+            }
+            if (PAIR) umma_commit_pair(smem_u32(c.drain), 1);
+            else umma_commit(smem_u32(c.drain));
+            mbar_wait_drain(smem_u32(c.drain), 0);
         }
-        p.q_scales[((size_t)(row >> 7) * tiles + (blk >> 2)) * kMx4TileBytes + (row & 31) * 16 + ((row >> 5) & 3) * 4 +
-                   (blk & 3)] = (uint8_t)s.byte;
+    } else {
+        // ---------------------------------------------------------- epilogue --
+        constexpr int PER = P::PER;
+        const int ew = warp - 2, quad = warp & 3, half = ew >> 2;
+        float *bias_s = sBias + ew * PER * 32;
+        float bnext[PER];
+        uint32_t t = 0;
+        // this warp's i-th chunk of a tile: the first accumulator of a pair is read from its
+        // upper end, the second from its lower end, so that the overlap comes first
+        auto chunk_of = [&](uint32_t tt, int i) { return (PAIR && (tt & 1) == 0) ? (TN / 32 - 2 + half) - 2 * i : half + 2 * i; };
+        auto bias_load = [&](long long u, uint32_t tt) {
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                const int col = (int)(u % n_sub) * TN + chunk_of(tt, i) * 32 + lane;
+                bnext[i] = (p.bias && col < p.N) ? __ldg(p.bias + col) : 0.f;
+            }
+        };
+        if (slot < units) bias_load(slot, 0);
+        bool ok = true;
+        for (long long u = slot; u < units && ok; u += nslots, ++t) {
+            const int m = (int)(u / n_sub), n = (int)(u % n_sub);
+            const int row = m * P::UM + (int)rank * 128 + quad * 32 + lane;
+            const bool row_ok = row < n_rows;
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < PER; ++i) bias_s[i * 32 + lane] = bnext[i];
+            __syncwarp();
+            if (u + nslots < units) bias_load(u + nslots, t + 1);
+            bool got = mbar_wait(smem_u32(&c.tfull[t & 1]), (t >> 1) & 1, c.abort_flag);
+            if (!__all_sync(0xffffffffu, got)) break;
+            tc_fence_after();
+            const uint32_t tb = tmem + ((uint32_t)(quad * 32) << 16) + (t & 1) * P::ACC1;
+            uint32_t r[2][32];
+            tmem_ld32(tb + chunk_of(t, 0) * 32, r[0]);
+            if (PER > 1) tmem_ld32(tb + chunk_of(t, 1) * 32, r[1]);
+#pragma unroll
+            for (int i = 0; i < PER; ++i) {
+                tmem_ld_wait();
+                if (i == (PAIR ? 0 : PER - 2)) {
+                    // pair: the overlap is in registers; else: the whole accumulator is
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (PAIR) mbar_arrive_cluster(mapa_shared(smem_u32(&c.tfree[t & 1]), 0));
+                        else mbar_arrive(smem_u32(&c.tfree[t & 1]));
+                    }
+                }
+                const int col0 = n * TN + chunk_of(t, i) * 32;
+                const int left = p.N - col0;  // columns of this chunk that exist
+                float v[32];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const float4 b = *reinterpret_cast<const float4 *>(bias_s + i * 32 + 4 * q);
+                    v[4 * q] = fmaf(p.alpha, __uint_as_float(r[i & 1][4 * q]), b.x);
+                    v[4 * q + 1] = fmaf(p.alpha, __uint_as_float(r[i & 1][4 * q + 1]), b.y);
+                    v[4 * q + 2] = fmaf(p.alpha, __uint_as_float(r[i & 1][4 * q + 2]), b.z);
+                    v[4 * q + 3] = fmaf(p.alpha, __uint_as_float(r[i & 1][4 * q + 3]), b.w);
+                }
+                if (i + 2 < PER) tmem_ld32(tb + chunk_of(t, i + 2) * 32, r[i & 1]);
+                if (p.gelu) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) v[j] = gelu_exact(v[j]);
+                }
+                if constexpr (QOUT) {
+                    constexpr int kB = Mx4<NV>::kBlock, kNB = 32 / kB;
+                    const int pitch = mx4_code_pitch(p.N), tiles = mx4_stages(p.N) * ST;
+                    uint32_t bytes = 0, q[4] = {};
+#pragma unroll
+                    for (int b = 0; b < kNB; ++b) {
+                        uint32_t mx = 0;
+#pragma unroll
+                        for (int j = 0; j < kB; ++j) {
+                            if (b * kB + j >= left) v[b * kB + j] = 0.f;
+                            mx = umax(mx, abs_bits(v[b * kB + j]));
+                        }
+                        const Mx4Scale s = mx4_block_scale<NV>(mx, p.q_ts, 6.0f * p.q_ts);
+                        bytes |= s.byte << (8 * b);
+#pragma unroll
+                        for (int j = 0; j < kB; j += 8) {
+                            float y[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) y[e] = __fmul_rn(v[b * kB + j + e], s.mul);
+                            q[(b * kB + j) / 8] = s.zero ? 0u : cvt_e2m1x8(y);
+                        }
+                    }
+                    if (row_ok) {
+                        if (col0 / 2 < pitch)
+                            *reinterpret_cast<uint4 *>(p.q + (size_t)row * pitch + col0 / 2) = make_uint4(q[0], q[1], q[2], q[3]);
+                        const int blk = col0 / kB;
+                        uint8_t *sp = p.q_scales + ((size_t)(row >> 7) * tiles + (blk >> 2)) * kMx4TileBytes + (row & 31) * 16 +
+                                      ((row >> 5) & 3) * 4 + (blk & 3);
+                        if (NV) *reinterpret_cast<uint16_t *>(sp) = (uint16_t)bytes;
+                        else *sp = (uint8_t)bytes;
+                    }
+                } else if (row_ok && left > 0) {
+                    const size_t ro = (size_t)row * p.ld_res + col0, oo = (size_t)row * p.ld_out + col0;
+                    const int cnt = left < 32 ? left : 32;
+                    if (p.out_type == kElemF32) {
+                        if (p.res) add_row(static_cast<const float *>(p.res) + ro, cnt, vec_res, v);
+                        store_row(static_cast<float *>(p.out) + oo, cnt, vec_out, v);
+                    } else if (p.out_type == kElemF16) {
+                        if (p.res) add_row(static_cast<const __half *>(p.res) + ro, cnt, vec_res, v);
+                        store_row(static_cast<__half *>(p.out) + oo, cnt, vec_out, v);
+                    } else {
+                        if (p.res) add_row(static_cast<const bf16 *>(p.res) + ro, cnt, vec_res, v);
+                        store_row(static_cast<bf16 *>(p.out) + oo, cnt, vec_out, v);
+                    }
+                }
+            }
+        }
     }
-    // the scale bytes between the last block and the end of the row's tiles are 0
-    const int last = (pitch * 2) / kB, all = tiles * 4;
-    if (blockIdx.x == gridDim.x - 1)
-        for (int i = threadIdx.x; i < TM * (all - last); i += 256) {
-            const int row = m0 + i / (all - last), blk = last + i % (all - last);
-            if (row < nr)
-                p.q_scales[((size_t)(row >> 7) * tiles + (blk >> 2)) * kMx4TileBytes + (row & 31) * 16 +
-                           ((row >> 5) & 3) * 4 + (blk & 3)] = 0;
-        }
+    tc_fence_before();
+    if (PAIR) cluster_sync();
+    else __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        if (PAIR) tmem_dealloc_pair(tmem, 512);
+        else tmem_dealloc(tmem, 512);
+    }
+    if (threadIdx.x == 0 && *c.abort_flag) set_status(p.status, kStatusTimeout);
+}
+
+template <bool NV, bool PAIR, bool QOUT>
+cudaError_t configure() {
+    static std::atomic<unsigned long long> done{0};
+    return ensure_smem_attr(reinterpret_cast<const void *>(mx4_gemm_kernel<NV, PAIR, QOUT>), Plan<NV, PAIR>::SMEM, done);
+}
+
+template <bool NV, bool PAIR, bool QOUT>
+cudaError_t launch_tile(const Mx4GemmArgs &a, int num_sms, cudaStream_t s, bool pdl) {
+    using P = Plan<NV, PAIR>;
+    CUtensorMap tmA, tmB, tmSA, tmSB;
+    const int pitch = mx4_code_pitch(a.K), stages = mx4_stages(a.K);
+    const uint64_t ta = (uint64_t)((a.M + 127) / 128) * stages * P::ST, tb = (uint64_t)((a.N + 127) / 128) * stages * P::ST;
+    if (make_tmap_u8(&tmA, a.a, a.M, pitch, 128, 128, true) || make_tmap_u8(&tmB, a.w, a.N, pitch, 128, 128, true) ||
+        make_tmap_u8(&tmSA, a.a_scales, 2 * ta, 256, 256, 2 * P::ST, false) ||
+        make_tmap_u8(&tmSB, a.w_scales, 2 * tb, 256, 256, 2 * P::ST, false))
+        return cudaErrorInvalidValue;
+    cudaError_t e = configure<NV, PAIR, QOUT>();
+    if (e != cudaSuccess) return e;
+    // a 4-bit result's scale tiles reach to a multiple of 256 columns
+    const int n_sub = ((QOUT ? mx4_stages(a.N) * kMx4StageCols : a.N) + P::TN - 1) / P::TN;
+    const long long units = (long long)((a.M + P::UM - 1) / P::UM) * n_sub;
+    const int slots = PAIR ? num_sms / 2 : num_sms;
+    const int grid = (PAIR ? 2 : 1) * (int)(units < slots ? units : slots);
+    const int es = a.out_type == kElemF32 ? 4 : 2;
+    auto ok16 = [&](const void *q, long long ld) { return (reinterpret_cast<uintptr_t>(q) & 15) == 0 && ld * es % 16 == 0; };
+    const int vec_out = ok16(a.out, a.ld_out), vec_res = ok16(a.res, a.ld_res);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    int na = 0;
+    if (PAIR) {
+        attr[na].id = cudaLaunchAttributeClusterDimension;
+        attr[na].val.clusterDim.x = 2;
+        attr[na].val.clusterDim.y = 1;
+        attr[na++].val.clusterDim.z = 1;
+    }
+    if (pdl) {
+        attr[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;  // see launch_pdl
+        attr[na++].val.programmaticStreamSerializationAllowed = 1;
+    }
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = P::SMEM;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = na;
+    return cudaLaunchKernelEx(&cfg, mx4_gemm_kernel<NV, PAIR, QOUT>, tmA, tmB, tmSA, tmSB, a, n_sub, vec_out, vec_res);
+}
+
+template <bool NV, bool QOUT>
+cudaError_t launch_fmt(const Mx4GemmArgs &a, int num_sms, cudaStream_t s, bool pdl) {
+    // pairs when their tiles fill the machine
+    const long long pair_units = (long long)((a.M + 255) / 256) * ((a.N + 255) / 256);
+    if (pair_units >= num_sms / 2) return launch_tile<NV, true, QOUT>(a, num_sms, s, pdl);
+    return launch_tile<NV, false, QOUT>(a, num_sms, s, pdl);
 }
 
 }  // namespace
 
 cudaError_t launch_mx4_gemm(const Mx4GemmArgs &a, int num_sms, cudaStream_t s, bool pdl) {
-    (void)num_sms;
     if (a.M < 1) return cudaSuccess;
-    const dim3 grid((a.N + TN - 1) / TN, (a.M + TM - 1) / TM);
-    if (pdl) return launch_pdl(a.nv ? mx4_gemm_kernel<true> : mx4_gemm_kernel<false>, grid, dim3(256), 0, s, a);
-    if (a.nv) mx4_gemm_kernel<true><<<grid, 256, 0, s>>>(a);
-    else mx4_gemm_kernel<false><<<grid, 256, 0, s>>>(a);
-    return cudaGetLastError();
+    if (a.q) return a.nv ? launch_fmt<true, true>(a, num_sms, s, pdl) : launch_fmt<false, true>(a, num_sms, s, pdl);
+    return a.nv ? launch_fmt<true, false>(a, num_sms, s, pdl) : launch_fmt<false, false>(a, num_sms, s, pdl);
 }
 
 }  // namespace albert
