@@ -129,6 +129,9 @@ int make_tmap_bf16(CUtensorMap *tm, const void *base, uint64_t rows, uint64_t co
 // Map of an E4M3 (byte) row-major [rows, cols] tensor with a {128, box_rows} box
 // and the 128-byte swizzle: the operands of the E4M3 GEMM variant.
 int make_tmap_e4m3(CUtensorMap *tm, const void *base, uint64_t rows, uint64_t cols, uint32_t box_rows);
+// Map of [rows, cols] elements of an ElemType, rows ld elements apart, with a 32x32
+// box: 16-bit types with the 64-byte swizzle, fp32 with the 128-byte swizzle.
+int make_tmap_tile32(CUtensorMap *tm, const void *base, int type, uint64_t rows, uint64_t cols, uint64_t ld);
 // Map of a byte row-major [rows, cols] tensor with a {box_cols, box_rows} box.
 int make_tmap_u8(CUtensorMap *tm, const void *base, uint64_t rows, uint64_t cols, uint32_t box_cols, uint32_t box_rows,
                  bool swizzle128);

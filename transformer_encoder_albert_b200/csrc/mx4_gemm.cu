@@ -8,10 +8,14 @@
 //   warp 0     : TMA producer: per stage 256 columns of A and W (128-byte rows,
 //                128-byte swizzle) and their scale tiles (512 bytes per 128 rows and
 //                four blocks, plain);
-//   warp 1     : issues, per stage, the copies of the scale tiles to tensor memory
-//                and four products of K = 64;
+//   warp 1     : issues four products of K = 64 per stage;
+//   warp 10    : issues the copies of a stage's scale tiles to tensor memory, one
+//                stage ahead of the products (6 or 12 copies per stage at about 26
+//                cycles each would cost the products' warp more than half their time);
 //   warps 2..9 : epilogue, a lane quadrant each, two warps per quadrant taking
-//                alternate 32-column chunks.
+//                alternate 32-column chunks; rows leave through a swizzled staging
+//                tile by TMA (or coalesced stores where the rows are not 16-byte
+//                aligned), 16-bit residual tiles arrive the same way a chunk ahead.
 // Two tile shapes:
 //   * a CTA pair per 256x256 tile (cta_group::2): each CTA stages 128 rows of A and of
 //     W and the scales of its A rows and of all W rows.  Two 256-column accumulators
@@ -33,7 +37,8 @@ namespace albert {
 namespace {
 
 constexpr int kEpiWarps = 8;
-constexpr int kThreads = 32 * (2 + kEpiWarps);
+constexpr int kThreads = 32 * (3 + kEpiWarps);
+constexpr int kStgBytes = 3 * 2048;    // staging per epilogue warp: three 16-bit 32x32 tiles
 constexpr int kRowsBytes = 128 * 128;  // 128 rows x 256 columns of codes
 
 template <bool NV, bool PAIR>
@@ -44,18 +49,19 @@ struct Plan {
     static constexpr int SFA = ST * kMx4TileBytes;
     static constexpr int SFB = (TN / 128) * SFA;
     static constexpr int STAGE = 2 * kRowsBytes + SFA + SFB;  // bytes per CTA and stage
-    static constexpr int NST = 5;
+    static constexpr int NST = NV ? 4 : 5;
     static constexpr int ACC1 = PAIR ? 160 : 128;            // first column of the second accumulator
     static constexpr int SFCOL = PAIR ? 416 : 256;           // first scale column
     static constexpr int SFBUF = 4 * ST * (1 + TN / 128);    // scale columns per stage
     static constexpr int PER = TN / 64;                      // 32-column chunks per epilogue warp
-    static constexpr int SMEM = 1024 + NST * STAGE + kEpiWarps * PER * 128 + 1024;
+    static constexpr int SMEM = 1024 + NST * STAGE + kEpiWarps * (kStgBytes + 256) + 512;
     static_assert(SFCOL + 2 * SFBUF <= 512, "tensor memory columns");
-    static_assert(SMEM <= 232448, "shared memory per CTA");
+    static_assert(SMEM + 64 <= 232448, "shared memory per CTA, the wait limit included");
+    static_assert((2 * NST + 8 + kEpiWarps) * 8 + 32 <= 512, "barriers");
 };
 
 struct Ctrl {
-    uint64_t *full, *empty, *tfull, *tfree, *drain;
+    uint64_t *full, *empty, *sfull, *tfull, *tfree, *drain, *sdrain, *rbar;
     uint32_t *tmem_slot;
     volatile int *abort_flag;
     int *misc;
@@ -80,37 +86,55 @@ __device__ __forceinline__ void add_row(const T *p, int n, bool vec, float (&v)[
         for (int i = 0; i < 8; ++i) v[8 * q + i] += r[i];
     }
 }
-template <typename T>
-__device__ __forceinline__ void store_row(T *p, int n, bool vec, const float (&v)[32]) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        float r[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) r[i] = v[8 * q + i];
-        const int left = n - 8 * q;
-        store8<T>(p + 8 * q, left > 0 ? left : 0, vec, r);
-    }
+
+// Byte offset of 16-byte chunk q of row r in a 32x32 16-bit tile stored with the TMA
+// 64-byte swizzle.
+__device__ __forceinline__ uint32_t stg_off(int r, int q) {
+    return (uint32_t)(r * 64 + ((q ^ ((r >> 1) & 3)) << 4));
+}
+__device__ __forceinline__ void st_shared_u4(uint32_t a, uint4 v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared_u4(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t ld_shared_u1(uint32_t a) {
+    uint32_t v;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint16_t ld_shared_u16(uint32_t a) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
+    return v;
 }
 
 template <bool NV, bool PAIR, bool QOUT>
 __global__ void __launch_bounds__(kThreads, 1)
 mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-                const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB, const Mx4GemmArgs p,
-                int n_sub, int vec_out, int vec_res) {
+                const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
+                const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ CUtensorMap tmRes, const Mx4GemmArgs p,
+                int n_sub, int tma_out, int tma_res, int vec_res) {
     using P = Plan<NV, PAIR>;
     constexpr int NST = P::NST, TN = P::TN, ST = P::ST;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *sA = base, *sB = sA + NST * kRowsBytes, *sSA = sB + NST * kRowsBytes, *sSB = sSA + NST * P::SFA;
-    float *sBias = reinterpret_cast<float *>(sSB + NST * P::SFB);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(reinterpret_cast<uint8_t *>(sBias) + kEpiWarps * P::PER * 128);
+    uint8_t *sStg = sSB + NST * P::SFB;  // (a multiple of 1024 from base: the stages and scale tiles are)
+    float *sBias = reinterpret_cast<float *>(sStg + kEpiWarps * kStgBytes);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(reinterpret_cast<uint8_t *>(sBias) + kEpiWarps * 256);
     Ctrl c;
     c.full = bars;
     c.empty = bars + NST;
-    c.tfull = bars + 2 * NST;
-    c.tfree = bars + 2 * NST + 2;
-    c.drain = bars + 2 * NST + 4;
-    uint32_t *u32 = reinterpret_cast<uint32_t *>(bars + 2 * NST + 5);
+    c.sfull = bars + 2 * NST;
+    c.tfull = bars + 2 * NST + 2;
+    c.tfree = bars + 2 * NST + 4;
+    c.drain = bars + 2 * NST + 6;
+    c.sdrain = bars + 2 * NST + 7;
+    c.rbar = bars + 2 * NST + 8;
+    uint32_t *u32 = reinterpret_cast<uint32_t *>(bars + 2 * NST + 8 + kEpiWarps);
     c.tmem_slot = u32;
     c.abort_flag = reinterpret_cast<volatile int *>(u32 + 1);
     c.misc = reinterpret_cast<int *>(u32 + 2);
@@ -129,10 +153,13 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             mbar_init(smem_u32(&c.empty[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_u32(&c.sfull[i]), 1);
             mbar_init(smem_u32(&c.tfull[i]), 1);
             mbar_init(smem_u32(&c.tfree[i]), (PAIR ? 2 : 1) * kEpiWarps);
         }
         mbar_init(smem_u32(c.drain), 1);
+        mbar_init(smem_u32(c.sdrain), 1);
+        for (int i = 0; i < kEpiWarps; ++i) mbar_init(smem_u32(&c.rbar[i]), 1);
         fence_mbar_init();
     }
     if (warp == 0 && lane == 0) {
@@ -215,67 +242,93 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         }
     } else if (warp == 1) {
         // -------------------------------------------------------- MMA issuer --
-        if (lane == 0 && rank == 0) {
-            int stage = 0;
-            uint32_t phase = 0, t = 0;  // t: tiles issued by this CTA
-            long long it = 0;           // stages consumed
+        // (the whole warp walks the loop in step, one elected lane issues)
+        if (rank == 0) {
+            const uint32_t leader = elect_leader();
+            auto wait = [&](uint64_t *bar, uint32_t parity) {
+                return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, c.abort_flag)) != 0;
+            };
+            uint32_t stage = 0, phase = 0, t = 0;  // t: tiles issued by this CTA
+            uint32_t it = 0;                       // stages consumed
             bool ok = true;
             for (long long u = slot; u < units && ok; u += nslots, ++t) {
                 if (PAIR) {
                     // the previous tile's columns of the overlap have been read
-                    if (t >= 1 && !mbar_wait(smem_u32(&c.tfree[(t - 1) & 1]), ((t - 1) >> 1) & 1, c.abort_flag)) break;
+                    if (t >= 1 && !wait(&c.tfree[(t - 1) & 1], ((t - 1) >> 1) & 1)) break;
                 } else {
-                    if (t >= 2 && !mbar_wait(smem_u32(&c.tfree[t & 1]), ((t - 2) >> 1) & 1, c.abort_flag)) break;
+                    if (t >= 2 && !wait(&c.tfree[t & 1], ((t - 2) >> 1) & 1)) break;
                 }
-                tc_fence_after();
                 const uint32_t d = tmem + (t & 1) * P::ACC1;
                 for (int kb = 0; kb < kblocks; ++kb, ++it) {
-                    if (!mbar_wait(smem_u32(&c.full[stage]), phase, c.abort_flag)) { ok = false; break; }
-                    if (it >= 2) {
-                        // the products that read these scale columns two stages ago have completed
-                        const int es = (int)((it - 2) % NST);
-                        if (!mbar_wait(smem_u32(&c.empty[es]), (uint32_t)((it - 2) / NST) & 1, c.abort_flag)) { ok = false; break; }
-                    }
+                    // operands in shared memory, scales in tensor memory
+                    if (!wait(&c.full[stage], phase) || !wait(&c.sfull[it & 1], (it >> 1) & 1)) { ok = false; break; }
                     tc_fence_after();
-                    const uint32_t a0 = smem_u32(sA + stage * kRowsBytes), b0 = smem_u32(sB + stage * kRowsBytes);
-                    const uint32_t fa = smem_u32(sSA + stage * P::SFA), fs = smem_u32(sSB + stage * P::SFB);
-                    const uint32_t ca = tmem + P::SFCOL + (uint32_t)(it & 1) * P::SFBUF, cb = ca + 4 * ST;
-#pragma unroll
-                    for (int g = 0; g < ST; ++g) {
-                        tmem_cp_scales<PAIR>(ca + 4 * g, scale_tile_desc(fa + g * kMx4TileBytes));
-#pragma unroll
-                        for (int h = 0; h < TN / 128; ++h)
-                            tmem_cp_scales<PAIR>(cb + (g * (TN / 128) + h) * 4,
-                                                 scale_tile_desc(fs + h * P::SFA + g * kMx4TileBytes));
-                    }
+                    const uint32_t a0 = smem_u32(sA) + stage * kRowsBytes, b0 = smem_u32(sB) + stage * kRowsBytes;
+                    const uint32_t ca = tmem + P::SFCOL + (it & 1) * P::SFBUF, cb = ca + 4 * ST;
                     const int left = p.K - kb * kMx4StageCols;  // products past the last column are left out
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        if (k * 64 >= left) break;
                         const int g = NV ? k : k >> 1;
-                        umma_mx4<NV, PAIR>(d, sw128_kmajor_desc(a0 + k * 32), sw128_kmajor_desc(b0 + k * 32),
-                                           idesc_mx4<NV>(P::UM, TN, NV ? 0 : 2 * (k & 1)), ca + 4 * g,
-                                           cb + g * (TN / 128) * 4, (kb | k) != 0);
+                        umma_mx4<NV, PAIR>(k * 64 < left ? leader : 0u, d, sw128_kmajor_desc(a0 + k * 32),
+                                           sw128_kmajor_desc(b0 + k * 32), idesc_mx4<NV>(P::UM, TN, NV ? 0 : 2 * (k & 1)),
+                                           ca + 4 * g, cb + g * (TN / 128) * 4, (kb | k) != 0);
                     }
-                    if (PAIR) umma_commit_pair(smem_u32(&c.empty[stage]), 3);
-                    else umma_commit(smem_u32(&c.empty[stage]));
+                    umma_commit_elected<PAIR>(leader, smem_u32(c.empty) + 8 * stage, 3);
                     if (++stage == NST) { stage = 0; phase ^= 1; }
                 }
                 if (!ok) break;
-                if (PAIR) umma_commit_pair(smem_u32(&c.tfull[t & 1]), 3);
-                else umma_commit(smem_u32(&c.tfull[t & 1]));
+                umma_commit_elected<PAIR>(leader, smem_u32(&c.tfull[t & 1]), 3);
             }
-            if (PAIR) umma_commit_pair(smem_u32(c.drain), 1);
-            else umma_commit(smem_u32(c.drain));
+            umma_commit_elected<PAIR>(leader, smem_u32(c.drain), 1);
             mbar_wait_drain(smem_u32(c.drain), 0);
+        }
+    } else if (warp == 2 + kEpiWarps) {
+        // ------------------------------------------------------- scale copies --
+        if (rank == 0) {
+            const uint32_t leader = elect_leader();
+            auto wait = [&](uint64_t *bar, uint32_t parity) {
+                return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, c.abort_flag)) != 0;
+            };
+            uint32_t stage = 0, phase = 0, it = 0;
+            uint32_t es = 0, eph = 0;  // stage and phase of the stage before last
+            bool ok = true;
+            for (long long u = slot; u < units && ok; u += nslots) {
+                for (int kb = 0; kb < kblocks; ++kb, ++it) {
+                    if (!wait(&c.full[stage], phase)) { ok = false; break; }
+                    if (it >= 2) {
+                        // the products that read these columns two stages ago have completed
+                        if (!wait(&c.empty[es], eph)) { ok = false; break; }
+                        if (++es == NST) { es = 0; eph ^= 1; }
+                    }
+                    tc_fence_after();
+                    const uint32_t fa = smem_u32(sSA) + stage * P::SFA, fs = smem_u32(sSB) + stage * P::SFB;
+                    const uint32_t ca = tmem + P::SFCOL + (it & 1) * P::SFBUF, cb = ca + 4 * ST;
+#pragma unroll
+                    for (int g = 0; g < ST; ++g) {
+                        tmem_cp_scales<PAIR>(leader, ca + 4 * g, scale_tile_desc(fa + g * kMx4TileBytes));
+#pragma unroll
+                        for (int h = 0; h < TN / 128; ++h)
+                            tmem_cp_scales<PAIR>(leader, cb + (g * (TN / 128) + h) * 4,
+                                                 scale_tile_desc(fs + h * P::SFA + g * kMx4TileBytes));
+                    }
+                    umma_commit_elected<PAIR>(leader, smem_u32(&c.sfull[it & 1]), 1);
+                    if (++stage == NST) { stage = 0; phase ^= 1; }
+                }
+            }
+            umma_commit_elected<PAIR>(leader, smem_u32(c.sdrain), 1);
+            mbar_wait_drain(smem_u32(c.sdrain), 0);
         }
     } else {
         // ---------------------------------------------------------- epilogue --
         constexpr int PER = P::PER;
         const int ew = warp - 2, quad = warp & 3, half = ew >> 2;
-        float *bias_s = sBias + ew * PER * 32;
+        float *bias_s = sBias + ew * 64;  // two chunks' biases
+        const uint32_t stg = smem_u32(sStg + ew * kStgBytes);
+        const uint32_t rstg = stg + 4096, rbar = smem_u32(&c.rbar[ew]);
+        const bool res = !QOUT && p.res != nullptr;
         float bnext[PER];
-        uint32_t t = 0;
+        uint32_t t = 0, rph = 0, stores = 0;
+        bool res_pending = false;
         // this warp's i-th chunk of a tile: the first accumulator of a pair is read from its
         // upper end, the second from its lower end, so that the overlap comes first
         auto chunk_of = [&](uint32_t tt, int i) { return (PAIR && (tt & 1) == 0) ? (TN / 32 - 2 + half) - 2 * i : half + 2 * i; };
@@ -286,16 +339,26 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 bnext[i] = (p.bias && col < p.N) ? __ldg(p.bias + col) : 0.f;
             }
         };
-        if (slot < units) bias_load(slot, 0);
+        auto res_issue = [&](long long u, uint32_t tt, int i) {
+            if (lane == 0) {
+                mbar_arrive_expect_tx(rbar, 2048);
+                tma_load_2d(rstg, &tmRes, rbar, (int)(u % n_sub) * TN + chunk_of(tt, i) * 32,
+                            (int)(u / n_sub) * P::UM + (int)rank * 128 + quad * 32);
+            }
+            res_pending = true;
+        };
+        if (slot < units) {
+            bias_load(slot, 0);
+            if (res && tma_res) res_issue(slot, 0, 0);
+        }
         bool ok = true;
         for (long long u = slot; u < units && ok; u += nslots, ++t) {
             const int m = (int)(u / n_sub), n = (int)(u % n_sub);
-            const int row = m * P::UM + (int)rank * 128 + quad * 32 + lane;
+            const int row0 = m * P::UM + (int)rank * 128 + quad * 32, row = row0 + lane;
             const bool row_ok = row < n_rows;
-            __syncwarp();
+            float bcur[PER];
 #pragma unroll
-            for (int i = 0; i < PER; ++i) bias_s[i * 32 + lane] = bnext[i];
-            __syncwarp();
+            for (int i = 0; i < PER; ++i) bcur[i] = bnext[i];
             if (u + nslots < units) bias_load(u + nslots, t + 1);
             bool got = mbar_wait(smem_u32(&c.tfull[t & 1]), (t >> 1) & 1, c.abort_flag);
             if (!__all_sync(0xffffffffu, got)) break;
@@ -303,9 +366,11 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             const uint32_t tb = tmem + ((uint32_t)(quad * 32) << 16) + (t & 1) * P::ACC1;
             uint32_t r[2][32];
             tmem_ld32(tb + chunk_of(t, 0) * 32, r[0]);
-            if (PER > 1) tmem_ld32(tb + chunk_of(t, 1) * 32, r[1]);
+            tmem_ld32(tb + chunk_of(t, 1) * 32, r[1]);
 #pragma unroll
             for (int i = 0; i < PER; ++i) {
+                // (the slot's readers, two chunks ago, have passed a __syncwarp since)
+                bias_s[(i & 1) * 32 + lane] = bcur[i];
                 tmem_ld_wait();
                 if (i == (PAIR ? 0 : PER - 2)) {
                     // pair: the overlap is in registers; else: the whole accumulator is
@@ -316,12 +381,13 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                         else mbar_arrive(smem_u32(&c.tfree[t & 1]));
                     }
                 }
+                __syncwarp();
                 const int col0 = n * TN + chunk_of(t, i) * 32;
                 const int left = p.N - col0;  // columns of this chunk that exist
                 float v[32];
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
-                    const float4 b = *reinterpret_cast<const float4 *>(bias_s + i * 32 + 4 * q);
+                    const float4 b = *reinterpret_cast<const float4 *>(bias_s + (i & 1) * 32 + 4 * q);
                     v[4 * q] = fmaf(p.alpha, __uint_as_float(r[i & 1][4 * q]), b.x);
                     v[4 * q + 1] = fmaf(p.alpha, __uint_as_float(r[i & 1][4 * q + 1]), b.y);
                     v[4 * q + 2] = fmaf(p.alpha, __uint_as_float(r[i & 1][4 * q + 2]), b.z);
@@ -363,22 +429,95 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                         if (NV) *reinterpret_cast<uint16_t *>(sp) = (uint16_t)bytes;
                         else *sp = (uint8_t)bytes;
                     }
-                } else if (row_ok && left > 0) {
-                    const size_t ro = (size_t)row * p.ld_res + col0, oo = (size_t)row * p.ld_out + col0;
-                    const int cnt = left < 32 ? left : 32;
-                    if (p.out_type == kElemF32) {
-                        if (p.res) add_row(static_cast<const float *>(p.res) + ro, cnt, vec_res, v);
-                        store_row(static_cast<float *>(p.out) + oo, cnt, vec_out, v);
+                } else {
+                    if (res) {
+                        if (tma_res) {
+                            bool rok = mbar_wait(rbar, rph, c.abort_flag);
+                            if (!__all_sync(0xffffffffu, rok)) { ok = false; tmem_ld_wait(); break; }
+                            rph ^= 1;
+                            res_pending = false;
+                            const bool f16 = p.out_type == kElemF16;
+#pragma unroll
+                            for (int q = 0; q < 4; ++q) {
+                                const uint4 w = ld_shared_u4(rstg + stg_off(lane, q));
+                                const uint32_t w4[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                                for (int e = 0; e < 4; ++e) {
+                                    const float2 f = f16 ? unpack_x2<__half>(w4[e]) : unpack_x2<bf16>(w4[e]);
+                                    v[8 * q + 2 * e] += f.x;
+                                    v[8 * q + 2 * e + 1] += f.y;
+                                }
+                            }
+                            __syncwarp();
+                            if (i + 1 < PER) res_issue(u, t, i + 1);
+                            else if (u + nslots < units) res_issue(u + nslots, t + 1, 0);
+                        } else if (row_ok && left > 0) {
+                            const size_t ro = (size_t)row * p.ld_res + col0;
+                            const int cnt = left < 32 ? left : 32;
+                            if (p.out_type == kElemF32) add_row(static_cast<const float *>(p.res) + ro, cnt, vec_res, v);
+                            else if (p.out_type == kElemF16) add_row(static_cast<const __half *>(p.res) + ro, cnt, vec_res, v);
+                            else add_row(static_cast<const bf16 *>(p.res) + ro, cnt, vec_res, v);
+                        }
+                    }
+                    // the chunk as a 32x32 tile in shared memory: 16-bit rows of 64 bytes (two tiles
+                    // in turn, 64-byte swizzle), fp32 rows of 128 bytes (one tile, 128-byte swizzle)
+                    const bool f32 = p.out_type == kElemF32;
+                    const uint32_t tile = f32 ? stg : stg + (stores & 1) * 2048;
+                    if (lane == 0) {
+                        if (f32) bulk_wait_read0();
+                        else bulk_wait_read1();
+                    }
+                    __syncwarp();
+                    if (f32) {
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            st_shared_u4(tile + lane * 128 + ((q ^ (lane & 7)) << 4),
+                                         make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
+                                                    __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3])));
                     } else if (p.out_type == kElemF16) {
-                        if (p.res) add_row(static_cast<const __half *>(p.res) + ro, cnt, vec_res, v);
-                        store_row(static_cast<__half *>(p.out) + oo, cnt, vec_out, v);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            st_shared_u4(tile + stg_off(lane, q),
+                                         make_uint4(pack_x2<__half>(v[8 * q], v[8 * q + 1]), pack_x2<__half>(v[8 * q + 2], v[8 * q + 3]),
+                                                    pack_x2<__half>(v[8 * q + 4], v[8 * q + 5]), pack_x2<__half>(v[8 * q + 6], v[8 * q + 7])));
                     } else {
-                        if (p.res) add_row(static_cast<const bf16 *>(p.res) + ro, cnt, vec_res, v);
-                        store_row(static_cast<bf16 *>(p.out) + oo, cnt, vec_out, v);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            st_shared_u4(tile + stg_off(lane, q),
+                                         make_uint4(pack_x2<bf16>(v[8 * q], v[8 * q + 1]), pack_x2<bf16>(v[8 * q + 2], v[8 * q + 3]),
+                                                    pack_x2<bf16>(v[8 * q + 4], v[8 * q + 5]), pack_x2<bf16>(v[8 * q + 6], v[8 * q + 7])));
+                    }
+                    // by TMA unless rows past the last one would be written
+                    if (tma_out && (row0 + 32 <= n_rows || n_rows == p.M)) {
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane == 0 && left > 0 && row0 < n_rows) {
+                            tma_store_2d(&tmOut, tile, col0, row0);
+                        }
+                        if (lane == 0) bulk_commit();
+                        ++stores;
+                    } else {
+                        __syncwarp();
+                        if (lane < left) {
+                            const int rows = n_rows - row0 < 32 ? n_rows - row0 : 32;
+                            const uint32_t sh = (lane & 7) * 2;
+                            for (int y = 0; y < rows; ++y) {
+                                const size_t o = (size_t)(row0 + y) * p.ld_out + col0 + lane;
+                                if (f32)
+                                    static_cast<uint32_t *>(p.out)[o] = ld_shared_u1(tile + y * 128 + (((lane >> 2) ^ (y & 7)) << 4) + (lane & 3) * 4);
+                                else
+                                    static_cast<uint16_t *>(p.out)[o] = ld_shared_u16(tile + stg_off(y, lane >> 3) + sh);
+                            }
+                        }
+                        __syncwarp();
                     }
                 }
             }
         }
+        // outstanding copies finish before the CTA's shared memory goes away
+        if (lane == 0) bulk_wait0();
+        if (res_pending && lane == 0) mbar_wait_drain(rbar, rph);
+        __syncwarp();
     }
     tc_fence_before();
     if (PAIR) cluster_sync();
@@ -415,8 +554,12 @@ cudaError_t launch_tile(const Mx4GemmArgs &a, int num_sms, cudaStream_t s, bool 
     const int slots = PAIR ? num_sms / 2 : num_sms;
     const int grid = (PAIR ? 2 : 1) * (int)(units < slots ? units : slots);
     const int es = a.out_type == kElemF32 ? 4 : 2;
-    auto ok16 = [&](const void *q, long long ld) { return (reinterpret_cast<uintptr_t>(q) & 15) == 0 && ld * es % 16 == 0; };
-    const int vec_out = ok16(a.out, a.ld_out), vec_res = ok16(a.res, a.ld_res);
+    auto ok16 = [&](const void *q, long long ld) { return q && (reinterpret_cast<uintptr_t>(q) & 15) == 0 && ld * es % 16 == 0; };
+    CUtensorMap tmOut = tmA, tmRes = tmA;
+    const int vec_res = ok16(a.res, a.ld_res), tma_res = vec_res && a.out_type != kElemF32, tma_out = ok16(a.out, a.ld_out);
+    if ((tma_out && make_tmap_tile32(&tmOut, a.out, a.out_type, a.M, a.N, a.ld_out)) ||
+        (tma_res && make_tmap_tile32(&tmRes, a.res, a.out_type, a.M, a.N, a.ld_res)))
+        return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     int na = 0;
@@ -436,7 +579,8 @@ cudaError_t launch_tile(const Mx4GemmArgs &a, int num_sms, cudaStream_t s, bool 
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = na;
-    return cudaLaunchKernelEx(&cfg, mx4_gemm_kernel<NV, PAIR, QOUT>, tmA, tmB, tmSA, tmSB, a, n_sub, vec_out, vec_res);
+    return cudaLaunchKernelEx(&cfg, mx4_gemm_kernel<NV, PAIR, QOUT>, tmA, tmB, tmSA, tmSB, tmOut, tmRes, a, n_sub, tma_out,
+                              tma_res, vec_res);
 }
 
 template <bool NV, bool QOUT>
