@@ -127,28 +127,55 @@ __device__ __forceinline__ float2 unpack_x2(uint32_t u) {
     else return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u));
 }
 
-// Eight consecutive values of a row from p; only the first `n` (0..8) exist, the
-// rest read as 0.  vec: p is 16-byte aligned whenever all eight exist.
+// Eight consecutive values of a row as they are stored: 16 bytes, or 32 for fp32.
 template <typename T>
-__device__ __forceinline__ void load8(const T *p, int n, bool vec, float (&v)[8]) {
+struct Raw8 {
+    uint32_t w[sizeof(T) * 2];
+};
+// From p; only the first `n` (0..8, or more) exist, the rest are 0.  vec: p is
+// 16-byte aligned whenever all eight exist.
+template <typename T>
+__device__ __forceinline__ Raw8<T> load_raw8(const T *p, int n, bool vec) {
+    Raw8<T> r;
     if (vec && n >= 8) {
+        const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p));
+        r.w[0] = a.x; r.w[1] = a.y; r.w[2] = a.z; r.w[3] = a.w;
         if constexpr (sizeof(T) == 4) {
-            const float4 a = __ldg(reinterpret_cast<const float4 *>(p)), b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
-            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w; v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-        } else {
-            const uint4 a = __ldg(reinterpret_cast<const uint4 *>(p));
-            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 f = unpack_x2<T>(w[i]);
-                v[2 * i] = f.x;
-                v[2 * i + 1] = f.y;
-            }
+            const uint4 b = __ldg(reinterpret_cast<const uint4 *>(p) + 1);
+            r.w[4] = b.x; r.w[5] = b.y; r.w[6] = b.z; r.w[7] = b.w;
         }
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r.w[i] = i < n ? __ldg(reinterpret_cast<const uint32_t *>(p) + i) : 0u;
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = i < n ? to_f32<T>(p[i]) : 0.0f;
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t lo = 2 * i < n ? __ldg(reinterpret_cast<const unsigned short *>(p) + 2 * i) : 0u;
+            const uint32_t hi = 2 * i + 1 < n ? __ldg(reinterpret_cast<const unsigned short *>(p) + 2 * i + 1) : 0u;
+            r.w[i] = lo | (hi << 16);
+        }
     }
+    return r;
+}
+template <typename T>
+__device__ __forceinline__ void raw8_values(const Raw8<T> &r, float (&v)[8]) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r.w[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float2 f;
+            if constexpr (std::is_same<T, __half>::value) f = unpack_x2<T>(r.w[i]);
+            else f = make_float2(__uint_as_float(r.w[i] << 16), __uint_as_float(r.w[i] & 0xffff0000u));
+            v[2 * i] = f.x;
+            v[2 * i + 1] = f.y;
+        }
+    }
+}
+template <typename T>
+__device__ __forceinline__ void load8(const T *p, int n, bool vec, float (&v)[8]) {
+    raw8_values<T>(load_raw8<T>(p, n, vec), v);
 }
 template <typename T>
 __device__ __forceinline__ void store8(T *p, int n, bool vec, const float (&v)[8]) {
@@ -170,15 +197,36 @@ __device__ __forceinline__ void store8(T *p, int n, bool vec, const float (&v)[8
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 __device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
 
-// A warp quantizes 256 consecutive columns of a row, eight per lane: the block's
-// lanes (four, or two) share its largest value by shuffles.  Returns the lane's
-// codes; `word` becomes the four scale bytes of the lane's tile (every lane of
-// the tile holds it).
-template <bool NV>
-__device__ __forceinline__ uint32_t mx4_warp_quant(const float (&v)[8], float ts, float six_ts, int lane, uint32_t &word) {
-    uint32_t m = abs_bits(v[0]);
+// The largest magnitude of eight values, as bits that order like it (16-bit types:
+// their own bits, two at a time), and those bits as fp32 bits.
+template <typename T>
+__device__ __forceinline__ uint32_t raw8_amax(const Raw8<T> &r) {
+    if constexpr (sizeof(T) == 4) {
+        uint32_t m = r.w[0] & 0x7fffffffu;
 #pragma unroll
-    for (int i = 1; i < 8; ++i) m = umax(m, abs_bits(v[i]));
+        for (int i = 1; i < 8; ++i) m = umax(m, r.w[i] & 0x7fffffffu);
+        return m;
+    } else {
+        uint32_t m = r.w[0] & 0x7fff7fffu;
+#pragma unroll
+        for (int i = 1; i < 4; ++i) m = __vmaxu2(m, r.w[i] & 0x7fff7fffu);
+        return umax(m & 0xffffu, m >> 16);
+    }
+}
+template <typename T>
+__device__ __forceinline__ uint32_t amax_f32_bits(uint32_t m) {
+    if constexpr (sizeof(T) == 4) return m;
+    else if constexpr (std::is_same<T, __half>::value) return __float_as_uint(__half2float(__ushort_as_half((unsigned short)m)));
+    else return m << 16;
+}
+
+// A warp quantizes 256 consecutive columns of a row, eight per lane: the block's
+// lanes (four, or two) share its largest magnitude `m` (of the lane's own eight
+// values, fp32 bits) by shuffles.  Returns the lane's codes; `word` becomes the four
+// scale bytes of the lane's tile (every lane of the tile holds it).
+template <bool NV>
+__device__ __forceinline__ uint32_t mx4_warp_quant(const float (&v)[8], uint32_t m, float ts, float six_ts, int lane,
+                                                   uint32_t &word) {
     m = umax(m, __shfl_xor_sync(0xffffffffu, m, 1));
     if constexpr (!NV) m = umax(m, __shfl_xor_sync(0xffffffffu, m, 2));
     const Mx4Scale s = mx4_block_scale<NV>(m, ts, six_ts);
@@ -193,6 +241,18 @@ __device__ __forceinline__ uint32_t mx4_warp_quant(const float (&v)[8], float ts
     w |= __shfl_xor_sync(0xffffffffu, w, 2 * kLanes);
     word = w;
     return q;
+}
+
+// Eight E2M1 codes -> their values.
+__device__ __forceinline__ void e2m1x8_values(uint32_t q, float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t h;
+        asm("{\n\t.reg .b8 b;\n\tcvt.u8.u32 b, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b;\n\t}" : "=r"(h) : "r"(q >> (8 * i)));
+        const float2 f = unpack_x2<__half>(h);
+        v[2 * i] = f.x;
+        v[2 * i + 1] = f.y;
+    }
 }
 
 }  // namespace albert

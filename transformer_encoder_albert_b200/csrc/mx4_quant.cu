@@ -1,11 +1,14 @@
 // mx4_quant.cu -- rows to microscaled 4-bit values and back, and LayerNorm with
 // a 4-bit result.
 //
-// Quantizing reads every value once and writes 1/2 byte plus the block's scale
-// for it: bound by memory.  A warp takes 256 columns (eight per lane, one 16-byte
-// load of 16-bit values) of the four rows r, r+32, r+64, r+96 of a 128-row scale
-// tile: four loads in flight per lane, and the four rows' scale words of a tile
-// are 16 adjacent bytes.
+// Quantizing reads every value once and writes 1/2 byte plus the block's scale for
+// it, so memory is its floor; what it came down to was instructions (106 per lane and
+// eight values at first, 65% of the issue slots).  Here a lane takes 16 consecutive
+// values (one 32-byte load of 16-bit values), which halves the work per block scale
+// and leaves one shuffle (mxfp4) or none (nvfp4) for it; 16-bit magnitudes are
+// compared two at a time; whole chunks take a path without bounds.  A half-warp
+// covers 256 columns of a row, a warp the rows r and r + 32 of a 128-row scale tile,
+// and the next such pair's loads are in flight while one is converted.
 #include <type_traits>
 
 #include "kernels.h"
@@ -22,109 +25,306 @@ __device__ __forceinline__ size_t scale_word_offset(int row, int tile, int row_t
     return ((size_t)(row >> 7) * row_tiles + tile) * kMx4TileBytes + (row & 31) * 16 + ((row >> 5) & 3) * 4;
 }
 
+// A warp's walk over (row pair, chunk) items with a grid stride, chunks innermost:
+// one division at the start, none per item.  Pair g is the rows 128 (g / 64) +
+// 64 (g / 32 % 2) + g % 32 and the row 32 below.
+struct Walk {
+    int chunk, chunks, dc;
+    long long pair, dp;
+    __device__ Walk(int chunks_, long long first, long long stride) : chunks(chunks_) {
+        pair = first / chunks_;
+        chunk = (int)(first - pair * chunks_);
+        dp = stride / chunks_;
+        dc = (int)(stride - dp * chunks_);
+    }
+    __device__ void next() {
+        chunk += dc;
+        pair += dp;
+        if (chunk >= chunks) {
+            chunk -= chunks;
+            ++pair;
+        }
+    }
+    __device__ int row0() const { return (int)(pair >> 6) * 128 + (int)((pair >> 5) & 1) * 64 + (int)(pair & 31); }
+};
+
+__device__ __forceinline__ void ld_global_v8(const void *p, uint32_t *w) {
+    asm("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7]) : "l"(p));
+}
+__device__ __forceinline__ void st_global_v8(void *p, const uint32_t *w) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7]) : "memory");
+}
+
+// Sixteen consecutive values as stored: 8 words, or 16 for fp32.  vec: 2 = p is 32-byte
+// aligned, 1 = 16-byte, 0 = neither.
+template <typename T>
+struct Raw16 {
+    Raw8<T> h[2];
+};
+template <typename T>
+__device__ __forceinline__ Raw16<T> load_raw16(const T *p, int n, int vec) {
+    Raw16<T> r;
+    if (vec == 2 && n >= 16) {
+        if constexpr (sizeof(T) == 4) {
+            ld_global_v8(p, r.h[0].w);
+            ld_global_v8(p + 8, r.h[1].w);
+        } else {
+            uint32_t w[8];
+            ld_global_v8(p, w);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                r.h[0].w[i] = w[i];
+                r.h[1].w[i] = w[4 + i];
+            }
+        }
+    } else {
+        r.h[0] = load_raw8<T>(p, n, vec != 0);
+        r.h[1] = load_raw8<T>(p + 8, n - 8, vec != 0);
+    }
+    return r;
+}
+
 template <typename T, bool NV>
 __global__ void __launch_bounds__(32 * kQWarps)
 mx4_quant_kernel(const T *__restrict__ x, long long ld, int rows, int cols, const int *n_rows, float ts, float six_ts,
-                 uint8_t *__restrict__ codes, uint8_t *__restrict__ scales, int vec, long long items, const int *status,
+                 uint8_t *__restrict__ codes, uint8_t *__restrict__ scales, int vec, long long pairs, const int *status,
                  int trigger) {
     if (trigger) griddep_launch_dependents();
     griddep_wait();
     if (status && *reinterpret_cast<const volatile int *>(status) != 0) return;
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, sub = lane & 15, lower = lane >> 4;  // lower: the row 32 below
     int nr = n_rows ? *reinterpret_cast<const volatile int *>(n_rows) : rows;
     nr = nr < rows ? nr : rows;
     const int chunks = mx4_stages(cols), pitch = mx4_code_pitch(cols);
     const int row_tiles = chunks * Mx4<NV>::kStageTiles;
-    // item = (128-row tile, row r of 32, 256-column chunk), chunks innermost
-    for (long long it = (long long)blockIdx.x * kQWarps + (threadIdx.x >> 5); it < items;
-         it += (long long)gridDim.x * kQWarps) {
-        const int chunk = (int)(it % chunks);
-        const long long rr = it / chunks;
-        const int row0 = (int)(rr >> 5) * 128 + (int)(rr & 31);
-        const int col = chunk * kMx4StageCols + lane * 8;
-        const int n = cols - col;
-        float v[4][8];
+    Walk w(chunks, (long long)blockIdx.x * kQWarps + (threadIdx.x >> 5), (long long)gridDim.x * kQWarps);
+    auto load = [&]() {
+        const int row = w.row0() + 32 * lower, col = w.chunk * kMx4StageCols + sub * 16;
+        return load_raw16<T>(x + (size_t)row * ld + col, w.pair < pairs && row < nr ? cols - col : 0, vec);
+    };
+    auto store = [&](const Raw16<T> &r, int row0, int chunk) {
+        const int row = row0 + 32 * lower, col = chunk * kMx4StageCols + sub * 16;
+        uint32_t m;
+        if constexpr (sizeof(T) == 4) {
+            m = umax(raw8_amax<T>(r.h[0]), raw8_amax<T>(r.h[1]));
+        } else {
+            uint32_t m2 = r.h[0].w[0] & 0x7fff7fffu;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int row = row0 + 32 * i;
-            load8<T>(x + (size_t)row * ld + col, row < nr ? (n > 0 ? n : 0) : 0, vec != 0, v[i]);
+            for (int i = 1; i < 8; ++i) m2 = __vmaxu2(m2, r.h[i >> 2].w[i & 3] & 0x7fff7fffu);
+            m = umax(m2 & 0xffffu, m2 >> 16);
         }
+        if constexpr (!NV) m = umax(m, __shfl_xor_sync(0xffffffffu, m, 1));  // a block is two lanes
+        const Mx4Scale s = mx4_block_scale<NV>(amax_f32_bits<T>(m), ts, six_ts);
+        const uint64_t mul2 = f2_make(s.mul, s.mul);
+        uint32_t q[2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int row = row0 + 32 * i;
-            uint32_t word;
-            const uint32_t q = mx4_warp_quant<NV>(v[i], ts, six_ts, lane, word);
-            if (row < nr && col / 2 < pitch) *reinterpret_cast<uint32_t *>(codes + (size_t)row * pitch + col / 2) = q;
-            constexpr int kTileLanes = Mx4<NV>::kTileCols / 8;
-            if (lane % kTileLanes == 0)  // (rows past the end: scale 0, so that a tile is always whole)
-                *reinterpret_cast<uint32_t *>(scales + scale_word_offset(row, chunk * Mx4<NV>::kStageTiles + lane / kTileLanes,
-                                                                         row_tiles)) = word;
+        for (int h = 0; h < 2; ++h) {
+            float v[8];
+            raw8_values<T>(r.h[h], v);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = f2_split(f2_mul(f2_make(v[2 * i], v[2 * i + 1]), mul2));
+                v[2 * i] = f.x;
+                v[2 * i + 1] = f.y;
+            }
+            q[h] = s.zero ? 0u : cvt_e2m1x8(v);
         }
+        // the lanes of a tile put their scale bytes together
+        constexpr int kLanes = NV ? 1 : 2, kTileLanes = 4 * kLanes;
+        uint32_t word = s.byte << (8 * ((sub / kLanes) & 3));
+        word |= __shfl_xor_sync(0xffffffffu, word, kLanes);
+        word |= __shfl_xor_sync(0xffffffffu, word, 2 * kLanes);
+        if (row < nr && col / 2 < pitch) {  // (a row's codes end at a multiple of 16 bytes: the last 8 may be beyond)
+            *reinterpret_cast<uint2 *>(codes + (size_t)row * pitch + col / 2) = make_uint2(q[0], q[1]);
+        }
+        if (sub % kTileLanes == 0)  // (rows past the end: scale 0, so that a tile is always whole)
+            *reinterpret_cast<uint32_t *>(scales + scale_word_offset(row, chunk * Mx4<NV>::kStageTiles + sub / kTileLanes,
+                                                                     row_tiles)) = word;
+    };
+    // the next item's rows load while the current ones are converted
+    Raw16<T> a = load(), b;
+    while (w.pair < pairs) {
+        int row0 = w.row0(), chunk = w.chunk;
+        w.next();
+        b = load();
+        store(a, row0, chunk);
+        if (w.pair >= pairs) break;
+        row0 = w.row0();
+        chunk = w.chunk;
+        w.next();
+        a = load();
+        store(b, row0, chunk);
     }
 }
 
 template <typename T, bool NV>
 __global__ void __launch_bounds__(32 * kQWarps)
 mx4_dequant_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales, int rows, int cols, float ts,
-                   T *__restrict__ out, long long ld, int vec, long long items) {
-    const int lane = threadIdx.x & 31;
+                   T *__restrict__ out, long long ld, int vec, long long pairs) {
+    const int lane = threadIdx.x & 31, sub = lane & 15, lower = lane >> 4;
     const int chunks = mx4_stages(cols), pitch = mx4_code_pitch(cols);
     const int row_tiles = chunks * Mx4<NV>::kStageTiles;
-    for (long long it = (long long)blockIdx.x * kQWarps + (threadIdx.x >> 5); it < items;
-         it += (long long)gridDim.x * kQWarps) {
-        const int chunk = (int)(it % chunks);
-        const long long rr = it / chunks;
-        const int row0 = (int)(rr >> 5) * 128 + (int)(rr & 31);
-        const int col = chunk * kMx4StageCols + lane * 8;
-        const int n = cols - col;
-        uint32_t q[4] = {}, sb[4] = {};
-        if (n > 0) {
+    Walk w(chunks, (long long)blockIdx.x * kQWarps + (threadIdx.x >> 5), (long long)gridDim.x * kQWarps);
+    auto load = [&](uint2 &q, uint32_t &sb) {
+        const int row = w.row0() + 32 * lower, col = w.chunk * kMx4StageCols + sub * 16, blk = col / Mx4<NV>::kBlock;
+        q = make_uint2(0, 0);
+        sb = 0;
+        if (w.pair < pairs && row < rows && col < cols) {
+            q = __ldg(reinterpret_cast<const uint2 *>(codes + (size_t)row * pitch + col / 2));
+            sb = __ldg(scales + scale_word_offset(row, blk >> 2, row_tiles) + (blk & 3));
+        }
+    };
+    auto store = [&](uint2 q, uint32_t sb, int row0, int chunk) {
+        const int row = row0 + 32 * lower, col = chunk * kMx4StageCols + sub * 16, n = cols - col;
+        if (row >= rows || n <= 0) return;
+        const float s = mx4_scale_value<NV>(sb);
+        float v[2][8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = row0 + 32 * i;
-                if (row >= rows) continue;
-                q[i] = __ldg(reinterpret_cast<const uint32_t *>(codes + (size_t)row * pitch + col / 2));
-                const int blk = col / Mx4<NV>::kBlock;
-                sb[i] = __ldg(scales + scale_word_offset(row, blk >> 2, row_tiles) + (blk & 3));
+        for (int h = 0; h < 2; ++h) {
+            e2m1x8_values(h ? q.y : q.x, v[h]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                v[h][j] = __fmul_rn(v[h][j], s);  // exact
+                if (NV) v[h][j] = __fmul_rn(v[h][j], ts);
             }
+        }
+        T *dst = out + (size_t)row * ld + col;
+        if (vec == 2 && n >= 16) {
+            if constexpr (sizeof(T) == 4) {
+                st_global_v8(dst, reinterpret_cast<const uint32_t *>(v[0]));
+                st_global_v8(dst + 8, reinterpret_cast<const uint32_t *>(v[1]));
+            } else {
+                uint32_t o[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = row0 + 32 * i;
-                if (row >= rows) continue;
-                const float s = mx4_scale_value<NV>(sb[i]);
-                float v[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    v[j] = __fmul_rn(e2m1_value((q[i] >> (4 * j)) & 15u), s);  // exact
-                    if (NV) v[j] = __fmul_rn(v[j], ts);
-                }
-                store8<T>(out + (size_t)row * ld + col, n, vec != 0, v);
+                for (int j = 0; j < 8; ++j) o[j] = pack_x2<T>(v[j >> 2][2 * (j & 3)], v[j >> 2][2 * (j & 3) + 1]);
+                st_global_v8(dst, o);
             }
+        } else {
+            store8<T>(dst, n, vec != 0, v[0]);
+            store8<T>(dst + 8, n - 8, vec != 0, v[1]);
+        }
+    };
+    uint2 qa, qb;
+    uint32_t sa, sb;
+    load(qa, sa);
+    while (w.pair < pairs) {
+        int row0 = w.row0(), chunk = w.chunk;
+        w.next();
+        load(qb, sb);
+        store(qa, sa, row0, chunk);
+        if (w.pair >= pairs) break;
+        row0 = w.row0();
+        chunk = w.chunk;
+        w.next();
+        load(qa, sa);
+        store(qb, sb, row0, chunk);
+    }
+}
+
+// LayerNorm, one warp per row of at most 256 NCH columns: the row stays in registers
+// (one read), both sums by shuffles, the next row's loads in flight meanwhile.  fp32
+// statistics in two passes (mean, then the squares of the differences); the 4-bit
+// form is taken of the fp32 result, y is its rounding to x's type.
+template <typename T, bool NV, int NCH>
+__global__ void __launch_bounds__(32 * kQWarps)
+mx4_norm_warp_kernel(const T *__restrict__ x, long long ld, const float *__restrict__ gamma,
+                     const float *__restrict__ beta, float eps, int rows, int cols, const int *n_rows, float ts,
+                     float six_ts, T *__restrict__ y, long long ld_y, uint8_t *__restrict__ codes,
+                     uint8_t *__restrict__ scales, int vec, int vec_y, int vec_g, const int *status, int trigger) {
+    if (trigger) griddep_launch_dependents();
+    griddep_wait();
+    if (status && *reinterpret_cast<const volatile int *>(status) != 0) return;
+    int nr = n_rows ? *reinterpret_cast<const volatile int *>(n_rows) : rows;
+    nr = nr < rows ? nr : rows;
+    const int lane = threadIdx.x & 31, stride = gridDim.x * kQWarps;
+    const int chunks = mx4_stages(cols), pitch = mx4_code_pitch(cols);
+    const int row_tiles = chunks * Mx4<NV>::kStageTiles;
+    int row = blockIdx.x * kQWarps + (threadIdx.x >> 5);
+    Raw8<T> raw[NCH];
+    auto load = [&](int r) {
+#pragma unroll
+        for (int c = 0; c < NCH; ++c) {
+            const int col = c * kMx4StageCols + lane * 8;
+            raw[c] = load_raw8<T>(x + (size_t)r * ld + col, r < nr ? cols - col : 0, vec != 0);
+        }
+    };
+    if (row < nr) load(row);
+    for (; row < nr; row += stride) {
+        float v[NCH][8];
+        float sum = 0.f;
+#pragma unroll
+        for (int c = 0; c < NCH; ++c) {
+            raw8_values<T>(raw[c], v[c]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum += v[c][i];
+        }
+        if (row + stride < nr) load(row + stride);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        const float mean = sum / (float)cols;
+        float sq = 0.f;
+#pragma unroll
+        for (int c = 0; c < NCH; ++c) {
+            const int n = cols - c * kMx4StageCols - lane * 8;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float d = i < n ? v[c][i] - mean : 0.f;
+                v[c][i] = d;
+                sq = fmaf(d, d, sq);
+            }
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+        const float rstd = rsqrtf(sq / (float)cols + eps);
+#pragma unroll
+        for (int c = 0; c < NCH; ++c) {
+            if (c >= chunks) break;
+            const int col = c * kMx4StageCols + lane * 8, n = cols - col;
+            float g[8], b[8];
+            load8<float>(gamma + col, n, vec_g != 0, g);  // (columns past the end: 0, and so the result)
+            load8<float>(beta + col, n, vec_g != 0, b);
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                v[c][i] = fmaf(v[c][i] * rstd, g[i], b[i]);
+                if (i >= n) v[c][i] = 0.f;
+                m = umax(m, abs_bits(v[c][i]));
+            }
+            if (y) store8<T>(y + (size_t)row * ld_y + col, n, vec_y != 0, v[c]);
+            uint32_t word;
+            const uint32_t q = mx4_warp_quant<NV>(v[c], m, ts, six_ts, lane, word);
+            if (col / 2 < pitch) *reinterpret_cast<uint32_t *>(codes + (size_t)row * pitch + col / 2) = q;
+            constexpr int kTileLanes = Mx4<NV>::kTileCols / 8;
+            if (lane % kTileLanes == 0)
+                *reinterpret_cast<uint32_t *>(scales + scale_word_offset(row, c * Mx4<NV>::kStageTiles + lane / kTileLanes,
+                                                                         row_tiles)) = word;
         }
     }
 }
 
-// LayerNorm of a row in fp32 (mean, then the mean square of the differences, both
-// over the row's values held in registers or read again), y in the input's type,
-// and the 4-bit form of the fp32 result.  One CTA per row.
-__device__ __forceinline__ float block_sum(float v, float *red, int warps) {
+// The same with one CTA per row, for wider rows and for few of them: each warp holds
+// HELD of the row's 256-column chunks (every eighth); chunks beyond those are read
+// again in each pass (from L1 or L2).
+__device__ __forceinline__ float block_sum(float v, float *red) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    __syncthreads();
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
     float s = 0.f;
-    for (int i = 0; i < warps; ++i) s += red[i];
+#pragma unroll
+    for (int i = 0; i < kQWarps; ++i) s += red[i];
     return s;
 }
 
-template <typename T, bool NV>
+template <typename T, bool NV, int HELD>
 __global__ void __launch_bounds__(32 * kQWarps)
-mx4_norm_kernel(const T *__restrict__ x, long long ld, const float *__restrict__ gamma, const float *__restrict__ beta,
-                float eps, int rows, int cols, const int *n_rows, float ts, float six_ts, T *__restrict__ y, long long ld_y,
-                uint8_t *__restrict__ codes, uint8_t *__restrict__ scales, int vec, int vec_y, int vec_g,
-                const int *status, int trigger) {
-    __shared__ float red[kQWarps];
+mx4_norm_cta_kernel(const T *__restrict__ x, long long ld, const float *__restrict__ gamma,
+                    const float *__restrict__ beta, float eps, int rows, int cols, const int *n_rows, float ts,
+                    float six_ts, T *__restrict__ y, long long ld_y, uint8_t *__restrict__ codes,
+                    uint8_t *__restrict__ scales, int vec, int vec_y, int vec_g, const int *status, int trigger) {
+    __shared__ float red[2][kQWarps];  // one per sum: a row's second barrier separates its first from the next row's
     if (trigger) griddep_launch_dependents();
     griddep_wait();
     if (status && *reinterpret_cast<const volatile int *>(status) != 0) return;
@@ -135,77 +335,108 @@ mx4_norm_kernel(const T *__restrict__ x, long long ld, const float *__restrict__
     const int row_tiles = chunks * Mx4<NV>::kStageTiles;
     for (int row = blockIdx.x; row < nr; row += gridDim.x) {
         const T *src = x + (size_t)row * ld;
-        float sum = 0.f;
-        for (int c = warp; c < chunks; c += kQWarps) {
-            const int col = c * kMx4StageCols + lane * 8, n = cols - col > 0 ? cols - col : 0;
+        Raw8<T> raw[HELD];
+#pragma unroll
+        for (int h = 0; h < HELD; ++h) {
+            const int col = (warp + h * kQWarps) * kMx4StageCols + lane * 8;
+            raw[h] = load_raw8<T>(src + col, cols - col, vec != 0);
+        }
+        // f(chunk, first column, columns left, values): held chunks, then the others
+        auto each = [&](auto f) {
             float v[8];
-            load8<T>(src + col, n, vec != 0, v);
+#pragma unroll
+            for (int h = 0; h < HELD; ++h) {
+                const int c = warp + h * kQWarps, col = c * kMx4StageCols + lane * 8;
+                if (c >= chunks) break;
+                raw8_values<T>(raw[h], v);
+                f(c, col, cols - col, v);
+            }
+            for (int c = warp + HELD * kQWarps; c < chunks; c += kQWarps) {
+                const int col = c * kMx4StageCols + lane * 8;
+                load8<T>(src + col, cols - col, vec != 0, v);
+                f(c, col, cols - col, v);
+            }
+        };
+        float sum = 0.f;
+        each([&](int, int, int, const float (&v)[8]) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) sum += v[i];
-        }
-        const float mean = block_sum(sum, red, kQWarps) / (float)cols;
+        });
+        const float mean = block_sum(sum, red[0]) / (float)cols;
         float sq = 0.f;
-        for (int c = warp; c < chunks; c += kQWarps) {
-            const int col = c * kMx4StageCols + lane * 8, n = cols - col > 0 ? cols - col : 0;
-            float v[8];
-            load8<T>(src + col, n, vec != 0, v);
+        each([&](int, int, int n, const float (&v)[8]) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float d = i < n ? v[i] - mean : 0.f;
                 sq = fmaf(d, d, sq);
             }
-        }
-        const float rstd = rsqrtf(block_sum(sq, red, kQWarps) / (float)cols + eps);
-        for (int c = warp; c < chunks; c += kQWarps) {
-            const int col = c * kMx4StageCols + lane * 8, n = cols - col > 0 ? cols - col : 0;
-            float v[8], g[8], b[8];
-            load8<T>(src + col, n, vec != 0, v);
+        });
+        const float rstd = rsqrtf(block_sum(sq, red[1]) / (float)cols + eps);
+        each([&](int c, int col, int n, float (&v)[8]) {
+            float g[8], b[8];
             load8<float>(gamma + col, n, vec_g != 0, g);
             load8<float>(beta + col, n, vec_g != 0, b);
+            uint32_t m = 0;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = i < n ? fmaf((v[i] - mean) * rstd, g[i], b[i]) : 0.f;
+            for (int i = 0; i < 8; ++i) {
+                v[i] = i < n ? fmaf((v[i] - mean) * rstd, g[i], b[i]) : 0.f;
+                m = umax(m, abs_bits(v[i]));
+            }
             if (y) store8<T>(y + (size_t)row * ld_y + col, n, vec_y != 0, v);
             uint32_t word;
-            const uint32_t q = mx4_warp_quant<NV>(v, ts, six_ts, lane, word);
+            const uint32_t q = mx4_warp_quant<NV>(v, m, ts, six_ts, lane, word);
             if (col / 2 < pitch) *reinterpret_cast<uint32_t *>(codes + (size_t)row * pitch + col / 2) = q;
             constexpr int kTileLanes = Mx4<NV>::kTileCols / 8;
             if (lane % kTileLanes == 0)
                 *reinterpret_cast<uint32_t *>(scales + scale_word_offset(row, c * Mx4<NV>::kStageTiles + lane / kTileLanes,
                                                                          row_tiles)) = word;
-        }
+        });
     }
 }
 
-// CTAs of `kernel` that are resident at once, at most `need`.
+// CTAs of `kernel` that are resident at once (asked once per device), at most `need`.
 template <typename K>
-cudaError_t resident_grid(K kernel, long long need, int &blocks) {
-    int dev = 0, sms = 0, per_sm = 0;
+cudaError_t resident_grid(K kernel, std::atomic<int> (&cached)[64], long long need, int &blocks) {
+    int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, 32 * kQWarps, 0);
-    const long long cap = (long long)(per_sm > 0 ? per_sm : 1) * sms;
+    if (e != cudaSuccess) return e;
+    int cap = dev < 64 ? cached[dev].load(std::memory_order_acquire) : 0;
+    if (cap == 0) {
+        int sms = 0, per_sm = 0;
+        e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, 32 * kQWarps, 0);
+        if (e != cudaSuccess) return e;
+        cap = (per_sm > 0 ? per_sm : 1) * sms;
+        if (dev < 64) cached[dev].store(cap, std::memory_order_release);
+    }
     blocks = (int)(need < cap ? need : cap);
-    return e;
+    return cudaSuccess;
 }
 
 inline bool aligned16(const void *p, long long ld, int elem) {
     return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * elem) % 16 == 0;
 }
 
+inline int vec_width(const void *p, long long ld, int elem) {
+    return (reinterpret_cast<uintptr_t>(p) & 31) == 0 && (ld * elem) % 32 == 0 ? 2 : aligned16(p, ld, elem) ? 1 : 0;
+}
+
 template <typename T, bool NV>
 cudaError_t quant_typed(const Mx4QuantArgs &a, cudaStream_t s, bool pdl) {
-    const long long items = (long long)((a.rows + 127) / 128) * 32 * mx4_stages(a.cols);
+    // (all row pairs of the last tile, whose scale bytes are written whole)
+    const long long pairs = (long long)((a.rows + 127) / 128) * 64, items = pairs * mx4_stages(a.cols);
+    static std::atomic<int> cached[64];
     int blocks = 0;
-    cudaError_t e = resident_grid(mx4_quant_kernel<T, NV>, (items + kQWarps - 1) / kQWarps, blocks);
+    cudaError_t e = resident_grid(mx4_quant_kernel<T, NV>, cached, (items + kQWarps - 1) / kQWarps, blocks);
     if (e != cudaSuccess) return e;
-    const int vec = aligned16(a.x, a.ld, sizeof(T));
+    const int vec = vec_width(a.x, a.ld, sizeof(T));
     const float six = 6.0f * a.tensor_scale;
     if (pdl)
         return launch_pdl(mx4_quant_kernel<T, NV>, dim3(blocks), dim3(32 * kQWarps), 0, s, static_cast<const T *>(a.x),
-                          a.ld, a.rows, a.cols, a.n_rows, a.tensor_scale, six, a.codes, a.scales, vec, items, a.status,
+                          a.ld, a.rows, a.cols, a.n_rows, a.tensor_scale, six, a.codes, a.scales, vec, pairs, a.status,
                           a.trigger);
     mx4_quant_kernel<T, NV><<<blocks, 32 * kQWarps, 0, s>>>(static_cast<const T *>(a.x), a.ld, a.rows, a.cols, a.n_rows,
-                                                            a.tensor_scale, six, a.codes, a.scales, vec, items, a.status,
+                                                            a.tensor_scale, six, a.codes, a.scales, vec, pairs, a.status,
                                                             a.trigger);
     return cudaGetLastError();
 }
@@ -213,31 +444,46 @@ cudaError_t quant_typed(const Mx4QuantArgs &a, cudaStream_t s, bool pdl) {
 template <typename T, bool NV>
 cudaError_t dequant_typed(const uint8_t *codes, const uint8_t *scales, int rows, int cols, float ts, void *out,
                           long long ld, cudaStream_t s) {
-    const long long items = (long long)((rows + 127) / 128) * 32 * mx4_stages(cols);
+    const long long pairs = (long long)((rows + 127) / 128) * 64, items = pairs * mx4_stages(cols);
+    static std::atomic<int> cached[64];
     int blocks = 0;
-    cudaError_t e = resident_grid(mx4_dequant_kernel<T, NV>, (items + kQWarps - 1) / kQWarps, blocks);
+    cudaError_t e = resident_grid(mx4_dequant_kernel<T, NV>, cached, (items + kQWarps - 1) / kQWarps, blocks);
     if (e != cudaSuccess) return e;
     mx4_dequant_kernel<T, NV><<<blocks, 32 * kQWarps, 0, s>>>(codes, scales, rows, cols, ts, static_cast<T *>(out), ld,
-                                                              aligned16(out, ld, sizeof(T)), items);
+                                                              vec_width(out, ld, sizeof(T)), pairs);
     return cudaGetLastError();
 }
 
-template <typename T, bool NV>
-cudaError_t norm_typed(const Mx4NormArgs &a, cudaStream_t s, bool pdl) {
+template <typename T, bool NV, typename K>
+cudaError_t norm_launch(K kernel, std::atomic<int> (&cached)[64], int rows_per_cta, const Mx4NormArgs &a, cudaStream_t s,
+                        bool pdl) {
     int blocks = 0;
-    cudaError_t e = resident_grid(mx4_norm_kernel<T, NV>, a.q.rows, blocks);
+    cudaError_t e = resident_grid(kernel, cached, (a.q.rows + rows_per_cta - 1) / rows_per_cta, blocks);
     if (e != cudaSuccess) return e;
     const int vec = aligned16(a.q.x, a.q.ld, sizeof(T)), vec_y = aligned16(a.y, a.ld_y, sizeof(T));
     const int vec_g = aligned16(a.gamma, 4, 4) && aligned16(a.beta, 4, 4);
     const float six = 6.0f * a.q.tensor_scale;
     if (pdl)
-        return launch_pdl(mx4_norm_kernel<T, NV>, dim3(blocks), dim3(32 * kQWarps), 0, s, static_cast<const T *>(a.q.x),
-                          a.q.ld, a.gamma, a.beta, a.eps, a.q.rows, a.q.cols, a.q.n_rows, a.q.tensor_scale, six,
-                          static_cast<T *>(a.y), a.ld_y, a.q.codes, a.q.scales, vec, vec_y, vec_g, a.q.status, a.q.trigger);
-    mx4_norm_kernel<T, NV><<<blocks, 32 * kQWarps, 0, s>>>(
-        static_cast<const T *>(a.q.x), a.q.ld, a.gamma, a.beta, a.eps, a.q.rows, a.q.cols, a.q.n_rows, a.q.tensor_scale,
-        six, static_cast<T *>(a.y), a.ld_y, a.q.codes, a.q.scales, vec, vec_y, vec_g, a.q.status, a.q.trigger);
+        return launch_pdl(kernel, dim3(blocks), dim3(32 * kQWarps), 0, s, static_cast<const T *>(a.q.x), a.q.ld, a.gamma,
+                          a.beta, a.eps, a.q.rows, a.q.cols, a.q.n_rows, a.q.tensor_scale, six, static_cast<T *>(a.y),
+                          a.ld_y, a.q.codes, a.q.scales, vec, vec_y, vec_g, a.q.status, a.q.trigger);
+    kernel<<<blocks, 32 * kQWarps, 0, s>>>(static_cast<const T *>(a.q.x), a.q.ld, a.gamma, a.beta, a.eps, a.q.rows,
+                                           a.q.cols, a.q.n_rows, a.q.tensor_scale, six, static_cast<T *>(a.y), a.ld_y,
+                                           a.q.codes, a.q.scales, vec, vec_y, vec_g, a.q.status, a.q.trigger);
     return cudaGetLastError();
+}
+
+template <typename T, bool NV>
+cudaError_t norm_typed(const Mx4NormArgs &a, cudaStream_t s, bool pdl) {
+    // A warp per row once the rows fill the machine's warps several times over; a CTA per
+    // row for few rows (5 rows of 1000: 4.4 us against 7.9) and for rows a warp cannot hold
+    // in half its registers.
+    static std::atomic<int> c1[64], c3[64], w1[64], w4[64];
+    if (a.q.cols <= 256) return norm_launch<T, NV>(mx4_norm_warp_kernel<T, NV, 1>, c1, kQWarps, a, s, pdl);
+    if (a.q.cols <= 768 && a.q.rows >= 512)
+        return norm_launch<T, NV>(mx4_norm_warp_kernel<T, NV, 3>, c3, kQWarps, a, s, pdl);
+    if (a.q.cols <= 2048) return norm_launch<T, NV>(mx4_norm_cta_kernel<T, NV, 1>, w1, 1, a, s, pdl);
+    return norm_launch<T, NV>(mx4_norm_cta_kernel<T, NV, 4>, w4, 1, a, s, pdl);
 }
 
 }  // namespace
