@@ -197,7 +197,7 @@ def _check_4bit(q, ref, tol, fmt, ts):
 # ------------------------------------------------------------------- product --
 
 LINEAR = [  # rows, n, k
-    (1, 1, 1), (1, 16, 32), (1, 2304, 768), (2, 48, 100), (8, 130, 256), (16, 512, 2048), (17, 257, 320), (33, 96, 768),
+    (1, 1, 1), (1, 16, 32), (1, 2304, 768), (2, 48, 100), (3, 130, 4200), (1, 300, 9000), (32, 200, 2500), (31, 1030, 1300), (8, 130, 256), (16, 512, 2048), (17, 257, 320), (33, 96, 768),
     (64, 129, 1000), (127, 768, 768), (128, 128, 256), (129, 300, 288), (200, 1001, 1000), (257, 2304, 64),
     (300, 256, 2080), (513, 520, 520), (1025, 192, 256),
     # enough 256x256 tiles for CTA pairs, with ragged last tiles, one and several tiles per pair

@@ -461,40 +461,13 @@ def length_regulate(logits, feats, cu_seqlens, speed: float = 1.0, max_frames: i
 
 
 # ------------------------------------------------------ microscaled 4-bit rows --
+# A call of these on one token is shorter on the GPU than a few Python statements, so
+# the common path (current stream, current device) stays short: one allocation per
+# 4-bit matrix, integers instead of views, checks that read each property once.
 
 MX4_FORMATS = {"mxfp4": ALBERT_MXFP4, "nvfp4": ALBERT_NVFP4}
-_MX4_BLOCK = {"mxfp4": 32, "nvfp4": 16}
-
-
-class Mx4Tensor:
-    """A [rows, cols] matrix in microscaled 4-bit form (layout: albert.h): E2M1 codes,
-    uint8 [rows, ceil(cols / 32) * 16], and scale bytes, uint8 [ceil(rows / 128),
-    tiles per row, 512].  ``fmt`` is "mxfp4" or "nvfp4"; ``tensor_scale`` multiplies
-    every value of an "nvfp4" tensor (ignored for "mxfp4")."""
-
-    __slots__ = ("codes", "scales", "rows", "cols", "fmt", "tensor_scale")
-
-    def __init__(self, codes, scales, rows: int, cols: int, fmt: str = "mxfp4", tensor_scale: float = 1.0):
-        import torch
-        shapes = mx4_shapes(rows, cols, fmt)
-        for name, t, shape in (("codes", codes, shapes[0]), ("scales", scales, shapes[1])):
-            if tuple(t.shape) != shape or t.dtype != torch.uint8 or not t.is_contiguous():
-                raise ValueError(f"Mx4Tensor: {name} must be a contiguous uint8 tensor of shape {shape}, "
-                                 f"got {tuple(t.shape)} {t.dtype}")
-        if codes.device != scales.device:
-            raise ValueError(f"Mx4Tensor: codes on {codes.device}, scales on {scales.device}")
-        if fmt == "nvfp4" and not 2.0 ** -100 <= tensor_scale <= 2.0 ** 100:
-            raise ValueError(f"Mx4Tensor: tensor_scale {tensor_scale} outside [2^-100, 2^100]")
-        self.codes, self.scales, self.rows, self.cols = codes, scales, rows, cols
-        self.fmt, self.tensor_scale = fmt, float(tensor_scale)
-
-    @property
-    def shape(self):
-        return (self.rows, self.cols)
-
-    @property
-    def device(self):
-        return self.codes.device
+_MX4_TILES = {"mxfp4": 2, "nvfp4": 4}  # scale tiles per 256 columns
+_mx4_types: dict = {}
 
 
 def mx4_shapes(rows: int, cols: int, fmt: str):
@@ -503,114 +476,191 @@ def mx4_shapes(rows: int, cols: int, fmt: str):
         raise ValueError(f"format must be one of {sorted(MX4_FORMATS)}, got {fmt!r}")
     if rows < 0 or not 1 <= cols <= 1 << 24:
         raise ValueError(f"a 4-bit matrix has rows >= 0 and 1 <= cols <= 2^24, got [{rows}, {cols}]")
-    tiles = (cols + 255) // 256 * (256 // (4 * _MX4_BLOCK[fmt]))
-    return (rows, (cols + 31) // 32 * 16), ((rows + 127) // 128, tiles, 512)
+    return (rows, (cols + 31) // 32 * 16), ((rows + 127) // 128, (cols + 255) // 256 * _MX4_TILES[fmt], 512)
+
+
+class Mx4Tensor:
+    """A [rows, cols] matrix in microscaled 4-bit form (layout: albert.h): ``codes``,
+    E2M1 pairs, uint8 [rows, ceil(cols / 32) * 16], and ``scales``, uint8
+    [ceil(rows / 128), tiles per row, 512].  ``fmt`` is "mxfp4" or "nvfp4";
+    ``tensor_scale`` multiplies every value of an "nvfp4" matrix (ignored for "mxfp4")."""
+
+    __slots__ = ("_buf", "_codes", "_scales", "_cptr", "_sptr", "_dev", "rows", "cols", "fmt", "tensor_scale")
+
+    def __init__(self, codes, scales, rows: int, cols: int, fmt: str = "mxfp4", tensor_scale: float = 1.0):
+        import torch
+        cs, ss = mx4_shapes(rows, cols, fmt)
+        u8 = torch.uint8
+        if codes.shape != cs or codes.dtype != u8 or not codes.is_contiguous():
+            raise ValueError(f"Mx4Tensor: codes must be a contiguous uint8 tensor of shape {cs}, "
+                             f"got {tuple(codes.shape)} {codes.dtype}")
+        if scales.shape != ss or scales.dtype != u8 or not scales.is_contiguous():
+            raise ValueError(f"Mx4Tensor: scales must be a contiguous uint8 tensor of shape {ss}, "
+                             f"got {tuple(scales.shape)} {scales.dtype}")
+        self._dev = codes.get_device()
+        if scales.get_device() != self._dev:
+            raise ValueError(f"Mx4Tensor: codes on {codes.device}, scales on {scales.device}")
+        self._buf, self._codes, self._scales = None, codes, scales
+        self._cptr, self._sptr = codes.data_ptr(), scales.data_ptr()
+        self.rows, self.cols, self.fmt, self.tensor_scale = rows, cols, fmt, _mx4_scale(fmt, tensor_scale)
+
+    def _split(self):
+        c, s = mx4_shapes(self.rows, self.cols, self.fmt)
+        n, off = c[0] * c[1], self._sptr - self._cptr
+        self._codes = self._buf[:n].view(c)
+        self._scales = self._buf[off:off + s[0] * s[1] * s[2]].view(s)
+
+    @property
+    def codes(self):
+        if self._codes is None:
+            self._split()
+        return self._codes
+
+    @property
+    def scales(self):
+        if self._scales is None:
+            self._split()
+        return self._scales
+
+    @property
+    def shape(self):
+        return (self.rows, self.cols)
+
+    @property
+    def device(self):
+        return (self._buf if self._buf is not None else self._codes).device
+
+
+def _mx4_scale(fmt: str, tensor_scale) -> float:
+    ts = float(tensor_scale)
+    if fmt == "nvfp4" and not 2.0 ** -100 <= ts <= 2.0 ** 100:
+        raise ValueError(f"tensor scale {ts} outside [2^-100, 2^100]")
+    return ts
 
 
 def mx4_empty(rows: int, cols: int, fmt: str = "mxfp4", tensor_scale: float = 1.0, device="cuda") -> Mx4Tensor:
-    """A 4-bit matrix with uninitialised contents."""
+    """A 4-bit matrix with uninitialised contents (codes and scales in one allocation)."""
     import torch
     c, s = mx4_shapes(rows, cols, fmt)
-    return Mx4Tensor(torch.empty(c, dtype=torch.uint8, device=device),
-                     torch.empty(s, dtype=torch.uint8, device=device), rows, cols, fmt, tensor_scale)
+    t = Mx4Tensor.__new__(Mx4Tensor)
+    off = (c[0] * c[1] + 127) // 128 * 128
+    t._buf = b = torch.empty(off + s[0] * s[1] * s[2], dtype=torch.uint8, device=device)
+    t._codes = t._scales = None
+    t._dev = b.get_device()
+    t._cptr = b.data_ptr()
+    t._sptr = t._cptr + off
+    t.rows, t.cols, t.fmt, t.tensor_scale = rows, cols, fmt, _mx4_scale(fmt, tensor_scale)
+    return t
 
 
-def _mx4_type(t, what: str) -> int:
-    import torch
-    code = {torch.bfloat16: ALBERT_BF16, torch.float32: ALBERT_FP32, torch.float16: ALBERT_FP16}.get(t)
+def _mx4_type(dtype, what: str) -> int:
+    if not _mx4_types:
+        import torch
+        _mx4_types.update({torch.bfloat16: ALBERT_BF16, torch.float32: ALBERT_FP32, torch.float16: ALBERT_FP16})
+    code = _mx4_types.get(dtype)
     if code is None:
-        raise ValueError(f"{what} must be bfloat16, float16 or float32, got {t}")
+        raise ValueError(f"{what} must be bfloat16, float16 or float32, got {dtype}")
     return code
 
 
-def _mx4_rows(t, what: str, shape=None) -> int:
-    """Check a matrix of rows (unit column stride, any row stride); its row stride."""
+def _mx4_grad(t, what: str) -> None:
     import torch
-    if not t.is_cuda or t.dim() != 2 or (shape is not None and tuple(t.shape) != tuple(shape)):
-        want = "" if shape is None else f" of shape {tuple(shape)}"
-        raise ValueError(f"{what} must be a 2-D CUDA tensor{want}, got {tuple(t.shape)} on {t.device}")
+    if torch.is_grad_enabled():
+        raise ValueError(f"{what} requires grad: the 4-bit operators have no backward pass (use torch.no_grad())")
+
+
+def _mx4_rows(t, what: str, dev: int | None = None, shape=None):
+    """Check a matrix of rows on a GPU (unit column stride, any row stride without
+    overlap); (rows, cols, row stride, device ordinal)."""
+    where = t.get_device()
+    if where < 0 or t.dim() != 2:
+        raise ValueError(f"{what} must be a 2-D CUDA tensor, got {tuple(t.shape)} on {t.device}")
+    if dev is not None and where != dev:
+        raise ValueError(f"{what} is on {t.device}, expected cuda:{dev}")
     rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
-        raise ValueError(f"{what} must have unit stride along its columns, got strides {t.stride()}")
-    if t.requires_grad and torch.is_grad_enabled():
-        raise ValueError(f"{what} requires grad: the 4-bit operators have no backward pass (use torch.no_grad())")
-    ld = t.stride(0)
-    if rows > 1 and ld < cols:
-        raise ValueError(f"{what}: rows overlap (strides {t.stride()})")
-    return ld if rows > 1 else cols
+    if shape is not None and (rows, cols) != shape:
+        raise ValueError(f"{what} must have shape {shape}, got {(rows, cols)}")
+    ld, one = t.stride()
+    if (one != 1 and cols > 1) or (ld < cols and rows > 1):
+        raise ValueError(f"{what} must have unit stride along its columns and rows that do not overlap, "
+                         f"got strides {(ld, one)} for shape {(rows, cols)}")
+    if t.requires_grad:
+        _mx4_grad(t, what)
+    return rows, cols, ld if rows > 1 else cols, where
 
 
-def _mx4_vector(t, n: int, what: str, device):
+def _mx4_vector(t, n: int, what: str, dev: int) -> int:
     import torch
-    if tuple(t.shape) != (n,) or t.dtype != torch.float32 or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{what} must be a contiguous float32 tensor of shape ({n},) on {device}, "
+    if t.shape != (n,) or t.dtype != torch.float32 or t.get_device() != dev or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{what} must be a contiguous float32 tensor of shape ({n},) on cuda:{dev}, "
                          f"got {tuple(t.shape)} {t.dtype} on {t.device}")
-    if t.requires_grad and torch.is_grad_enabled():
-        raise ValueError(f"{what} requires grad: the 4-bit operators have no backward pass (use torch.no_grad())")
+    if t.requires_grad:
+        _mx4_grad(t, what)
     return t.data_ptr()
 
 
-def _mx4_same(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
+def _mx4_away(dev: int, stream) -> bool:
+    """Whether a call must first switch to another device or stream."""
+    import torch
+    if dev < 0:
+        raise ValueError("4-bit matrices must be on a CUDA device")
+    return stream is not None or torch.cuda.current_device() != dev
 
 
-class _Mx4On:
-    """Run allocations and launches on `device`, and on `stream` if one is given."""
+def _mx4_on(dev: int, stream):
+    import torch
+    if stream is None:
+        return torch.cuda.device(dev)
+    if stream.device.index != dev:
+        raise ValueError(f"stream of {stream.device} for tensors on cuda:{dev}")
+    return torch.cuda.stream(stream)
 
-    __slots__ = ("ctx",)
 
-    def __init__(self, device, stream):
-        import torch
-        self.ctx = []
-        if stream is not None:
-            if stream.device != device:
-                raise ValueError(f"stream of {stream.device} for tensors on {device}")
-            self.ctx.append(torch.cuda.stream(stream))
-        elif torch.cuda.current_device() != device.index:
-            self.ctx.append(torch.cuda.device(device))
-
-    def __enter__(self):
-        for c in self.ctx:
-            c.__enter__()
-
-    def __exit__(self, *a):
-        for c in self.ctx:
-            c.__exit__(*a)
+def _mx4_stream(dev: int) -> int:
+    import torch
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def mx4_quantize(x, fmt: str = "mxfp4", tensor_scale: float = 1.0, out: Mx4Tensor | None = None, stream=None) -> Mx4Tensor:
     """Rows of x [rows, cols] (bf16, fp16 or fp32, any row stride) in 4-bit form
     (albert_mx4_quantize).  Asynchronous; outputs are allocated on the stream used."""
-    ld, typ = _mx4_rows(x, "x"), _mx4_type(x.dtype, "x")
-    rows, cols = x.shape
-    with _Mx4On(x.device, stream):
-        if out is None:
-            out = mx4_empty(rows, cols, fmt, tensor_scale, x.device)
-        elif out.shape != (rows, cols) or out.fmt != fmt or out.device != x.device:
-            raise ValueError(f"out must be a {fmt} matrix of shape {(rows, cols)} on {x.device}")
-        else:
-            out = Mx4Tensor(out.codes, out.scales, rows, cols, fmt, tensor_scale)
-        _check(lib().albert_mx4_quantize(_ptr(x), typ, ld, rows, cols, MX4_FORMATS[fmt], out.tensor_scale,
-                                         _ptr(out.codes), _ptr(out.scales), _stream_ptr()), "albert_mx4_quantize")
+    rows, cols, ld, dev = _mx4_rows(x, "x")
+    typ = _mx4_type(x.dtype, "x")
+    if _mx4_away(dev, stream):
+        with _mx4_on(dev, stream):
+            return mx4_quantize(x, fmt, tensor_scale, out)
+    if out is None:
+        out = mx4_empty(rows, cols, fmt, tensor_scale, x.device)
+    elif out.shape != (rows, cols) or out.fmt != fmt or out._dev != dev:
+        raise ValueError(f"out must be a {fmt} matrix of shape {(rows, cols)} on {x.device}")
+    else:
+        out.tensor_scale = _mx4_scale(fmt, tensor_scale)
+    rc = lib().albert_mx4_quantize(x.data_ptr(), typ, ld, rows, cols, MX4_FORMATS[fmt], out.tensor_scale, out._cptr,
+                                   out._sptr, _mx4_stream(dev))
+    if rc:
+        raise AlbertError(rc, "albert_mx4_quantize")
     return out
 
 
 def mx4_dequantize(t: Mx4Tensor, dtype=None, out=None, stream=None):
     """The values of a 4-bit matrix, rounded once to `dtype` (default bfloat16)."""
     import torch
-    if not t.codes.is_cuda:
-        raise ValueError(f"the 4-bit matrix must be on a CUDA device, got {t.device}")
-    if out is not None and dtype is not None and out.dtype != dtype:
-        raise ValueError(f"out is {out.dtype}, dtype is {dtype}")
-    with _Mx4On(t.device, stream):
-        if out is None:
-            out = torch.empty(t.rows, t.cols, dtype=torch.bfloat16 if dtype is None else dtype, device=t.device)
-        ld, typ = _mx4_rows(out, "out", t.shape), _mx4_type(out.dtype, "out")
-        _mx4_same(t.device, out=out)
-        _check(lib().albert_mx4_dequantize(_ptr(t.codes), _ptr(t.scales), t.rows, t.cols, MX4_FORMATS[t.fmt],
-                                           t.tensor_scale, _ptr(out), typ, ld, _stream_ptr()), "albert_mx4_dequantize")
+    dev = t._dev
+    if _mx4_away(dev, stream):
+        with _mx4_on(dev, stream):
+            return mx4_dequantize(t, dtype, out)
+    rows, cols = t.rows, t.cols
+    if out is None:
+        out = torch.empty((rows, cols), dtype=torch.bfloat16 if dtype is None else dtype, device=t.device)
+        ld = cols
+    else:
+        if dtype is not None and out.dtype != dtype:
+            raise ValueError(f"out is {out.dtype}, dtype is {dtype}")
+        ld = _mx4_rows(out, "out", dev, (rows, cols))[2]
+    rc = lib().albert_mx4_dequantize(t._cptr, t._sptr, rows, cols, MX4_FORMATS[t.fmt], t.tensor_scale, out.data_ptr(),
+                                     _mx4_type(out.dtype, "out"), ld, _mx4_stream(dev))
+    if rc:
+        raise AlbertError(rc, "albert_mx4_dequantize")
     return out
 
 
@@ -619,63 +669,75 @@ def mx4_layer_norm(x, gamma, beta, eps: float = 1e-12, fmt: str = "mxfp4", tenso
     """LayerNorm over the rows of x: (y in x's dtype, or None if not return_rows;
     the 4-bit form of the fp32 result) in one pass (albert_mx4_layer_norm)."""
     import torch
-    ld, typ = _mx4_rows(x, "x"), _mx4_type(x.dtype, "x")
-    rows, cols = x.shape
-    g, b = _mx4_vector(gamma, cols, "gamma", x.device), _mx4_vector(beta, cols, "beta", x.device)
-    with _Mx4On(x.device, stream):
-        y = torch.empty(rows, cols, dtype=x.dtype, device=x.device) if return_rows else None
-        q = mx4_empty(rows, cols, fmt, tensor_scale, x.device)
-        _check(lib().albert_mx4_layer_norm(_ptr(x), typ, ld, g, b, float(eps), rows, cols, MX4_FORMATS[fmt],
-                                           q.tensor_scale, _ptr(y), cols, _ptr(q.codes), _ptr(q.scales),
-                                           _stream_ptr()), "albert_mx4_layer_norm")
+    rows, cols, ld, dev = _mx4_rows(x, "x")
+    typ = _mx4_type(x.dtype, "x")
+    if _mx4_away(dev, stream):
+        with _mx4_on(dev, stream):
+            return mx4_layer_norm(x, gamma, beta, eps, fmt, tensor_scale, return_rows)
+    g, b = _mx4_vector(gamma, cols, "gamma", dev), _mx4_vector(beta, cols, "beta", dev)
+    y = torch.empty((rows, cols), dtype=x.dtype, device=x.device) if return_rows else None
+    q = mx4_empty(rows, cols, fmt, tensor_scale, x.device)
+    rc = lib().albert_mx4_layer_norm(x.data_ptr(), typ, ld, g, b, eps, rows, cols, MX4_FORMATS[fmt], q.tensor_scale,
+                                     None if y is None else y.data_ptr(), cols, q._cptr, q._sptr, _mx4_stream(dev))
+    if rc:
+        raise AlbertError(rc, "albert_mx4_layer_norm")
     return y, q
 
 
-def _mx4_linear(x, w: Mx4Tensor, bias, residual, gelu, x_scale, stream, out, out_dtype, q_scale):
+def _mx4_linear(x, w: Mx4Tensor, bias, residual, gelu, x_scale, stream, out, dtype, q_scale):
     import torch
-    a = albert_mx4_linear_args()
-    if isinstance(x, Mx4Tensor):
+    packed = isinstance(x, Mx4Tensor)
+    if packed:
+        rows, k, dev = x.rows, x.cols, x._dev
         if x.fmt != w.fmt:
             raise ValueError(f"x is {x.fmt}, w is {w.fmt}")
-        if not x.codes.is_cuda:
-            raise ValueError(f"x must be on a CUDA device, got {x.device}")
-        rows, k = x.shape
-        a.a_codes, a.a_scales, a.x_scale = _ptr(x.codes), _ptr(x.scales), x.tensor_scale
     else:
-        a.ld_x, a.x_type = _mx4_rows(x, "x"), _mx4_type(x.dtype, "x")
-        rows, k = x.shape
-        a.x, a.x_scale = _ptr(x), float(x_scale)
-    device, n = x.device, w.rows
-    if w.cols != k or n < 1:
-        raise ValueError(f"x is [{rows}, {k}], w is {list(w.shape)}: w must be [n >= 1, {k}]")
-    _mx4_same(device, w=w)
-    a.w_codes, a.w_scales, a.w_scale = _ptr(w.codes), _ptr(w.scales), w.tensor_scale
-    a.rows, a.n, a.k, a.fmt, a.gelu = rows, n, k, MX4_FORMATS[w.fmt], 1 if gelu else 0
+        rows, k, ld, dev = _mx4_rows(x, "x")
+    n = w.rows
+    if w.cols != k or n < 1 or w._dev != dev:
+        raise ValueError(f"x is [{rows}, {k}] on device {dev}, w is [{n}, {w.cols}] on device {w._dev}: "
+                         f"w must be [n >= 1, {k}] on the same device")
+    if _mx4_away(dev, stream):
+        with _mx4_on(dev, stream):
+            return _mx4_linear(x, w, bias, residual, gelu, x_scale, None, out, dtype, q_scale)
+    a = albert_mx4_linear_args()
+    if packed:
+        a.a_codes, a.a_scales, a.x_scale = x._cptr, x._sptr, x.tensor_scale
+    else:
+        a.x, a.ld_x, a.x_type, a.x_scale = x.data_ptr(), ld, _mx4_type(x.dtype, "x"), x_scale
+    a.w_codes, a.w_scales, a.w_scale = w._cptr, w._sptr, w.tensor_scale
+    a.rows, a.n, a.k = rows, n, k
+    a.fmt = fmt = MX4_FORMATS[w.fmt]
+    if gelu:
+        a.gelu = 1
     if bias is not None:
-        a.bias = _mx4_vector(bias, n, "bias", device)
-    with _Mx4On(device, stream):
-        if q_scale is None:
-            if out is None:
-                out = torch.empty(rows, n, dtype=out_dtype, device=device)
-            a.ld_out, a.out_type = _mx4_rows(out, "out", (rows, n)), _mx4_type(out.dtype, "out")
-            _mx4_same(device, out=out)
-            a.out = _ptr(out)
+        a.bias = _mx4_vector(bias, n, "bias", dev)
+    if q_scale is None:
+        if out is None:
+            out = torch.empty((rows, n), dtype=dtype, device=w.device)
+            a.ld_out = n
         else:
-            out = mx4_empty(rows, n, w.fmt, q_scale, device)
-            a.q_codes, a.q_scales, a.q_scale = _ptr(out.codes), _ptr(out.scales), out.tensor_scale
+            if dtype is not None and out.dtype != dtype:
+                raise ValueError(f"out is {out.dtype}, dtype is {dtype}")
+            a.ld_out = _mx4_rows(out, "out", dev, (rows, n))[2]
+        a.out, a.out_type = out.data_ptr(), _mx4_type(out.dtype, "out")
         if residual is not None:
-            a.ld_residual = _mx4_rows(residual, "residual", (rows, n))
-            if q_scale is not None or residual.dtype != out.dtype:
-                raise ValueError(f"residual must have the result's type ({out_dtype if q_scale is None else 'none'}), "
-                                 f"got {residual.dtype}")
-            _mx4_same(device, residual=residual)
-            a.residual = _ptr(residual)
-        if a.x:
-            ws = lib().albert_mx4_linear_workspace_bytes(rows, k, a.fmt)
-            if ws:
-                work = torch.empty(ws, dtype=torch.uint8, device=device)
-                a.workspace = _ptr(work)
-        _check(lib().albert_mx4_linear(C.byref(a), _stream_ptr()), "albert_mx4_linear")
+            if residual.dtype != out.dtype:
+                raise ValueError(f"residual must have the result's type {out.dtype}, got {residual.dtype}")
+            a.ld_residual = _mx4_rows(residual, "residual", dev, (rows, n))[2]
+            a.residual = residual.data_ptr()
+    else:
+        out = mx4_empty(rows, n, w.fmt, q_scale, w.device)
+        a.q_codes, a.q_scales, a.q_scale = out._cptr, out._sptr, out.tensor_scale
+    L = lib()
+    if not packed:
+        ws = L.albert_mx4_linear_workspace_bytes(rows, k, fmt)
+        if ws:
+            work = torch.empty(ws, dtype=torch.uint8, device=w.device)
+            a.workspace = work.data_ptr()
+    rc = L.albert_mx4_linear(C.byref(a), _mx4_stream(dev))
+    if rc:
+        raise AlbertError(rc, "albert_mx4_linear")
     return out
 
 
@@ -686,17 +748,16 @@ def mx4_linear(x, w: Mx4Tensor, bias=None, residual=None, gelu: bool = False, dt
     x: rows (bf16, fp16 or fp32), quantized in the call with tensor scale x_scale as
     mx4_quantize does, or a 4-bit matrix of w's format.  w: [n, k] 4-bit weights.
     bias [n] fp32; residual [rows, n] of the result's dtype (default bfloat16)."""
-    import torch
-    if out is not None and dtype is not None and out.dtype != dtype:
-        raise ValueError(f"out is {out.dtype}, dtype is {dtype}")
-    return _mx4_linear(x, w, bias, residual, gelu, x_scale, stream, out, torch.bfloat16 if dtype is None else dtype,
-                       None)
+    if out is None and dtype is None:
+        import torch
+        dtype = torch.bfloat16
+    return _mx4_linear(x, w, bias, residual, gelu, x_scale, stream, out, dtype, None)
 
 
 def mx4_linear_quant(x, w: Mx4Tensor, bias=None, gelu: bool = False, x_scale: float = 1.0, out_scale: float = 1.0,
                      stream=None) -> Mx4Tensor:
     """mx4_linear whose fp32 result leaves in w's 4-bit format (tensor scale out_scale)."""
-    return _mx4_linear(x, w, bias, None, gelu, x_scale, stream, None, None, float(out_scale))
+    return _mx4_linear(x, w, bias, None, gelu, x_scale, stream, None, None, out_scale)
 
 
 def mx4_status(stream=None) -> int:

@@ -360,6 +360,19 @@ struct Mx4GemmArgs {
 };
 cudaError_t launch_mx4_gemm(const Mx4GemmArgs &a, int num_sms, cudaStream_t s, bool pdl);
 
+// The same for at most kMx4MaxTokens rows (mx4_few_tokens), which it quantizes itself
+// when x is given (then a, a_scales are unused): one launch, no workspace.
+constexpr int kMx4MaxTokens = 32;
+struct Mx4TokArgs : Mx4GemmArgs {
+    const void *x;          // [M, K] rows of x_type, or nullptr: a, a_scales
+    int x_type;
+    long long ld_x;
+    float x_ts;
+    int vec_x;              // the rows are 16-byte aligned
+};
+bool mx4_few_tokens(int rows, int K);
+cudaError_t launch_mx4_tokens(const Mx4TokArgs &a, int num_sms, cudaStream_t s);
+
 // fp32 -> bf16 conversion of a parameter block.
 cudaError_t launch_f32_to_bf16(const float *src, bf16 *dst, size_t n, cudaStream_t s);
 

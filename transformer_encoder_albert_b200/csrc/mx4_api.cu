@@ -1,5 +1,6 @@
 // mx4_api.cu -- the C entries of the microscaled 4-bit operators (include/albert.h):
 // checks of their arguments and their launches.
+#include <atomic>
 #include <cmath>
 
 #include "albert.h"
@@ -30,6 +31,29 @@ size_t codes_bytes(int rows, int cols) { return (size_t)rows * mx4_code_pitch(co
 size_t up16(size_t n) { return (n + 15) / 16 * 16; }
 
 int status_of(cudaError_t e) { return e == cudaSuccess ? ALBERT_OK : ALBERT_ERR_CUDA; }
+
+// SM count and status word of the current device, looked up once per device.
+cudaError_t device_info(int &sms, int *&status) {
+    static std::atomic<int> known_sms[64];
+    static std::atomic<int *> known_status[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 64 && (status = known_status[dev].load(std::memory_order_acquire)) != nullptr) {
+        sms = known_sms[dev].load(std::memory_order_relaxed);
+        return cudaSuccess;
+    }
+    void *p = nullptr;
+    e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e == cudaSuccess) e = cudaGetSymbolAddress(&p, g_mx4_status);
+    if (e != cudaSuccess) return e;
+    status = static_cast<int *>(p);
+    if (dev < 64) {
+        known_sms[dev].store(sms, std::memory_order_relaxed);
+        known_status[dev].store(status, std::memory_order_release);
+    }
+    return cudaSuccess;
+}
 
 // Checks shared by the entries that write a 4-bit tensor from rows of x.
 int check_rows(const void *x, int x_type, long long ld, int rows, int cols, int fmt, float ts, const void *codes,
@@ -96,7 +120,7 @@ int albert_mx4_layer_norm(const void *x, int x_type, long long ld_x, const float
 }
 
 size_t albert_mx4_linear_workspace_bytes(int rows, int k, int fmt) {
-    if (rows < 1 || !cols_ok(k) || !is_format(fmt)) return 0;
+    if (rows < 1 || !cols_ok(k) || !is_format(fmt) || mx4_few_tokens(rows, k)) return 0;
     return up16(codes_bytes(rows, k)) + scales_bytes(rows, k, fmt == ALBERT_NVFP4);
 }
 
@@ -125,26 +149,11 @@ int albert_mx4_linear(const albert_mx4_linear_args *p, void *stream) {
 
     const bool nv = p->fmt == ALBERT_NVFP4;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    int dev = 0, sms = 0;
-    void *status = nullptr;
-    cudaError_t e = cudaGetDevice(&dev);
-    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-    if (e == cudaSuccess) e = cudaGetSymbolAddress(&status, g_mx4_status);
+    int sms = 0;
+    int *status = nullptr;
+    cudaError_t e = device_info(sms, status);
     if (e != cudaSuccess) return ALBERT_ERR_CUDA;
-    Mx4GemmArgs g{};
-    g.a = static_cast<const uint8_t *>(p->a_codes);
-    g.a_scales = static_cast<const uint8_t *>(p->a_scales);
-    if (p->x) {
-        Mx4QuantArgs q{};
-        q.x = p->x; q.type = p->x_type; q.ld = p->ld_x; q.rows = p->rows; q.cols = p->k;
-        q.nv = nv;
-        q.tensor_scale = nv ? p->x_scale : 1.0f;
-        q.codes = static_cast<uint8_t *>(p->workspace);
-        q.scales = q.codes + up16(codes_bytes(p->rows, p->k));
-        if ((e = launch_mx4_quant(q, s, false)) != cudaSuccess) return ALBERT_ERR_CUDA;
-        g.a = q.codes;
-        g.a_scales = q.scales;
-    }
+    Mx4TokArgs g{};
     g.w = static_cast<const uint8_t *>(p->w_codes);
     g.w_scales = static_cast<const uint8_t *>(p->w_scales);
     g.M = p->rows; g.N = p->n; g.K = p->k;
@@ -159,7 +168,28 @@ int albert_mx4_linear(const albert_mx4_linear_args *p, void *stream) {
         g.q_scales = static_cast<uint8_t *>(p->q_scales);
         g.q_ts = nv ? p->q_scale : 1.0f;
     }
-    g.status = static_cast<int *>(status);
+    g.status = status;
+    g.a = static_cast<const uint8_t *>(p->a_codes);
+    g.a_scales = static_cast<const uint8_t *>(p->a_scales);
+    if (mx4_few_tokens(p->rows, p->k)) {
+        g.x = p->x;
+        g.x_type = p->x_type;
+        g.ld_x = p->ld_x;
+        g.x_ts = nv ? p->x_scale : 1.0f;
+        g.vec_x = aligned(p->x, 16) && p->ld_x * elem_size(p->x_type) % 16 == 0;
+        return status_of(launch_mx4_tokens(g, sms, s));
+    }
+    if (p->x) {
+        Mx4QuantArgs q{};
+        q.x = p->x; q.type = p->x_type; q.ld = p->ld_x; q.rows = p->rows; q.cols = p->k;
+        q.nv = nv;
+        q.tensor_scale = nv ? p->x_scale : 1.0f;
+        q.codes = static_cast<uint8_t *>(p->workspace);
+        q.scales = q.codes + up16(codes_bytes(p->rows, p->k));
+        if ((e = launch_mx4_quant(q, s, false)) != cudaSuccess) return ALBERT_ERR_CUDA;
+        g.a = q.codes;
+        g.a_scales = q.scales;
+    }
     return status_of(launch_mx4_gemm(g, sms, s, p->x != nullptr));
 }
 

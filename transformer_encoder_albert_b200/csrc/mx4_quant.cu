@@ -136,9 +136,8 @@ mx4_quant_kernel(const T *__restrict__ x, long long ld, int rows, int cols, cons
         uint32_t word = s.byte << (8 * ((sub / kLanes) & 3));
         word |= __shfl_xor_sync(0xffffffffu, word, kLanes);
         word |= __shfl_xor_sync(0xffffffffu, word, 2 * kLanes);
-        if (row < nr && col / 2 < pitch) {  // (a row's codes end at a multiple of 16 bytes: the last 8 may be beyond)
+        if (row < nr && col / 2 < pitch)
             *reinterpret_cast<uint2 *>(codes + (size_t)row * pitch + col / 2) = make_uint2(q[0], q[1]);
-        }
         if (sub % kTileLanes == 0)  // (rows past the end: scale 0, so that a tile is always whole)
             *reinterpret_cast<uint32_t *>(scales + scale_word_offset(row, chunk * Mx4<NV>::kStageTiles + sub / kTileLanes,
                                                                      row_tiles)) = word;

@@ -1,0 +1,344 @@
+// mx4_tokens.cu -- the linear layer on 4-bit operands for a few rows (tokens): one
+// launch that quantizes the rows itself and is bound by reading the weights.
+//
+// The operands change places: 128 rows of W (features) are the product's M, the
+// tokens its N, so a 128x256 block of codes (16 KB) and its scales feed four
+// products whose cost does not matter.  A CTA holds one 128-feature tile and a slice
+// of K; a cluster of up to 8 CTAs shares a tile's K when the tiles alone would leave
+// SMs without work, and adds the partial sums over distributed shared memory in rank
+// order (no atomics, the same bits every time, no workspace).
+//   warp 0      : TMA ring of weight stages (all in flight before any product);
+//   warp 1      : scale copies and products.  A ring stage has scale columns of its
+//                 own in tensor memory, so the stage's barrier guards them too;
+//   warps 2..9  : quantize (or copy) the tokens of the slice, a stage per warp in turn,
+//                 into shared memory as the second operand, then the epilogue.
+// Rows of the token operand past the last token are never written: they only reach
+// result columns that nobody reads.
+#include <type_traits>
+
+#include "kernels.h"
+#include "mx4.cuh"
+#include "sm100_ptx.cuh"
+
+namespace albert {
+namespace {
+
+constexpr int kWorkers = 8;
+constexpr int kTokThreads = 32 * (2 + kWorkers);
+constexpr int kWBytes = 128 * 128;   // codes of a weight stage
+constexpr int kMaxRing = 6;
+constexpr int kMaxSlice = 16;        // stages of a CTA's K slice
+constexpr int kMaxCluster = 8;
+
+template <bool NV, int NT>
+struct TokPlan {
+    static constexpr int ST = Mx4<NV>::kStageTiles;
+    static constexpr int RING = kWBytes + ST * kMx4TileBytes;           // bytes of a weight stage
+    static constexpr int TOK = NT * 128 + ST * kMx4TileBytes;           // bytes of a token stage
+    static constexpr int SFCOLS = 8 * ST;                               // scale columns of a ring stage
+    static constexpr int COLS = NT + kMaxRing * SFCOLS <= 128 ? 128 : 256;
+    static_assert(NT + kMaxRing * SFCOLS <= 256, "tensor memory columns");
+    // CTAs of a cluster wait for one another, so none may hold tensor memory that keeps
+    // another from starting: a CTA takes at least its columns' share of an SM's shared
+    // memory (228 KB for 512 columns, 1 KB of each CTA's being the system's), and what
+    // fits an SM by shared memory also fits it by tensor memory.
+    static constexpr int kLeast = 233472 / 512 * COLS - 1024 - 64;
+    static int smem(int ring, int slice) {
+        const int n = 1024 + ring * RING + slice * TOK + NT * 128 * 4 + 512;
+        return n > kLeast ? n : kLeast;
+    }
+};
+
+__device__ __forceinline__ float ld_dsmem_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_shared_u2(uint32_t a, uint2 v) {
+    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(a), "r"(v.x), "r"(v.y) : "memory");
+}
+__device__ __forceinline__ void st_shared_u1(uint32_t a, uint32_t v) {
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+__device__ __forceinline__ float gelu_tok(float x) {
+    const float k = -2.0f * 0.7978845608028654f * 1.4426950408889634f;
+    return __fdividef(x, 1.0f + ex2_approx(k * x * fmaf(0.044715f * x, x, 1.0f)));
+}
+
+// One 256-column stage of the tokens, by a warp: a half-warp per row, 16 columns a lane.
+template <typename T, bool NV>
+__device__ __forceinline__ void stage_tokens(const Mx4TokArgs &p, int kb, uint32_t codes, uint32_t scales, int lane) {
+    const int sub = lane & 15, half = lane >> 4, col = kb * kMx4StageCols + sub * 16;
+    for (int r0 = 0; r0 < p.M; r0 += 2) {
+        const int row = r0 + half;
+        const T *src = static_cast<const T *>(p.x) + (size_t)row * p.ld_x + col;
+        const int n = row < p.M ? p.K - col : 0;
+        const Raw8<T> a = load_raw8<T>(src, n, p.vec_x != 0), b = load_raw8<T>(src + 8, n - 8, p.vec_x != 0);
+        uint32_t m = umax(raw8_amax<T>(a), raw8_amax<T>(b));
+        if constexpr (!NV) m = umax(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        const Mx4Scale s = mx4_block_scale<NV>(amax_f32_bits<T>(m), p.x_ts, 6.0f * p.x_ts);
+        float v[8], u[8];
+        raw8_values<T>(a, v);
+        raw8_values<T>(b, u);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            v[i] = __fmul_rn(v[i], s.mul);
+            u[i] = __fmul_rn(u[i], s.mul);
+        }
+        const uint2 q = s.zero ? make_uint2(0, 0) : make_uint2(cvt_e2m1x8(v), cvt_e2m1x8(u));
+        constexpr int kLanes = NV ? 1 : 2, kTileLanes = 4 * kLanes;
+        uint32_t word = s.byte << (8 * ((sub / kLanes) & 3));
+        word |= __shfl_xor_sync(0xffffffffu, word, kLanes);
+        word |= __shfl_xor_sync(0xffffffffu, word, 2 * kLanes);
+        if (row < p.M) {
+            // 128-byte rows with the 128-byte swizzle (16-byte chunk index XOR row % 8)
+            st_shared_u2(codes + row * 128 + (((sub >> 1) ^ (row & 7)) << 4) + (sub & 1) * 8, q);
+            if (sub % kTileLanes == 0) st_shared_u1(scales + (sub / kTileLanes) * kMx4TileBytes + row * 16, word);
+        }
+    }
+}
+template <bool NV>
+__device__ __forceinline__ void stage_packed(const Mx4TokArgs &p, int kb, uint32_t codes, uint32_t scales, int lane) {
+    constexpr int ST = Mx4<NV>::kStageTiles;
+    const int sub = lane & 15, half = lane >> 4, pitch = mx4_code_pitch(p.K), byte = kb * 128 + sub * 8;
+    for (int r0 = 0; r0 < p.M; r0 += 2) {
+        const int row = r0 + half;
+        if (row >= p.M) continue;
+        uint2 q = make_uint2(0, 0);
+        if (byte < pitch) q = __ldg(reinterpret_cast<const uint2 *>(p.a + (size_t)row * pitch + byte));
+        st_shared_u2(codes + row * 128 + (((sub >> 1) ^ (row & 7)) << 4) + (sub & 1) * 8, q);
+        if (sub < ST)  // (rows below 32: the first words of the tile's lanes)
+            st_shared_u1(scales + sub * kMx4TileBytes + row * 16,
+                         __ldg(reinterpret_cast<const uint32_t *>(p.a_scales + ((size_t)kb * ST + sub) * kMx4TileBytes + row * 16)));
+    }
+}
+
+template <bool NV, int NT>
+__global__ void __launch_bounds__(kTokThreads)
+mx4_tokens_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmSW, const Mx4TokArgs p,
+                  int ring, int slice_cap, int nclu) {
+    using P = TokPlan<NV, NT>;
+    constexpr int ST = P::ST;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *sW = base, *sT = sW + ring * kWBytes;                              // codes: weights, tokens
+    uint8_t *sSW = sT + slice_cap * NT * 128, *sST = sSW + ring * ST * kMx4TileBytes;  // scale tiles
+    float *sum = reinterpret_cast<float *>(sST + slice_cap * ST * kMx4TileBytes);      // [NT][128] partial sums
+    uint64_t *bars = reinterpret_cast<uint64_t *>(sum + NT * 128);
+    uint64_t *full = bars, *empty = bars + kMaxRing, *ready = bars + 2 * kMaxRing, *done = ready + kMaxSlice;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = nclu > 1 ? cluster_ctarank() : 0;
+    const int tile = (int)(blockIdx.x / nclu);
+    const int stages = mx4_stages(p.K);
+    const int kb0 = (int)((long long)stages * rank / nclu), kb1 = (int)((long long)stages * (rank + 1) / nclu);
+    const int nkb = kb1 - kb0;  // >= 1
+
+    if (threadIdx.x == 0) {
+        *abort_flag = 0;
+        wait_limit_init(p.wait_ns);
+        for (int i = 0; i < ring; ++i) {
+            mbar_init(smem_u32(&full[i]), 1);
+            mbar_init(smem_u32(&empty[i]), 1);
+        }
+        for (int i = 0; i < nkb; ++i) mbar_init(smem_u32(&ready[i]), 32);
+        mbar_init(smem_u32(done), 1);
+        fence_mbar_init();
+    }
+    if (warp == 1) {
+        tmem_alloc(smem_u32(tmem_slot), P::COLS);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            int stage = 0, issued = 0;
+            uint32_t phase = 0;
+            bool ok = true;
+            for (int kb = kb0; kb < kb1; ++kb) {
+                if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1, abort_flag)) { ok = false; break; }
+                const uint32_t fb = smem_u32(&full[stage]);
+                mbar_arrive_expect_tx(fb, P::RING);
+                tma_load_2d(smem_u32(sW) + stage * kWBytes, &tmW, fb, kb * 128, tile * 128);
+                tma_load_2d(smem_u32(sSW) + stage * ST * kMx4TileBytes, &tmSW, fb, 0, (tile * stages + kb) * 2 * ST);
+                ++issued;
+                if (++stage == ring) { stage = 0; phase ^= 1; }
+            }
+            if (!ok)
+                for (int i = 0; i < ring && i < issued; ++i) {
+                    if (--stage < 0) { stage = ring - 1; phase ^= 1; }
+                    mbar_wait_drain(smem_u32(&full[stage]), phase);
+                }
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        const uint32_t leader = elect_leader();
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, abort_flag)) != 0;
+        };
+        uint32_t stage = 0, phase = 0;
+        for (int i = 0; i < nkb; ++i) {
+            if (!wait(&ready[i], 0) || !wait(&full[stage], phase)) break;
+            tc_fence_after();
+            const uint32_t w0 = smem_u32(sW) + stage * kWBytes, t0 = smem_u32(sT) + i * NT * 128;
+            const uint32_t fw = smem_u32(sSW) + stage * ST * kMx4TileBytes, ft = smem_u32(sST) + i * ST * kMx4TileBytes;
+            const uint32_t ca = tmem + NT + stage * P::SFCOLS, cb = ca + 4 * ST;
+#pragma unroll
+            for (int g = 0; g < ST; ++g) {
+                tmem_cp_scales<false>(leader, ca + 4 * g, scale_tile_desc(fw + g * kMx4TileBytes));
+                tmem_cp_scales<false>(leader, cb + 4 * g, scale_tile_desc(ft + g * kMx4TileBytes));
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int g = NV ? k : k >> 1;
+                umma_mx4<NV, false>(leader, tmem, sw128_kmajor_desc(w0 + k * 32), sw128_kmajor_desc(t0 + k * 32),
+                                    idesc_mx4<NV>(128, NT, NV ? 0 : 2 * (k & 1)), ca + 4 * g, cb + 4 * g, (i | k) != 0);
+            }
+            umma_commit_elected<false>(leader, smem_u32(empty) + 8 * stage, 0);
+            if (++stage == (uint32_t)ring) { stage = 0; phase ^= 1; }
+        }
+        umma_commit_elected<false>(leader, smem_u32(done), 0);
+    } else {
+        // ------------------------------------------------------------ tokens --
+        const int wk = warp - 2;
+        for (int i = wk; i < nkb; i += kWorkers) {
+            const uint32_t codes = smem_u32(sT) + i * NT * 128, scales = smem_u32(sST) + i * ST * kMx4TileBytes;
+            if (!p.x) stage_packed<NV>(p, kb0 + i, codes, scales, lane);
+            else if (p.x_type == kElemF32) stage_tokens<float, NV>(p, kb0 + i, codes, scales, lane);
+            else if (p.x_type == kElemF16) stage_tokens<__half, NV>(p, kb0 + i, codes, scales, lane);
+            else stage_tokens<bf16, NV>(p, kb0 + i, codes, scales, lane);
+            fence_proxy_async_smem();  // the products read this through the async proxy
+            mbar_arrive(smem_u32(&ready[i]));
+        }
+    }
+    // ------------------------------------------------------------- epilogue --
+    // every product has completed, or a wait has run out somewhere in this CTA
+    const bool got = mbar_wait(smem_u32(done), 0, abort_flag);
+    const bool ok = __syncthreads_and(got && *abort_flag == 0) != 0;
+    tc_fence_after();
+    if (warp >= 2 && warp < 6) {
+        // lane quadrant warp % 4: feature 32 (warp % 4) + lane
+        const int quad = warp & 3;
+        uint32_t r[32];
+        tmem_ld32(tmem + ((uint32_t)(quad * 32) << 16), r);  // (columns past NT: not read below)
+        tmem_ld_wait();
+#pragma unroll
+        for (int t = 0; t < NT; ++t) sum[t * 128 + quad * 32 + lane] = __uint_as_float(r[t]);
+    }
+    tc_fence_before();
+    if (nclu > 1) cluster_sync();
+    else __syncthreads();
+    if (warp >= 2 && ok) {
+        const int wk = warp - 2, f = (wk & 3) * 32 + lane, feat = tile * 128 + f;
+        const float bias = p.bias && feat < p.N ? __ldg(p.bias + feat) : 0.f;
+        const uint32_t own = smem_u32(sum);
+        // this CTA's tokens: rank, rank + nclu, ..., the two groups of four warps alternating
+        for (int t = (int)rank + (wk >> 2) * nclu; t < p.M; t += 2 * nclu) {
+            float acc = 0.f;
+            if (nclu == 1) {
+                acc = sum[t * 128 + f];
+            } else {
+                for (int c = 0; c < nclu; ++c) acc += ld_dsmem_f32(mapa_shared(own + (t * 128 + f) * 4, c));
+            }
+            float v = fmaf(p.alpha, acc, bias);
+            if (p.gelu) v = gelu_tok(v);
+            if (p.out) {
+                if (feat < p.N) {
+                    const size_t ro = (size_t)t * p.ld_res + feat, oo = (size_t)t * p.ld_out + feat;
+                    if (p.out_type == kElemF32) {
+                        if (p.res) v += __ldg(static_cast<const float *>(p.res) + ro);
+                        static_cast<float *>(p.out)[oo] = v;
+                    } else if (p.out_type == kElemF16) {
+                        if (p.res) v += __half2float(static_cast<const __half *>(p.res)[ro]);
+                        static_cast<__half *>(p.out)[oo] = __float2half_rn(v);
+                    } else {
+                        if (p.res) v += __bfloat162float(static_cast<const bf16 *>(p.res)[ro]);
+                        static_cast<bf16 *>(p.out)[oo] = __float2bfloat16_rn(v);
+                    }
+                }
+            } else {
+                // 4-bit result: a warp's 32 features are one block (mxfp4) or two (nvfp4)
+                if (feat >= p.N) v = 0.f;
+                uint32_t m = abs_bits(v);
+#pragma unroll
+                for (int o = 1; o < Mx4<NV>::kBlock; o <<= 1) m = umax(m, __shfl_xor_sync(0xffffffffu, m, o));
+                const Mx4Scale s = mx4_block_scale<NV>(m, p.q_ts, 6.0f * p.q_ts);
+                float y[8];
+                y[0] = __fmul_rn(v, s.mul);
+#pragma unroll
+                for (int j = 1; j < 8; ++j) y[j] = __shfl_down_sync(0xffffffffu, y[0], j);
+                const uint32_t q = s.zero ? 0u : cvt_e2m1x8(y);
+                const int pitch = mx4_code_pitch(p.N);
+                if ((lane & 7) == 0 && feat / 2 < pitch) *reinterpret_cast<uint32_t *>(p.q + (size_t)t * pitch + feat / 2) = q;
+                if (lane % Mx4<NV>::kBlock == 0) {
+                    // (token t < 32: row t of the first row tile)
+                    const int blk = feat / Mx4<NV>::kBlock;
+                    p.q_scales[(size_t)(blk >> 2) * kMx4TileBytes + t * 16 + (blk & 3)] = (uint8_t)s.byte;
+                }
+            }
+        }
+    }
+    // a peer may still read this CTA's partial sums
+    if (nclu > 1) cluster_sync();
+    else __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tmem, P::COLS);
+    }
+    if (threadIdx.x == 0 && *abort_flag) set_status(p.status, kStatusTimeout);
+}
+
+template <bool NV, int NT>
+cudaError_t launch_tok(const Mx4TokArgs &a, int num_sms, cudaStream_t s) {
+    using P = TokPlan<NV, NT>;
+    const int stages = mx4_stages(a.K), pitch = mx4_code_pitch(a.K);
+    // a 4-bit result's scale tiles reach to a multiple of 256 columns
+    const int tiles = ((a.out ? a.N : mx4_stages(a.N) * kMx4StageCols) + 127) / 128;
+    int nclu = 1;
+    while (nclu < kMaxCluster && 2 * nclu <= stages &&
+           (2 * nclu * tiles <= num_sms || (stages + nclu - 1) / nclu > kMaxSlice))
+        nclu *= 2;
+    const int slice = (stages + nclu - 1) / nclu;
+    if (slice > kMaxSlice) return cudaErrorInvalidValue;
+    const int ring = slice < kMaxRing ? slice : kMaxRing;
+    CUtensorMap tmW, tmSW;
+    const uint64_t st = (uint64_t)((a.N + 127) / 128) * stages * P::ST;
+    if (make_tmap_u8(&tmW, a.w, a.N, pitch, 128, 128, true) || make_tmap_u8(&tmSW, a.w_scales, 2 * st, 256, 256, 2 * P::ST, false))
+        return cudaErrorInvalidValue;
+    static std::atomic<unsigned long long> done{0};
+    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(mx4_tokens_kernel<NV, NT>), P::smem(kMaxRing, kMaxSlice), done);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = nclu;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(tiles * nclu);
+    cfg.blockDim = dim3(kTokThreads);
+    cfg.dynamicSmemBytes = P::smem(ring, slice);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = nclu > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, mx4_tokens_kernel<NV, NT>, tmW, tmSW, a, ring, slice, nclu);
+}
+
+}  // namespace
+
+bool mx4_few_tokens(int rows, int K) {
+    return rows <= kMx4MaxTokens && mx4_stages(K) <= kMaxSlice * kMaxCluster;
+}
+
+cudaError_t launch_mx4_tokens(const Mx4TokArgs &a, int num_sms, cudaStream_t s) {
+    if (a.M < 1) return cudaSuccess;
+    if (a.M <= 16) return a.nv ? launch_tok<true, 16>(a, num_sms, s) : launch_tok<false, 16>(a, num_sms, s);
+    return a.nv ? launch_tok<true, 32>(a, num_sms, s) : launch_tok<false, 32>(a, num_sms, s);
+}
+
+}  // namespace albert
