@@ -129,8 +129,8 @@ int make_tmap_bf16(CUtensorMap *tm, const void *base, uint64_t rows, uint64_t co
 // Map of an E4M3 (byte) row-major [rows, cols] tensor with a {128, box_rows} box
 // and the 128-byte swizzle: the operands of the E4M3 GEMM variant.
 int make_tmap_e4m3(CUtensorMap *tm, const void *base, uint64_t rows, uint64_t cols, uint32_t box_rows);
-// Map of [rows, cols] elements of an ElemType, rows ld elements apart, with a 32x32
-// box: 16-bit types with the 64-byte swizzle, fp32 with the 128-byte swizzle.
+// Map of [rows, cols] elements of an ElemType, rows ld elements apart, with a box of
+// 32 rows of 64 bytes (32 16-bit or 16 fp32 columns) and the 64-byte swizzle.
 int make_tmap_tile32(CUtensorMap *tm, const void *base, int type, uint64_t rows, uint64_t cols, uint64_t ld);
 // Map of a byte row-major [rows, cols] tensor with a {box_cols, box_rows} box.
 int make_tmap_u8(CUtensorMap *tm, const void *base, uint64_t rows, uint64_t cols, uint32_t box_cols, uint32_t box_rows,
@@ -360,7 +360,7 @@ struct Mx4GemmArgs {
 };
 cudaError_t launch_mx4_gemm(const Mx4GemmArgs &a, int num_sms, cudaStream_t s, bool pdl);
 
-// The same for at most kMx4MaxTokens rows (mx4_few_tokens), which it quantizes itself
+// The same for at most kMx4MaxTokens rows, which it quantizes itself
 // when x is given (then a, a_scales are unused): one launch, no workspace.
 constexpr int kMx4MaxTokens = 32;
 struct Mx4TokArgs : Mx4GemmArgs {
@@ -370,7 +370,6 @@ struct Mx4TokArgs : Mx4GemmArgs {
     float x_ts;
     int vec_x;              // the rows are 16-byte aligned
 };
-bool mx4_few_tokens(int rows, int K);
 cudaError_t launch_mx4_tokens(const Mx4TokArgs &a, int num_sms, cudaStream_t s);
 
 // fp32 -> bf16 conversion of a parameter block.

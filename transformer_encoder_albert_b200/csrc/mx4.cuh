@@ -93,7 +93,7 @@ __device__ __forceinline__ Mx4Scale mx4_block_scale(uint32_t amax_bits, float ts
         s.byte = bad ? 0x7fu : (uint32_t)(c & 0xffu);
         s.zero = bad || s.byte == 0u;
         const float d = __fmul_rn(e4m3_value(s.byte), ts);
-        s.mul = s.zero ? 0.0f : __fdiv_rn(1.0f, d);
+        s.mul = __frcp_rn(s.zero ? 1.0f : d);  // = fl(1 / d); zero: the codes are dropped anyway
     }
     return s;
 }

@@ -120,7 +120,7 @@ int albert_mx4_layer_norm(const void *x, int x_type, long long ld_x, const float
 }
 
 size_t albert_mx4_linear_workspace_bytes(int rows, int k, int fmt) {
-    if (rows < 1 || !cols_ok(k) || !is_format(fmt) || mx4_few_tokens(rows, k)) return 0;
+    if (rows < 1 || !cols_ok(k) || !is_format(fmt) || rows <= kMx4MaxTokens) return 0;
     return up16(codes_bytes(rows, k)) + scales_bytes(rows, k, fmt == ALBERT_NVFP4);
 }
 
@@ -171,7 +171,7 @@ int albert_mx4_linear(const albert_mx4_linear_args *p, void *stream) {
     g.status = status;
     g.a = static_cast<const uint8_t *>(p->a_codes);
     g.a_scales = static_cast<const uint8_t *>(p->a_scales);
-    if (mx4_few_tokens(p->rows, p->k)) {
+    if (p->rows <= kMx4MaxTokens) {
         g.x = p->x;
         g.x_type = p->x_type;
         g.ld_x = p->ld_x;

@@ -4,24 +4,26 @@
 // codes with block scales (mx4.cuh), the products and the multiplication by both
 // scales on tcgen05 (kind::mxf4 / mxf4nvf4, block_scale), sums in fp32.
 //
-// Persistent, one CTA per SM, warp-specialized like the bf16 GEMM:
-//   warp 0     : TMA producer: per stage 256 columns of A and W (128-byte rows,
-//                128-byte swizzle) and their scale tiles (512 bytes per 128 rows and
-//                four blocks, plain);
-//   warp 1     : issues four products of K = 64 per stage;
-//   warp 10    : issues the copies of a stage's scale tiles to tensor memory, one
-//                stage ahead of the products (6 or 12 copies per stage at about 26
-//                cycles each would cost the products' warp more than half their time);
-//   warps 2..9 : epilogue, a lane quadrant each, two warps per quadrant taking
-//                alternate 32-column chunks; rows leave through a swizzled staging
-//                tile by TMA (or coalesced stores where the rows are not 16-byte
-//                aligned), 16-bit residual tiles arrive the same way a chunk ahead.
+// Persistent, one CTA per SM, warp-specialized:
+//   warp 0      : TMA producer: per stage 256 columns of A and W (128-byte rows,
+//                 128-byte swizzle) and their scale tiles (512 bytes per 128 rows and
+//                 four blocks, plain);
+//   warp 1      : issues four products of K = 64 per stage;
+//   warp 2      : issues the copies of a stage's scale tiles to tensor memory, one
+//                 stage ahead of the products (6 or 12 copies per stage at about 26
+//                 cycles each would cost the products' warp more than half their time);
+//   warps 4..19 : epilogue, four warps per lane quadrant, each every fourth 32-column
+//                 chunk (a chunk is some 190 dependent instructions: with two warps per
+//                 quadrant it took 1330 cycles, and K = 768 only gives a tile 1536);
+//                 rows leave through swizzled staging tiles by TMA (or coalesced stores
+//                 where they are not 16-byte aligned), 16-bit residual tiles arrive by
+//                 TMA a chunk ahead.
 // Two tile shapes:
 //   * a CTA pair per 256x256 tile (cta_group::2): each CTA stages 128 rows of A and of
 //     W and the scales of its A rows and of all W rows.  Two 256-column accumulators
 //     would fill tensor memory; they overlap by 96 columns, which leaves 96 for the
-//     scales (two stages).  The epilogue first reads the chunks that lie in the
-//     overlap into registers, so the next tile's products start after two loads.
+//     scales (two stages).  The epilogue's first chunks cover the overlap, so the next
+//     tile's products start once those are in registers.
 //   * one CTA per 128x128 tile, two separate accumulators, for work that would leave
 //     pairs idle.
 // Scale columns are written again only after the products that read them have
@@ -36,9 +38,10 @@
 namespace albert {
 namespace {
 
-constexpr int kEpiWarps = 8;
-constexpr int kThreads = 32 * (3 + kEpiWarps);
-constexpr int kStgBytes = 3 * 2048;    // staging per epilogue warp: three 16-bit 32x32 tiles
+constexpr int kEpiWarps = 16, kEpi0 = 4;  // epilogue warps, the first of them
+constexpr int kThreads = 32 * (kEpi0 + kEpiWarps);
+constexpr int kTile = 2048;               // a staging tile: 32 rows of 64 bytes
+constexpr int kStgBytes = 2 * kTile;      // per epilogue warp
 constexpr int kRowsBytes = 128 * 128;  // 128 rows x 256 columns of codes
 
 template <bool NV, bool PAIR>
@@ -49,11 +52,11 @@ struct Plan {
     static constexpr int SFA = ST * kMx4TileBytes;
     static constexpr int SFB = (TN / 128) * SFA;
     static constexpr int STAGE = 2 * kRowsBytes + SFA + SFB;  // bytes per CTA and stage
-    static constexpr int NST = NV ? 4 : 5;
+    static constexpr int NST = 4;
     static constexpr int ACC1 = PAIR ? 160 : 128;            // first column of the second accumulator
     static constexpr int SFCOL = PAIR ? 416 : 256;           // first scale column
     static constexpr int SFBUF = 4 * ST * (1 + TN / 128);    // scale columns per stage
-    static constexpr int PER = TN / 64;                      // 32-column chunks per epilogue warp
+    static constexpr int PER = TN / 128;                     // 32-column chunks per epilogue warp
     static constexpr int SMEM = 1024 + NST * STAGE + kEpiWarps * (kStgBytes + 256) + 512;
     static_assert(SFCOL + 2 * SFBUF <= 512, "tensor memory columns");
     static_assert(SMEM + 64 <= 232448, "shared memory per CTA, the wait limit included");
@@ -282,7 +285,7 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             umma_commit_elected<PAIR>(leader, smem_u32(c.drain), 1);
             mbar_wait_drain(smem_u32(c.drain), 0);
         }
-    } else if (warp == 2 + kEpiWarps) {
+    } else if (warp == 2) {
         // ------------------------------------------------------- scale copies --
         if (rank == 0) {
             const uint32_t leader = elect_leader();
@@ -318,37 +321,35 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             umma_commit_elected<PAIR>(leader, smem_u32(c.sdrain), 1);
             mbar_wait_drain(smem_u32(c.sdrain), 0);
         }
-    } else {
+    } else if (warp >= kEpi0) {
         // ---------------------------------------------------------- epilogue --
         constexpr int PER = P::PER;
-        const int ew = warp - 2, quad = warp & 3, half = ew >> 2;
+        const int ew = warp - kEpi0, quad = warp & 3, part = ew >> 2;
         float *bias_s = sBias + ew * 64;  // two chunks' biases
-        const uint32_t stg = smem_u32(sStg + ew * kStgBytes);
-        const uint32_t rstg = stg + 4096, rbar = smem_u32(&c.rbar[ew]);
+        const uint32_t stg = smem_u32(sStg + ew * kStgBytes), rbar = smem_u32(&c.rbar[ew]);
         const bool res = !QOUT && p.res != nullptr;
-        float bnext[PER];
-        uint32_t t = 0, rph = 0, stores = 0;
+        const bool f32 = p.out_type == kElemF32;
+        uint32_t t = 0, rph = 0, stores = 0, chunks = 0;
         bool res_pending = false;
         // this warp's i-th chunk of a tile: the first accumulator of a pair is read from its
         // upper end, the second from its lower end, so that the overlap comes first
-        auto chunk_of = [&](uint32_t tt, int i) { return (PAIR && (tt & 1) == 0) ? (TN / 32 - 2 + half) - 2 * i : half + 2 * i; };
-        auto bias_load = [&](long long u, uint32_t tt) {
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                const int col = (int)(u % n_sub) * TN + chunk_of(tt, i) * 32 + lane;
-                bnext[i] = (p.bias && col < p.N) ? __ldg(p.bias + col) : 0.f;
-            }
-        };
+        auto chunk_of = [&](uint32_t tt, int i) { return (PAIR && (tt & 1) == 0) ? (TN / 32 - 1 - part) - 4 * i : part + 4 * i; };
+        // residual tiles use the second staging tile, results then only the first
         auto res_issue = [&](long long u, uint32_t tt, int i) {
             if (lane == 0) {
-                mbar_arrive_expect_tx(rbar, 2048);
-                tma_load_2d(rstg, &tmRes, rbar, (int)(u % n_sub) * TN + chunk_of(tt, i) * 32,
+                mbar_arrive_expect_tx(rbar, kTile);
+                tma_load_2d(stg + kTile, &tmRes, rbar, (int)(u % n_sub) * TN + chunk_of(tt, i) * 32,
                             (int)(u / n_sub) * P::UM + (int)rank * 128 + quad * 32);
             }
             res_pending = true;
         };
+        auto bias_load = [&](long long u, uint32_t tt, int i) {
+            const int col = (int)(u % n_sub) * TN + chunk_of(tt, i) * 32 + lane;
+            return (p.bias && col < p.N) ? __ldg(p.bias + col) : 0.f;
+        };
+        float bnext = 0.f;
         if (slot < units) {
-            bias_load(slot, 0);
+            bnext = bias_load(slot, 0, 0);
             if (res && tma_res) res_issue(slot, 0, 0);
         }
         bool ok = true;
@@ -356,44 +357,38 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             const int m = (int)(u / n_sub), n = (int)(u % n_sub);
             const int row0 = m * P::UM + (int)rank * 128 + quad * 32, row = row0 + lane;
             const bool row_ok = row < n_rows;
-            float bcur[PER];
-#pragma unroll
-            for (int i = 0; i < PER; ++i) bcur[i] = bnext[i];
-            if (u + nslots < units) bias_load(u + nslots, t + 1);
             bool got = mbar_wait(smem_u32(&c.tfull[t & 1]), (t >> 1) & 1, c.abort_flag);
             if (!__all_sync(0xffffffffu, got)) break;
             tc_fence_after();
             const uint32_t tb = tmem + ((uint32_t)(quad * 32) << 16) + (t & 1) * P::ACC1;
-            uint32_t r[2][32];
-            tmem_ld32(tb + chunk_of(t, 0) * 32, r[0]);
-            tmem_ld32(tb + chunk_of(t, 1) * 32, r[1]);
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                // (the slot's readers, two chunks ago, have passed a __syncwarp since)
-                bias_s[(i & 1) * 32 + lane] = bcur[i];
+#pragma unroll 1
+            for (int i = 0; i < PER; ++i, ++chunks) {
+                const int ch = chunk_of(t, i);
+                uint32_t r[32];
+                tmem_ld32(tb + ch * 32, r);
+                float *bs = bias_s + (chunks & 1) * 32;  // (its readers, two chunks ago, have passed a __syncwarp since)
+                bs[lane] = bnext;
                 tmem_ld_wait();
-                if (i == (PAIR ? 0 : PER - 2)) {
-                    // pair: the overlap is in registers; else: the whole accumulator is
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if (PAIR) mbar_arrive_cluster(mapa_shared(smem_u32(&c.tfree[t & 1]), 0));
-                        else mbar_arrive(smem_u32(&c.tfree[t & 1]));
-                    }
-                }
+                if (i == 0) tc_fence_before();
                 __syncwarp();
-                const int col0 = n * TN + chunk_of(t, i) * 32;
+                if (i == 0 && lane == 0) {
+                    // pair: the overlap is in registers; else: the whole accumulator is
+                    if (PAIR) mbar_arrive_cluster(mapa_shared(smem_u32(&c.tfree[t & 1]), 0));
+                    else mbar_arrive(smem_u32(&c.tfree[t & 1]));
+                }
+                if (i + 1 < PER) bnext = bias_load(u, t, i + 1);
+                else if (u + nslots < units) bnext = bias_load(u + nslots, t + 1, 0);
+                const int col0 = n * TN + ch * 32;
                 const int left = p.N - col0;  // columns of this chunk that exist
                 float v[32];
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
-                    const float4 b = *reinterpret_cast<const float4 *>(bias_s + (i & 1) * 32 + 4 * q);
-                    v[4 * q] = fmaf(p.alpha, __uint_as_float(r[i & 1][4 * q]), b.x);
-                    v[4 * q + 1] = fmaf(p.alpha, __uint_as_float(r[i & 1][4 * q + 1]), b.y);
-                    v[4 * q + 2] = fmaf(p.alpha, __uint_as_float(r[i & 1][4 * q + 2]), b.z);
-                    v[4 * q + 3] = fmaf(p.alpha, __uint_as_float(r[i & 1][4 * q + 3]), b.w);
+                    const float4 b = *reinterpret_cast<const float4 *>(bs + 4 * q);
+                    v[4 * q] = fmaf(p.alpha, __uint_as_float(r[4 * q]), b.x);
+                    v[4 * q + 1] = fmaf(p.alpha, __uint_as_float(r[4 * q + 1]), b.y);
+                    v[4 * q + 2] = fmaf(p.alpha, __uint_as_float(r[4 * q + 2]), b.z);
+                    v[4 * q + 3] = fmaf(p.alpha, __uint_as_float(r[4 * q + 3]), b.w);
                 }
-                if (i + 2 < PER) tmem_ld32(tb + chunk_of(t, i + 2) * 32, r[i & 1]);
                 if (p.gelu) {
 #pragma unroll
                     for (int j = 0; j < 32; ++j) v[j] = gelu_exact(v[j]);
@@ -433,13 +428,13 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                     if (res) {
                         if (tma_res) {
                             bool rok = mbar_wait(rbar, rph, c.abort_flag);
-                            if (!__all_sync(0xffffffffu, rok)) { ok = false; tmem_ld_wait(); break; }
+                            if (!__all_sync(0xffffffffu, rok)) { ok = false; break; }
                             rph ^= 1;
                             res_pending = false;
                             const bool f16 = p.out_type == kElemF16;
 #pragma unroll
                             for (int q = 0; q < 4; ++q) {
-                                const uint4 w = ld_shared_u4(rstg + stg_off(lane, q));
+                                const uint4 w = ld_shared_u4(stg + kTile + stg_off(lane, q));
                                 const uint32_t w4[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
                                 for (int e = 0; e < 4; ++e) {
@@ -454,24 +449,23 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                         } else if (row_ok && left > 0) {
                             const size_t ro = (size_t)row * p.ld_res + col0;
                             const int cnt = left < 32 ? left : 32;
-                            if (p.out_type == kElemF32) add_row(static_cast<const float *>(p.res) + ro, cnt, vec_res, v);
+                            if (f32) add_row(static_cast<const float *>(p.res) + ro, cnt, vec_res, v);
                             else if (p.out_type == kElemF16) add_row(static_cast<const __half *>(p.res) + ro, cnt, vec_res, v);
                             else add_row(static_cast<const bf16 *>(p.res) + ro, cnt, vec_res, v);
                         }
                     }
-                    // the chunk as a 32x32 tile in shared memory: 16-bit rows of 64 bytes (two tiles
-                    // in turn, 64-byte swizzle), fp32 rows of 128 bytes (one tile, 128-byte swizzle)
-                    const bool f32 = p.out_type == kElemF32;
-                    const uint32_t tile = f32 ? stg : stg + (stores & 1) * 2048;
+                    // the chunk through shared memory: a 16-bit 32x32 tile, or two fp32 tiles of 16
+                    // columns (rows of 64 bytes, 64-byte swizzle)
+                    const uint32_t tile = f32 || (res && tma_res) ? stg : stg + (stores & 1) * kTile;
                     if (lane == 0) {
-                        if (f32) bulk_wait_read0();
+                        if (f32 || res) bulk_wait_read0();
                         else bulk_wait_read1();
                     }
                     __syncwarp();
                     if (f32) {
 #pragma unroll
                         for (int q = 0; q < 8; ++q)
-                            st_shared_u4(tile + lane * 128 + ((q ^ (lane & 7)) << 4),
+                            st_shared_u4(tile + (q >> 2) * kTile + stg_off(lane, q & 3),
                                          make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
                                                     __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3])));
                     } else if (p.out_type == kElemF16) {
@@ -491,22 +485,25 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                     if (tma_out && (row0 + 32 <= n_rows || n_rows == p.M)) {
                         fence_proxy_async_smem();
                         __syncwarp();
-                        if (lane == 0 && left > 0 && row0 < n_rows) {
-                            tma_store_2d(&tmOut, tile, col0, row0);
+                        if (lane == 0) {
+                            if (left > 0 && row0 < n_rows) {
+                                tma_store_2d(&tmOut, tile, col0, row0);
+                                if (f32 && left > 16) tma_store_2d(&tmOut, tile + kTile, col0 + 16, row0);
+                            }
+                            bulk_commit();
                         }
-                        if (lane == 0) bulk_commit();
                         ++stores;
                     } else {
                         __syncwarp();
                         if (lane < left) {
                             const int rows = n_rows - row0 < 32 ? n_rows - row0 : 32;
-                            const uint32_t sh = (lane & 7) * 2;
                             for (int y = 0; y < rows; ++y) {
                                 const size_t o = (size_t)(row0 + y) * p.ld_out + col0 + lane;
                                 if (f32)
-                                    static_cast<uint32_t *>(p.out)[o] = ld_shared_u1(tile + y * 128 + (((lane >> 2) ^ (y & 7)) << 4) + (lane & 3) * 4);
+                                    static_cast<uint32_t *>(p.out)[o] =
+                                        ld_shared_u1(tile + (lane >> 4) * kTile + stg_off(y, (lane >> 2) & 3) + (lane & 3) * 4);
                                 else
-                                    static_cast<uint16_t *>(p.out)[o] = ld_shared_u16(tile + stg_off(y, lane >> 3) + sh);
+                                    static_cast<uint16_t *>(p.out)[o] = ld_shared_u16(tile + stg_off(y, lane >> 3) + (lane & 7) * 2);
                             }
                         }
                         __syncwarp();

@@ -8,10 +8,11 @@
 // SMs without work, and adds the partial sums over distributed shared memory in rank
 // order (no atomics, the same bits every time, no workspace).
 //   warp 0      : TMA ring of weight stages (all in flight before any product);
-//   warp 1      : scale copies and products.  A ring stage has scale columns of its
-//                 own in tensor memory, so the stage's barrier guards them too;
-//   warps 2..9  : quantize (or copy) the tokens of the slice, a stage per warp in turn,
-//                 into shared memory as the second operand, then the epilogue.
+//   warp 10     : copies a stage's scales to tensor memory.  A ring stage has scale
+//                 columns of its own there, so the stage's barrier guards them too;
+//   warp 1      : products;
+//   warps 2..9  : quantize (or copy) the tokens into a stage's second operand (warp 2 + i
+//                 stage i of the ring), then the epilogue.
 // Rows of the token operand past the last token are never written: they only reach
 // result columns that nobody reads.
 #include <type_traits>
@@ -24,17 +25,16 @@ namespace albert {
 namespace {
 
 constexpr int kWorkers = 8;
-constexpr int kTokThreads = 32 * (2 + kWorkers);
+constexpr int kTokThreads = 32 * (3 + kWorkers);
 constexpr int kWBytes = 128 * 128;   // codes of a weight stage
-constexpr int kMaxRing = 6;
-constexpr int kMaxSlice = 16;        // stages of a CTA's K slice
+constexpr int kMaxRing = 6;            // at most kWorkers
 constexpr int kMaxCluster = 8;
 
 template <bool NV, int NT>
 struct TokPlan {
     static constexpr int ST = Mx4<NV>::kStageTiles;
-    static constexpr int RING = kWBytes + ST * kMx4TileBytes;           // bytes of a weight stage
-    static constexpr int TOK = NT * 128 + ST * kMx4TileBytes;           // bytes of a token stage
+    static constexpr int RING = kWBytes + ST * kMx4TileBytes;           // bytes of a stage's weights
+    static constexpr int TOK = NT * 128 + ST * kMx4TileBytes;           // and of its tokens
     static constexpr int SFCOLS = 8 * ST;                               // scale columns of a ring stage
     static constexpr int COLS = NT + kMaxRing * SFCOLS <= 128 ? 128 : 256;
     static_assert(NT + kMaxRing * SFCOLS <= 256, "tensor memory columns");
@@ -43,8 +43,8 @@ struct TokPlan {
     // memory (228 KB for 512 columns, 1 KB of each CTA's being the system's), and what
     // fits an SM by shared memory also fits it by tensor memory.
     static constexpr int kLeast = 233472 / 512 * COLS - 1024 - 64;
-    static int smem(int ring, int slice) {
-        const int n = 1024 + ring * RING + slice * TOK + NT * 128 * 4 + 512;
+    static int smem(int ring) {
+        const int n = 1024 + ring * (RING + TOK) + NT * 128 * 4 + 512;
         return n > kLeast ? n : kLeast;
     }
 };
@@ -65,25 +65,34 @@ __device__ __forceinline__ float gelu_tok(float x) {
     return __fdividef(x, 1.0f + ex2_approx(k * x * fmaf(0.044715f * x, x, 1.0f)));
 }
 
-// One 256-column stage of the tokens, by a warp: a half-warp per row, 16 columns a lane.
-template <typename T, bool NV>
-__device__ __forceinline__ void stage_tokens(const Mx4TokArgs &p, int kb, uint32_t codes, uint32_t scales, int lane) {
-    const int sub = lane & 15, half = lane >> 4, col = kb * kMx4StageCols + sub * 16;
-    for (int r0 = 0; r0 < p.M; r0 += 2) {
-        const int row = r0 + half;
+// Rows r0 .. r0 + 2 PAIRS - 1 of a 256-column stage of the tokens, by a warp: a
+// half-warp per row, 16 columns a lane; the row pairs' loads and chains of dependent
+// instructions overlap (rows past the last read as 0 and are not stored).
+template <typename T, bool NV, int PAIRS>
+__device__ __forceinline__ void stage_rows(const Mx4TokArgs &p, int r0, int col, uint32_t codes, uint32_t scales, int sub,
+                                           int half) {
+    Raw8<T> a[PAIRS], b[PAIRS];
+#pragma unroll
+    for (int i = 0; i < PAIRS; ++i) {
+        const int row = r0 + 2 * i + half;
         const T *src = static_cast<const T *>(p.x) + (size_t)row * p.ld_x + col;
         const int n = row < p.M ? p.K - col : 0;
-        const Raw8<T> a = load_raw8<T>(src, n, p.vec_x != 0), b = load_raw8<T>(src + 8, n - 8, p.vec_x != 0);
-        uint32_t m = umax(raw8_amax<T>(a), raw8_amax<T>(b));
+        a[i] = load_raw8<T>(src, n, p.vec_x != 0);
+        b[i] = load_raw8<T>(src + 8, n - 8, p.vec_x != 0);
+    }
+#pragma unroll
+    for (int i = 0; i < PAIRS; ++i) {
+        const int row = r0 + 2 * i + half;
+        uint32_t m = umax(raw8_amax<T>(a[i]), raw8_amax<T>(b[i]));
         if constexpr (!NV) m = umax(m, __shfl_xor_sync(0xffffffffu, m, 1));
         const Mx4Scale s = mx4_block_scale<NV>(amax_f32_bits<T>(m), p.x_ts, 6.0f * p.x_ts);
         float v[8], u[8];
-        raw8_values<T>(a, v);
-        raw8_values<T>(b, u);
+        raw8_values<T>(a[i], v);
+        raw8_values<T>(b[i], u);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            v[i] = __fmul_rn(v[i], s.mul);
-            u[i] = __fmul_rn(u[i], s.mul);
+        for (int e = 0; e < 8; ++e) {
+            v[e] = __fmul_rn(v[e], s.mul);
+            u[e] = __fmul_rn(u[e], s.mul);
         }
         const uint2 q = s.zero ? make_uint2(0, 0) : make_uint2(cvt_e2m1x8(v), cvt_e2m1x8(u));
         constexpr int kLanes = NV ? 1 : 2, kTileLanes = 4 * kLanes;
@@ -95,6 +104,15 @@ __device__ __forceinline__ void stage_tokens(const Mx4TokArgs &p, int kb, uint32
             st_shared_u2(codes + row * 128 + (((sub >> 1) ^ (row & 7)) << 4) + (sub & 1) * 8, q);
             if (sub % kTileLanes == 0) st_shared_u1(scales + (sub / kTileLanes) * kMx4TileBytes + row * 16, word);
         }
+    }
+}
+template <typename T, bool NV>
+__device__ __forceinline__ void stage_tokens(const Mx4TokArgs &p, int kb, uint32_t codes, uint32_t scales, int lane) {
+    const int sub = lane & 15, half = lane >> 4, col = kb * kMx4StageCols + sub * 16;
+    if (p.M <= 2) {
+        stage_rows<T, NV, 1>(p, 0, col, codes, scales, sub, half);
+    } else {
+        for (int r0 = 0; r0 < p.M; r0 += 8) stage_rows<T, NV, 4>(p, r0, col, codes, scales, sub, half);
     }
 }
 template <bool NV>
@@ -116,16 +134,16 @@ __device__ __forceinline__ void stage_packed(const Mx4TokArgs &p, int kb, uint32
 template <bool NV, int NT>
 __global__ void __launch_bounds__(kTokThreads)
 mx4_tokens_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmSW, const Mx4TokArgs p,
-                  int ring, int slice_cap, int nclu) {
+                  int ring, int nclu) {
     using P = TokPlan<NV, NT>;
     constexpr int ST = P::ST;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *sW = base, *sT = sW + ring * kWBytes;                              // codes: weights, tokens
-    uint8_t *sSW = sT + slice_cap * NT * 128, *sST = sSW + ring * ST * kMx4TileBytes;  // scale tiles
-    float *sum = reinterpret_cast<float *>(sST + slice_cap * ST * kMx4TileBytes);      // [NT][128] partial sums
+    uint8_t *sSW = sT + ring * NT * 128, *sST = sSW + ring * ST * kMx4TileBytes;  // scale tiles
+    float *sum = reinterpret_cast<float *>(sST + ring * ST * kMx4TileBytes);      // [NT][128] partial sums
     uint64_t *bars = reinterpret_cast<uint64_t *>(sum + NT * 128);
-    uint64_t *full = bars, *empty = bars + kMaxRing, *ready = bars + 2 * kMaxRing, *done = ready + kMaxSlice;
+    uint64_t *full = bars, *empty = bars + kMaxRing, *ready = bars + 2 * kMaxRing, *scaled = bars + 3 * kMaxRing, *done = bars + 4 * kMaxRing;
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
@@ -142,9 +160,10 @@ mx4_tokens_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
         for (int i = 0; i < ring; ++i) {
             mbar_init(smem_u32(&full[i]), 1);
             mbar_init(smem_u32(&empty[i]), 1);
+            mbar_init(smem_u32(&ready[i]), 32);
+            mbar_init(smem_u32(&scaled[i]), 1);
         }
-        for (int i = 0; i < nkb; ++i) mbar_init(smem_u32(&ready[i]), 32);
-        mbar_init(smem_u32(done), 1);
+        mbar_init(smem_u32(done), 2);
         fence_mbar_init();
     }
     if (warp == 1) {
@@ -177,44 +196,58 @@ mx4_tokens_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
                 }
         }
         __syncwarp();
-    } else if (warp == 1) {
+    } else if (warp == 1 || warp == 2 + kWorkers) {
         const uint32_t leader = elect_leader();
         auto wait = [&](uint64_t *bar, uint32_t parity) {
             return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, abort_flag)) != 0;
         };
         uint32_t stage = 0, phase = 0;
         for (int i = 0; i < nkb; ++i) {
-            if (!wait(&ready[i], 0) || !wait(&full[stage], phase)) break;
-            tc_fence_after();
-            const uint32_t w0 = smem_u32(sW) + stage * kWBytes, t0 = smem_u32(sT) + i * NT * 128;
-            const uint32_t fw = smem_u32(sSW) + stage * ST * kMx4TileBytes, ft = smem_u32(sST) + i * ST * kMx4TileBytes;
+            // (both warps: what the copies read, the products read too)
+            if (!wait(&ready[stage], phase) || !wait(&full[stage], phase)) break;
             const uint32_t ca = tmem + NT + stage * P::SFCOLS, cb = ca + 4 * ST;
+            if (warp == 1) {
+                if (!wait(&scaled[stage], phase)) break;
+                tc_fence_after();
+                const uint32_t w0 = smem_u32(sW) + stage * kWBytes, t0 = smem_u32(sT) + stage * NT * 128;
 #pragma unroll
-            for (int g = 0; g < ST; ++g) {
-                tmem_cp_scales<false>(leader, ca + 4 * g, scale_tile_desc(fw + g * kMx4TileBytes));
-                tmem_cp_scales<false>(leader, cb + 4 * g, scale_tile_desc(ft + g * kMx4TileBytes));
-            }
+                for (int k = 0; k < 4; ++k) {
+                    const int g = NV ? k : k >> 1;
+                    umma_mx4<NV, false>(leader, tmem, sw128_kmajor_desc(w0 + k * 32), sw128_kmajor_desc(t0 + k * 32),
+                                        idesc_mx4<NV>(128, NT, NV ? 0 : 2 * (k & 1)), ca + 4 * g, cb + 4 * g, (i | k) != 0);
+                }
+                umma_commit_elected<false>(leader, smem_u32(empty) + 8 * stage, 0);
+            } else {
+                tc_fence_after();
+                const uint32_t fw = smem_u32(sSW) + stage * ST * kMx4TileBytes, ft = smem_u32(sST) + stage * ST * kMx4TileBytes;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const int g = NV ? k : k >> 1;
-                umma_mx4<NV, false>(leader, tmem, sw128_kmajor_desc(w0 + k * 32), sw128_kmajor_desc(t0 + k * 32),
-                                    idesc_mx4<NV>(128, NT, NV ? 0 : 2 * (k & 1)), ca + 4 * g, cb + 4 * g, (i | k) != 0);
+                for (int g = 0; g < ST; ++g) {
+                    tmem_cp_scales<false>(leader, ca + 4 * g, scale_tile_desc(fw + g * kMx4TileBytes));
+                    tmem_cp_scales<false>(leader, cb + 4 * g, scale_tile_desc(ft + g * kMx4TileBytes));
+                }
+                umma_commit_elected<false>(leader, smem_u32(scaled) + 8 * stage, 0);
             }
-            umma_commit_elected<false>(leader, smem_u32(empty) + 8 * stage, 0);
             if (++stage == (uint32_t)ring) { stage = 0; phase ^= 1; }
         }
+        // (after a wait that ran out, copies of scales may still be in flight: the CTA's memory
+        // must outlast them)
         umma_commit_elected<false>(leader, smem_u32(done), 0);
     } else {
         // ------------------------------------------------------------ tokens --
         const int wk = warp - 2;
-        for (int i = wk; i < nkb; i += kWorkers) {
-            const uint32_t codes = smem_u32(sT) + i * NT * 128, scales = smem_u32(sST) + i * ST * kMx4TileBytes;
+        // warp `stage` fills that ring stage every time, so that it never waits for a phase
+        // two ahead of the barrier's (more warps than stages would)
+        const int stage = wk;
+        uint32_t phase = 1;
+        for (int i = wk; wk < ring && i < nkb; i += ring, phase ^= 1) {
+            if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&empty[stage]), phase, abort_flag))) break;
+            const uint32_t codes = smem_u32(sT) + stage * NT * 128, scales = smem_u32(sST) + stage * ST * kMx4TileBytes;
             if (!p.x) stage_packed<NV>(p, kb0 + i, codes, scales, lane);
             else if (p.x_type == kElemF32) stage_tokens<float, NV>(p, kb0 + i, codes, scales, lane);
             else if (p.x_type == kElemF16) stage_tokens<__half, NV>(p, kb0 + i, codes, scales, lane);
             else stage_tokens<bf16, NV>(p, kb0 + i, codes, scales, lane);
             fence_proxy_async_smem();  // the products read this through the async proxy
-            mbar_arrive(smem_u32(&ready[i]));
+            mbar_arrive(smem_u32(&ready[stage]));
         }
     }
     // ------------------------------------------------------------- epilogue --
@@ -234,7 +267,7 @@ mx4_tokens_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
     tc_fence_before();
     if (nclu > 1) cluster_sync();
     else __syncthreads();
-    if (warp >= 2 && ok) {
+    if (warp >= 2 && warp < 2 + kWorkers && ok) {
         const int wk = warp - 2, f = (wk & 3) * 32 + lane, feat = tile * 128 + f;
         const float bias = p.bias && feat < p.N ? __ldg(p.bias + feat) : 0.f;
         const uint32_t own = smem_u32(sum);
@@ -301,18 +334,15 @@ cudaError_t launch_tok(const Mx4TokArgs &a, int num_sms, cudaStream_t s) {
     // a 4-bit result's scale tiles reach to a multiple of 256 columns
     const int tiles = ((a.out ? a.N : mx4_stages(a.N) * kMx4StageCols) + 127) / 128;
     int nclu = 1;
-    while (nclu < kMaxCluster && 2 * nclu <= stages &&
-           (2 * nclu * tiles <= num_sms || (stages + nclu - 1) / nclu > kMaxSlice))
-        nclu *= 2;
+    while (nclu < kMaxCluster && 2 * nclu <= stages && 2 * nclu * tiles <= num_sms) nclu *= 2;
     const int slice = (stages + nclu - 1) / nclu;
-    if (slice > kMaxSlice) return cudaErrorInvalidValue;
     const int ring = slice < kMaxRing ? slice : kMaxRing;
     CUtensorMap tmW, tmSW;
     const uint64_t st = (uint64_t)((a.N + 127) / 128) * stages * P::ST;
     if (make_tmap_u8(&tmW, a.w, a.N, pitch, 128, 128, true) || make_tmap_u8(&tmSW, a.w_scales, 2 * st, 256, 256, 2 * P::ST, false))
         return cudaErrorInvalidValue;
     static std::atomic<unsigned long long> done{0};
-    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(mx4_tokens_kernel<NV, NT>), P::smem(kMaxRing, kMaxSlice), done);
+    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(mx4_tokens_kernel<NV, NT>), P::smem(kMaxRing), done);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
@@ -322,18 +352,14 @@ cudaError_t launch_tok(const Mx4TokArgs &a, int num_sms, cudaStream_t s) {
     attr[0].val.clusterDim.z = 1;
     cfg.gridDim = dim3(tiles * nclu);
     cfg.blockDim = dim3(kTokThreads);
-    cfg.dynamicSmemBytes = P::smem(ring, slice);
+    cfg.dynamicSmemBytes = P::smem(ring);
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = nclu > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, mx4_tokens_kernel<NV, NT>, tmW, tmSW, a, ring, slice, nclu);
+    return cudaLaunchKernelEx(&cfg, mx4_tokens_kernel<NV, NT>, tmW, tmSW, a, ring, nclu);
 }
 
 }  // namespace
-
-bool mx4_few_tokens(int rows, int K) {
-    return rows <= kMx4MaxTokens && mx4_stages(K) <= kMaxSlice * kMaxCluster;
-}
 
 cudaError_t launch_mx4_tokens(const Mx4TokArgs &a, int num_sms, cudaStream_t s) {
     if (a.M < 1) return cudaSuccess;
