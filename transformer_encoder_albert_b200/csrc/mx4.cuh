@@ -13,6 +13,10 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
+#include "sm100_ptx.cuh"
+
 namespace albert {
 
 // Storage geometry.  A scale tile holds 128 rows x 4 blocks (512 bytes): byte
@@ -192,6 +196,28 @@ __device__ __forceinline__ void store8(T *p, int n, bool vec, const float (&v)[8
         for (int i = 0; i < 8; ++i)
             if (i < n) p[i] = from_f32<T>(v[i]);
     }
+}
+
+// max(|a|, |b|, |c|), NaN if one is.
+__device__ __forceinline__ float fmax3_abs_nan(float a, float b, float c) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// GELU_tanh of a pair: x / (1 + e), e = exp(-2u), u = sqrt(2/pi) (x + 0.044715 x^3).  The
+// two quotients share one reciprocal, 1 / ((1 + e0)(1 + e1)): three special-function
+// operations for two values instead of four (they set the pace: 16 lanes per clock and
+// SM).  The exponent stops at 63, so that the product stays finite; the value there is
+// x 2^-63.  Relative error a few 2^-23 plus 2^-23 |2u| from the exponential's argument.
+__device__ __forceinline__ uint64_t gelu_f2(uint64_t x) {
+    const float k0 = -2.0f * 0.7978845608028654f * 1.4426950408889634f, k1 = k0 * 0.044715f;
+    const float2 t = f2_split(f2_mul(x, f2_fma(f2_mul(x, x), f2_make(k1, k1), f2_make(k0, k0))));
+    const uint64_t d = f2_add(f2_make(ex2_approx(fminf(t.x, 63.0f)), ex2_approx(fminf(t.y, 63.0f))), f2_make(1.0f, 1.0f));
+    const float2 df = f2_split(d);
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(df.x * df.y));
+    return f2_mul(f2_mul(x, f2_make(df.y, df.x)), f2_make(r, r));
 }
 
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }

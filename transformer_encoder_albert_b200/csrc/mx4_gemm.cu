@@ -70,14 +70,6 @@ struct Ctrl {
     int *misc;
 };
 
-// GELU_tanh(x) = x / (1 + exp(-2u)), u = sqrt(2/pi) (x + 0.044715 x^3): relative
-// error a few 2^-23 plus 2^-23 |2u| of the exponential's argument.
-__device__ __forceinline__ float gelu_exact(float x) {
-    const float k = -2.0f * 0.7978845608028654f * 1.4426950408889634f;
-    const float e = ex2_approx(k * x * fmaf(0.044715f * x, x, 1.0f));
-    return __fdividef(x, 1.0f + e);
-}
-
 template <typename T>
 __device__ __forceinline__ void add_row(const T *p, int n, bool vec, float (&v)[32]) {
 #pragma unroll
@@ -156,7 +148,7 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             mbar_init(smem_u32(&c.empty[i]), 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&c.sfull[i]), 1);
+            mbar_init(smem_u32(&c.sfull[i]), 2);
             mbar_init(smem_u32(&c.tfull[i]), 1);
             mbar_init(smem_u32(&c.tfree[i]), (PAIR ? 2 : 1) * kEpiWarps);
         }
@@ -251,7 +243,7 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             auto wait = [&](uint64_t *bar, uint32_t parity) {
                 return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, c.abort_flag)) != 0;
             };
-            uint32_t stage = 0, phase = 0, t = 0;  // t: tiles issued by this CTA
+            uint32_t stage = 0, t = 0;  // t: tiles issued by this CTA
             uint32_t it = 0;                       // stages consumed
             bool ok = true;
             for (long long u = slot; u < units && ok; u += nslots, ++t) {
@@ -263,8 +255,9 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 }
                 const uint32_t d = tmem + (t & 1) * P::ACC1;
                 for (int kb = 0; kb < kblocks; ++kb, ++it) {
-                    // operands in shared memory, scales in tensor memory
-                    if (!wait(&c.full[stage], phase) || !wait(&c.sfull[it & 1], (it >> 1) & 1)) { ok = false; break; }
+                    // scales in tensor memory, operands in shared memory: the scale warp, which has
+                    // waited for the stage, arrives on the same barrier as its copies
+                    if (!wait(&c.sfull[it & 1], (it >> 1) & 1)) { ok = false; break; }
                     tc_fence_after();
                     const uint32_t a0 = smem_u32(sA) + stage * kRowsBytes, b0 = smem_u32(sB) + stage * kRowsBytes;
                     const uint32_t ca = tmem + P::SFCOL + (it & 1) * P::SFBUF, cb = ca + 4 * ST;
@@ -277,7 +270,7 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                                            ca + 4 * g, cb + g * (TN / 128) * 4, (kb | k) != 0);
                     }
                     umma_commit_elected<PAIR>(leader, smem_u32(c.empty) + 8 * stage, 3);
-                    if (++stage == NST) { stage = 0; phase ^= 1; }
+                    if (++stage == NST) stage = 0;
                 }
                 if (!ok) break;
                 umma_commit_elected<PAIR>(leader, smem_u32(&c.tfull[t & 1]), 3);
@@ -315,6 +308,7 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                                                  scale_tile_desc(fs + h * P::SFA + g * kMx4TileBytes));
                     }
                     umma_commit_elected<PAIR>(leader, smem_u32(&c.sfull[it & 1]), 1);
+                    if (lane == 0) mbar_arrive(smem_u32(&c.sfull[it & 1]));
                     if (++stage == NST) { stage = 0; phase ^= 1; }
                 }
             }
@@ -380,38 +374,52 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 else if (u + nslots < units) bnext = bias_load(u + nslots, t + 1, 0);
                 const int col0 = n * TN + ch * 32;
                 const int left = p.N - col0;  // columns of this chunk that exist
-                float v[32];
+                uint64_t v2[16];  // columns col0 + 2j, col0 + 2j + 1
+                const uint64_t alpha2 = f2_make(p.alpha, p.alpha);
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
                     const float4 b = *reinterpret_cast<const float4 *>(bs + 4 * q);
-                    v[4 * q] = fmaf(p.alpha, __uint_as_float(r[4 * q]), b.x);
-                    v[4 * q + 1] = fmaf(p.alpha, __uint_as_float(r[4 * q + 1]), b.y);
-                    v[4 * q + 2] = fmaf(p.alpha, __uint_as_float(r[4 * q + 2]), b.z);
-                    v[4 * q + 3] = fmaf(p.alpha, __uint_as_float(r[4 * q + 3]), b.w);
+                    v2[2 * q] = f2_fma(alpha2, f2_make_u(r[4 * q], r[4 * q + 1]), f2_make(b.x, b.y));
+                    v2[2 * q + 1] = f2_fma(alpha2, f2_make_u(r[4 * q + 2], r[4 * q + 3]), f2_make(b.z, b.w));
                 }
                 if (p.gelu) {
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) v[j] = gelu_exact(v[j]);
+                    for (int j = 0; j < 16; ++j) v2[j] = gelu_f2(v2[j]);
+                }
+                float v[32];
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const float2 f = f2_split(v2[j]);
+                    v[2 * j] = f.x;
+                    v[2 * j + 1] = f.y;
                 }
                 if constexpr (QOUT) {
                     constexpr int kB = Mx4<NV>::kBlock, kNB = 32 / kB;
                     const int pitch = mx4_code_pitch(p.N), tiles = mx4_stages(p.N) * ST;
                     uint32_t bytes = 0, q[4] = {};
+                    if (left < 32) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (j >= left) v[j] = 0.f;
+                    }
 #pragma unroll
                     for (int b = 0; b < kNB; ++b) {
-                        uint32_t mx = 0;
+                        float mx = fabsf(v[b * kB]);
 #pragma unroll
-                        for (int j = 0; j < kB; ++j) {
-                            if (b * kB + j >= left) v[b * kB + j] = 0.f;
-                            mx = umax(mx, abs_bits(v[b * kB + j]));
-                        }
-                        const Mx4Scale s = mx4_block_scale<NV>(mx, p.q_ts, 6.0f * p.q_ts);
+                        for (int j = 1; j + 1 < kB; j += 2) mx = fmax3_abs_nan(mx, v[b * kB + j], v[b * kB + j + 1]);
+                        mx = fmax3_abs_nan(mx, v[b * kB + kB - 1], 0.f);
+                        const Mx4Scale s = mx4_block_scale<NV>(abs_bits(mx), p.q_ts, 6.0f * p.q_ts);
+                        const uint64_t mul2 = f2_make(s.mul, s.mul);
                         bytes |= s.byte << (8 * b);
 #pragma unroll
                         for (int j = 0; j < kB; j += 8) {
                             float y[8];
 #pragma unroll
-                            for (int e = 0; e < 8; ++e) y[e] = __fmul_rn(v[b * kB + j + e], s.mul);
+                            for (int e = 0; e < 8; e += 2) {
+                                const float2 f = f2_split(f2_mul(f2_make(v[b * kB + j + e], v[b * kB + j + e + 1]), mul2));
+                                y[e] = f.x;
+                                y[e + 1] = f.y;
+                            }
                             q[(b * kB + j) / 8] = s.zero ? 0u : cvt_e2m1x8(y);
                         }
                     }

@@ -60,11 +60,6 @@ __device__ __forceinline__ void st_shared_u2(uint32_t a, uint2 v) {
 __device__ __forceinline__ void st_shared_u1(uint32_t a, uint32_t v) {
     asm volatile("st.shared.b32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
-__device__ __forceinline__ float gelu_tok(float x) {
-    const float k = -2.0f * 0.7978845608028654f * 1.4426950408889634f;
-    return __fdividef(x, 1.0f + ex2_approx(k * x * fmaf(0.044715f * x, x, 1.0f)));
-}
-
 // Rows r0 .. r0 + 2 PAIRS - 1 of a 256-column stage of the tokens, by a warp: a
 // half-warp per row, 16 columns a lane; the row pairs' loads and chains of dependent
 // instructions overlap (rows past the last read as 0 and are not stored).
@@ -280,7 +275,7 @@ mx4_tokens_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
                 for (int c = 0; c < nclu; ++c) acc += ld_dsmem_f32(mapa_shared(own + (t * 128 + f) * 4, c));
             }
             float v = fmaf(p.alpha, acc, bias);
-            if (p.gelu) v = gelu_tok(v);
+            if (p.gelu) v = f2_split(gelu_f2(f2_make(v, 0.f))).x;
             if (p.out) {
                 if (feat < p.N) {
                     const size_t ro = (size_t)t * p.ld_res + feat, oo = (size_t)t * p.ld_out + feat;
