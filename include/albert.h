@@ -65,7 +65,11 @@ extern "C" {
                           token, weights per output channel), everything else as
                           ALBERT_BF16; see albert_test_quant_e4m3               */
 
-/* ---- microscaled 4-bit formats (see albert_mx4_quantize) ---- */
+/* Microscaled 4-bit formats (albert_mx4_quantize); as the precision of a handle:
+   the four layer GEMMs on 4-bit operands (weights quantized at creation, the
+   activations in each forward), LayerNorms in fp32 from bf16 rows, everything
+   else as ALBERT_BF16.  ALBERT_NVFP4's activations have the tensor scale 1/32
+   (magnitudes up to 84). */
 #define ALBERT_MXFP4 3 /* E2M1 values, blocks of 32, power-of-two scales (E8M0)  */
 #define ALBERT_NVFP4 4 /* E2M1 values, blocks of 16, E4M3 scales times one fp32
                           factor per tensor                                      */
@@ -92,7 +96,7 @@ typedef struct {
     int max_pos;     /* rows of the position table, <= 512              */
     int n_types;     /* rows of the token-type table (type 0 is used)   */
     int out_dim;     /* 512, or 0 for no final projection               */
-    int dtype;       /* ALBERT_BF16 or ALBERT_FP32                      */
+    int dtype;       /* ALBERT_BF16, _FP32, _FP8, _MXFP4 or _NVFP4      */
     int max_tokens;  /* workspace capacity in rows (>= 1)               */
     int pack;        /* albert_forward: 1 = pack valid tokens by length
                         (the GEMMs run on sum(L_b) rows), 0 = run on all B*T
@@ -140,7 +144,7 @@ int albert_create(const albert_weights *w, const albert_config *cfg, albert_hand
 
 /* Padded batch.  ids: [B, T] int64 (device); mask: [B, T] uint8 (device),
  * 1 = token, each row a non-empty prefix of ones; out: [B, T, D] (device),
- * D = out_dim or hidden, bf16 for ALBERT_BF16 and fp32 for ALBERT_FP32.
+ * D = out_dim or hidden, fp32 for ALBERT_FP32, else bf16.
  * Rows at padding slots are written as zeros.  Ids at padding slots are not
  * read for the result and may hold anything.  Asynchronous on `stream`.
  * Host errors: NULL pointers, B < 1, T < 1, T > max_pos, B*T > max_tokens. */

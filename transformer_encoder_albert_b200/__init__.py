@@ -20,7 +20,7 @@ LIB_PATH = os.path.join(PKG, "libalbert_b200.so")
 
 ALBERT_OK = 0
 ALBERT_BF16, ALBERT_FP32, ALBERT_FP8, ALBERT_MXFP4, ALBERT_NVFP4, ALBERT_FP16 = 0, 1, 2, 3, 4, 5
-DTYPES = {"bf16": ALBERT_BF16, "fp32": ALBERT_FP32, "fp8": ALBERT_FP8}
+DTYPES = {"bf16": ALBERT_BF16, "fp32": ALBERT_FP32, "fp8": ALBERT_FP8, "mxfp4": ALBERT_MXFP4, "nvfp4": ALBERT_NVFP4}
 STATUS_NAMES = {
     0: "ALBERT_OK", 1: "ALBERT_ERR_NULL", 2: "ALBERT_ERR_CONFIG", 3: "ALBERT_ERR_SHAPE",
     4: "ALBERT_ERR_ID", 5: "ALBERT_ERR_MASK", 6: "ALBERT_ERR_SEQLENS", 7: "ALBERT_ERR_CUDA",
@@ -226,7 +226,8 @@ def albert_destroy(h: int) -> None:
 # --------------------------------------------------------- convenience class --
 
 class Encoder:
-    """Owns one library handle.  Outputs are bf16 (dtype "bf16") or fp32 tensors."""
+    """Owns one library handle.  Outputs are fp32 tensors for dtype "fp32", else bf16
+    (dtypes "bf16", "fp8", "mxfp4", "nvfp4": the precision of the four layer products)."""
 
     def __init__(self, weights: dict, arch: dict, dtype: str = "bf16", max_tokens: int = 4096,
                  pack: bool = True, n_exec: int | None = None, out_dim: int | None = None, n_groups: int = 1,

@@ -9,6 +9,7 @@
 //   -> GEMM 768->512 scattered to [B, T, 512] -> zero padding rows.
 // The shared layer's weights exist once in device memory and every execution
 // reads the same copy, which stays resident in L2 across executions.
+#include <cmath>
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
@@ -17,6 +18,8 @@
 
 #include "albert.h"
 #include "kernels.h"
+#include "mx4.cuh"
+#include "mx4.h"
 
 using namespace albert;
 
@@ -25,16 +28,28 @@ namespace {
 enum ProfClass {
     kProfPrep = 0, kProfEmbed, kProfGemmIn, kProfGemmQKV, kProfAttention, kProfGemmWoLN,
     kProfGemmW1Gelu, kProfGemmW2LN, kProfGemmOut, kProfOutput, kProfLayerNorm, kProfSmall, kProfQuant,
-    kProfEmbedProj, kProfClasses
+    kProfEmbedProj, kProfQuantMx4, kProfNormMx4, kProfClasses
 };
 const char *kProfNames[kProfClasses] = {
     "prep", "embed_ln", "gemm_in_proj", "gemm_qkv", "attention", "gemm_out_proj_ln",
     "gemm_ffn_up_gelu", "gemm_ffn_down_ln", "gemm_final_proj", "output_rows", "layer_norm_f32",
-    "small_batch_forward", "quant_e4m3", "embed_proj"};
+    "small_batch_forward", "quant_e4m3", "embed_proj", "quant_mx4", "layer_norm_mx4"};
 
 constexpr int kEventPool = 16384;
 
+// ALBERT_NVFP4: tensor scale of every activation.  A block's E4M3 scale then reaches
+// magnitudes up to 6 * 448 / 32 = 84 and keeps its four bits down to a largest
+// magnitude of 6 * 2^-6 / 32 = 0.003; LayerNorm outputs stay below sqrt(768) = 28.
+constexpr float kMx4ActScale = 0.03125f;
+
 }  // namespace
+
+// A [n, k] weight matrix in 4-bit form (mx4.cuh).
+struct Mx4Weight {
+    uint8_t *codes = nullptr, *scales = nullptr;
+    float tensor_scale = 1.0f;
+    int n = 0, k = 0;
+};
 
 struct albert_handle {
     albert_config cfg{};
@@ -60,6 +75,8 @@ struct albert_handle {
         uint8_t *q_wqkv = nullptr, *q_wo = nullptr, *q_w1 = nullptr, *q_w2 = nullptr;
         float *s_wqkv = nullptr, *s_wo = nullptr, *s_w1 = nullptr, *s_w2 = nullptr;
         CUtensorMap tq_wqkv, tq_wo, tq_w1, tq_w2;
+        // ALBERT_MXFP4 / ALBERT_NVFP4: 4-bit copies of the four layer matrices
+        Mx4Weight m_wqkv, m_wo, m_w1, m_w2;
     };
     std::vector<Group> grp;
     // bf16, execution l >= 1: its group's Q|K|V and out-projection with the LN2
@@ -91,6 +108,10 @@ struct albert_handle {
     uint8_t *qA = nullptr;
     float *sA = nullptr;
     CUtensorMap tq_A768, tq_A2048;
+
+    // ALBERT_MXFP4 / ALBERT_NVFP4: the 4-bit layer input or attention output [rows, 768] and
+    // the 4-bit FFN activation [rows, 2048]
+    uint8_t *mA = nullptr, *mA_scales = nullptr, *mH = nullptr, *mH_scales = nullptr;
 
     // host-buffer staging
     int64_t *st_ids = nullptr;
@@ -168,6 +189,11 @@ int dev_alloc(albert_handle *h, void **p, size_t bytes) {
     return ALBERT_OK;
 }
 
+bool is_mx4(const albert_config &c) { return c.dtype == ALBERT_MXFP4 || c.dtype == ALBERT_NVFP4; }
+size_t mx4_scale_bytes(size_t rows, int cols, bool nv) {
+    return (rows + 127) / 128 * mx4_stages(cols) * (nv ? 4 : 2) * kMx4TileBytes;
+}
+
 size_t elem_bytes(const albert_handle *h) { return h->cfg.dtype == ALBERT_FP32 ? 4 : 2; }
 int out_width(const albert_handle *h) { return h->cfg.out_dim > 0 ? h->cfg.out_dim : kHidden; }
 
@@ -182,7 +208,7 @@ int check_config(const albert_config *c) {
     if (c->n_exec < 0 || c->n_groups < 1 || c->n_groups > (c->n_exec > 0 ? c->n_exec : 1)) return ALBERT_ERR_CONFIG;
     if (c->max_pos < 1 || c->max_pos > kMaxPos || c->vocab < 1 || c->n_types < 1) return ALBERT_ERR_CONFIG;
     if (c->out_dim != 0 && c->out_dim != 512) return ALBERT_ERR_CONFIG;
-    if (c->dtype != ALBERT_BF16 && c->dtype != ALBERT_FP32 && c->dtype != ALBERT_FP8) return ALBERT_ERR_CONFIG;
+    if (c->dtype < ALBERT_BF16 || c->dtype > ALBERT_NVFP4) return ALBERT_ERR_CONFIG;
     if (c->max_tokens < 1 || c->max_tokens > (1 << 24)) return ALBERT_ERR_CONFIG;
     if (c->pack != 0 && c->pack != 1) return ALBERT_ERR_CONFIG;
     if (c->out_layout != 0 && c->out_layout != 1) return ALBERT_ERR_CONFIG;
@@ -298,6 +324,81 @@ GemmF32Args f32_args(albert_handle *h, const void *A, const void *W, const float
     return a;
 }
 
+// The layers of the 4-bit path: every layer product on 4-bit operands, with the block
+// scales of its input row by row, so a row needs no statistics but its own; the
+// LayerNorms run as one pass that leaves the bf16 row (the residual) and its 4-bit form
+// (the next product's operand), and the FFN's inner activation leaves its product in 4
+// bits.  X holds a layer's input, X1 the row between its halves, Z the pre-norm rows.
+int run_layers_mx4(albert_handle *h, Launch &L, int nseq, int max_len, long long row_bound) {
+    const albert_config &c = h->cfg;
+    const bool nv = c.dtype == ALBERT_NVFP4;
+    const float ats = nv ? kMx4ActScale : 1.0f;
+    const int M = row_bound < h->rows_cap ? (int)row_bound : h->rows_cap;
+    auto rows = [&](const void *x) {
+        Mx4QuantArgs q{};
+        q.x = x;
+        q.type = kElemBf16;
+        q.ld = q.cols = kHidden;
+        q.rows = M;
+        q.nv = nv;
+        q.tensor_scale = ats;
+        q.codes = h->mA;
+        q.scales = h->mA_scales;
+        q.n_rows = h->n_rows;
+        q.status = h->status;
+        return q;  // (trigger 0: see the E4M3 quantizer)
+    };
+    auto norm = [&](void *y, const float *g, const float *b) -> int {
+        Mx4NormArgs a{rows(h->Z), g, b, c.ln_eps, y, kHidden};
+        LAUNCH(L, kProfNormMx4, launch_mx4_norm(a, L.s, true));
+        return ALBERT_OK;
+    };
+    auto linear = [&](int cls, const uint8_t *a, const uint8_t *a_scales, const Mx4Weight &w, const float *bias,
+                      const void *res, void *out, bool gelu_to_H) -> int {
+        Mx4GemmArgs g{};
+        g.a = a; g.a_scales = a_scales;
+        g.w = w.codes; g.w_scales = w.scales;
+        g.M = M; g.N = w.n; g.K = w.k;
+        g.nv = nv;
+        g.alpha = ats * w.tensor_scale;
+        g.bias = bias;
+        g.gelu = gelu_to_H;
+        g.res = res; g.ld_res = w.n;
+        g.out = out; g.out_type = kElemBf16; g.ld_out = w.n;
+        if (gelu_to_H) { g.q = h->mH; g.q_scales = h->mH_scales; g.q_ts = ats; }
+        g.n_rows = h->n_rows;
+        g.status = h->status;
+        g.check_status = 1;
+        g.trigger = 1;
+        g.wait_ns = h->wait_ns;
+        g.withhold_loads = (h->stall_mask >> cls) & 1u;
+        LAUNCH(L, cls, launch_mx4_gemm(g, h->num_sms, L.s, true));
+        return ALBERT_OK;
+    };
+    int rc;
+    for (int l = 0; l < c.n_exec; ++l) {
+        const auto &W = h->grp[group_of(c, l)];
+        if (l == 0) LAUNCH(L, kProfQuantMx4, launch_mx4_quant(rows(h->X), L.s, true));
+        if ((rc = linear(kProfGemmQKV, h->mA, h->mA_scales, W.m_wqkv, W.bqkv, nullptr, h->QKV, false))) return rc;
+        if (max_len <= kAttnTcMaxLen) {
+            LAUNCH(L, kProfAttention, launch_attention_tc(h->tm_QKV, h->tm_QKV64, static_cast<bf16 *>(h->C), h->att_groups,
+                                                         h->n_att_groups, nseq, h->status, h->num_sms, L.s, true,
+                                                         h->wait_ns));
+        } else {
+            LAUNCH(L, kProfAttention, launch_attention_tc_long(h->tm_QKV, h->tm_QKV64, static_cast<bf16 *>(h->C),
+                                                              h->seq_start, h->seq_len, nseq, h->status, h->num_sms, L.s,
+                                                              true, h->wait_ns));
+        }
+        LAUNCH(L, kProfQuantMx4, launch_mx4_quant(rows(h->C), L.s, true));
+        if ((rc = linear(kProfGemmWoLN, h->mA, h->mA_scales, W.m_wo, W.bo, h->X, h->Z, false))) return rc;
+        if ((rc = norm(h->X1, W.ln1_g, W.ln1_b))) return rc;
+        if ((rc = linear(kProfGemmW1Gelu, h->mA, h->mA_scales, W.m_w1, W.b1, nullptr, nullptr, true))) return rc;
+        if ((rc = linear(kProfGemmW2LN, h->mH, h->mH_scales, W.m_w2, W.b2, h->X1, h->Z, false))) return rc;
+        if ((rc = norm(h->X, W.ln2_g, W.ln2_b))) return rc;
+    }
+    return ALBERT_OK;
+}
+
 // Everything after the prep kernel; `padded_api` selects zero-filled padding rows.
 int run_layers(albert_handle *h, Launch &L, const int64_t *ids, int ids_padded, int nseq, int T,
                int max_len, void *out, int padded_api, const float *emb_in = nullptr) {
@@ -307,8 +408,9 @@ int run_layers(albert_handle *h, Launch &L, const int64_t *ids, int ids_padded, 
     // which the last kernel transposes per sequence into the caller's output
     void *const user_out = out;
     if (padded_api && c.out_layout == 1) out = h->tout;
-    const bool bf = c.dtype != ALBERT_FP32;  // bf16 activations (ALBERT_BF16 and ALBERT_FP8)
+    const bool bf = c.dtype != ALBERT_FP32;  // bf16 activations (all but ALBERT_FP32)
     const bool f8 = c.dtype == ALBERT_FP8;
+    const bool f4 = is_mx4(c);
     EmbedArgs ea{};
     ea.ids = ids;
     ea.ids_padded = ids_padded;
@@ -375,7 +477,8 @@ int run_layers(albert_handle *h, Launch &L, const int64_t *ids, int ids_padded, 
     }
     if (bf) {
         int rc;
-        for (int l = 0; l < c.n_exec; ++l) {
+        if (f4 && (rc = run_layers_mx4(h, L, nseq, max_len, row_bound))) return rc;
+        for (int l = 0; l < (f4 ? 0 : c.n_exec); ++l) {
             const auto &W = h->grp[group_of(c, l)];                  // this execution's weights
             const auto &Wp = h->grp[group_of(c, l > 0 ? l - 1 : 0)];  // the previous execution's (its LN2)
             // ALBERT_FP8: a layer GEMM's A operand is first quantized per row (E4M3 codes
@@ -450,7 +553,7 @@ int run_layers(albert_handle *h, Launch &L, const int64_t *ids, int ids_padded, 
         }
         if (c.out_dim > 0) {
             // the final projection is followed by zero_pad only in the padded API
-            if (c.n_exec == 0) {
+            if (c.n_exec == 0 || f4) {
                 GemmArgs a = gemm_args(h, c.out_dim, kHidden, h->b_out, out, c.out_dim);
                 a.trigger = padded_api;
                 rc = gemm_bf16(L, kProfGemmOut, kEpiScatter, h->tm_X, h->tm_wout, h->t32_X, h->t32_X, a);
@@ -462,7 +565,7 @@ int run_layers(albert_handle *h, Launch &L, const int64_t *ids, int ids_padded, 
                 rc = gemm_bf16(L, kProfGemmOut, kEpiLnInScatter, h->tm_Z, h->tm_wout, h->t32_X, h->t32_X, a);
             }
             if (rc) return rc;
-        } else if (c.n_exec == 0) {
+        } else if (c.n_exec == 0 || f4) {
             LAUNCH(L, kProfOutput, launch_scatter_rows(h->X, out, kHidden, 2, h->rows_cap, h->n_rows, h->row_dst, h->status, L.s));
         } else {
             const auto &Wl = h->grp[group_of(c, c.n_exec - 1)];
@@ -526,8 +629,9 @@ int create_impl(albert_handle *h, const albert_weights *w) {
     h->rows_cap = (c.max_tokens + 127) / 128 * 128;
     h->seq_cap = c.max_tokens;
     const size_t R = h->rows_cap;
-    const bool bf = c.dtype != ALBERT_FP32;  // bf16 activations (ALBERT_BF16 and ALBERT_FP8)
+    const bool bf = c.dtype != ALBERT_FP32;  // bf16 activations (all but ALBERT_FP32)
     const bool f8 = c.dtype == ALBERT_FP8;
+    const bool f4 = is_mx4(c);
     const size_t eb = elem_bytes(h);
     int rc;
     cudaStream_t s = nullptr;
@@ -608,7 +712,54 @@ int create_impl(albert_handle *h, const albert_weights *w) {
     if ((rc = dev_alloc(h, &h->X1, R * kHidden * eb))) return rc;
     if ((rc = dev_alloc(h, &h->H, R * kFfn * eb))) return rc;
     if ((rc = dev_alloc(h, &h->Z, R * kHidden * eb))) return rc;
-    if (bf) {
+    if (f4) {
+        const bool nv = c.dtype == ALBERT_NVFP4;
+        struct { uint8_t **p; size_t n; } bufs[4] = {{&h->mA, R * (kHidden / 2)},
+                                                     {&h->mA_scales, mx4_scale_bytes(R, kHidden, nv)},
+                                                     {&h->mH, R * (kFfn / 2)},
+                                                     {&h->mH_scales, mx4_scale_bytes(R, kFfn, nv)}};
+        for (auto &b : bufs) {
+            if ((rc = dev_alloc(h, (void **)b.p, b.n))) return rc;
+            TRY(cudaMemsetAsync(*b.p, 0, b.n, s));
+        }
+        // 4-bit copies of the layer matrices (from their bf16 copies); an nvfp4 matrix's tensor
+        // scale puts its largest magnitude at the largest block scale
+        unsigned *amax = nullptr;
+        if ((rc = dev_alloc(h, (void **)&amax, sizeof(unsigned)))) return rc;
+        for (auto &gp : h->grp) {
+            struct { Mx4Weight *m; const void *w; int n, k; } mats[4] = {{&gp.m_wqkv, gp.wqkv, kQKV, kHidden},
+                                                                         {&gp.m_wo, gp.wo, kHidden, kHidden},
+                                                                         {&gp.m_w1, gp.w1, kFfn, kHidden},
+                                                                         {&gp.m_w2, gp.w2, kHidden, kFfn}};
+            for (auto &m : mats) {
+                m.m->n = m.n;
+                m.m->k = m.k;
+                if ((rc = dev_alloc(h, (void **)&m.m->codes, (size_t)m.n * mx4_code_pitch(m.k)))) return rc;
+                if ((rc = dev_alloc(h, (void **)&m.m->scales, mx4_scale_bytes(m.n, m.k, nv)))) return rc;
+                if (nv) {
+                    unsigned bits = 0;
+                    TRY(launch_amax_bf16(static_cast<const bf16 *>(m.w), (size_t)m.n * m.k, amax, s));
+                    TRY(cudaMemcpyAsync(&bits, amax, sizeof(bits), cudaMemcpyDeviceToHost, s));
+                    TRY(cudaStreamSynchronize(s));
+                    float a;
+                    memcpy(&a, &bits, sizeof(a));
+                    const float ts = a / (6.0f * 448.0f);
+                    m.m->tensor_scale = std::isfinite(ts) && ts >= 1e-30f ? ts : 1.0f;
+                }
+                Mx4QuantArgs q{};
+                q.x = m.w;
+                q.type = kElemBf16;
+                q.ld = q.cols = m.k;
+                q.rows = m.n;
+                q.nv = nv;
+                q.tensor_scale = m.m->tensor_scale;
+                q.codes = m.m->codes;
+                q.scales = m.m->scales;
+                TRY(launch_mx4_quant(q, s, false));
+            }
+        }
+    }
+    if (bf && !f4) {
         const size_t nst = R * gemm::LN_PARTS;
         if ((rc = dev_alloc(h, (void **)&h->st1, nst * sizeof(float2)))) return rc;
         if ((rc = dev_alloc(h, (void **)&h->st2, nst * sizeof(float2)))) return rc;
@@ -717,7 +868,7 @@ int create_impl(albert_handle *h, const albert_weights *w) {
                     return ALBERT_ERR_CUDA;
         }
         // the small-batch kernel: bf16, one weight set, at least one execution
-        if (!f8 && c.n_groups == 1 && c.n_exec >= 1) {
+        if (!f8 && !f4 && c.n_groups == 1 && c.n_exec >= 1) {
             const auto &gp = h->grp[0];
             if ((rc = dev_alloc(h, (void **)&h->sst1, kSmallMaxRows * kSmallParts * sizeof(float2)))) return rc;
             if ((rc = dev_alloc(h, (void **)&h->sst2, kSmallMaxRows * kSmallParts * sizeof(float2)))) return rc;
@@ -948,6 +1099,8 @@ void albert_destroy(albert_handle *h) {
 
 int albert_launches_per_forward(const albert_handle *h, int padded_api) {
     if (!h) return -1;
+    if (is_mx4(h->cfg))  // prep, embedding, first quantization, layers, final or scatter
+        return 3 + (h->cfg.n_exec > 0 ? 1 : 0) + 8 * h->cfg.n_exec + (padded_api ? 1 : 0);
     const int per_layer = h->cfg.dtype == ALBERT_BF16 ? 5 : h->cfg.dtype == ALBERT_FP8 ? 9 : 7;
     return 1 /*prep*/ + 1 /*embed*/ + 1 /*in proj*/ + per_layer * h->cfg.n_exec + 1 /*final or scatter*/ +
            (padded_api ? 1 : 0);

@@ -4,8 +4,8 @@
 #include <cmath>
 
 #include "albert.h"
-#include "kernels.h"
 #include "mx4.cuh"
+#include "mx4.h"
 
 using namespace albert;
 

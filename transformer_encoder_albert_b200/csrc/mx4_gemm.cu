@@ -31,9 +31,9 @@
 // Every wait is bounded; see the bf16 GEMM.
 #include <type_traits>
 
-#include "kernels.h"
 #include "mx4.cuh"
-#include "sm100_ptx.cuh"
+#include "mx4.h"
+#include "mx4_ptx.cuh"
 
 namespace albert {
 namespace {

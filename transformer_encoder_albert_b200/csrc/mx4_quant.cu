@@ -11,8 +11,8 @@
 // and the next such pair's loads are in flight while one is converted.
 #include <type_traits>
 
-#include "kernels.h"
 #include "mx4.cuh"
+#include "mx4.h"
 #include "sm100_ptx.cuh"
 
 namespace albert {
@@ -393,6 +393,15 @@ mx4_norm_cta_kernel(const T *__restrict__ x, long long ld, const float *__restri
     }
 }
 
+// (weights, once per handle: no need to be fast)
+__global__ void amax_bf16_kernel(const bf16 *__restrict__ x, size_t n, unsigned *out) {
+    uint32_t m = 0;
+    for (size_t i = (size_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (size_t)gridDim.x * blockDim.x)
+        m = umax(m, abs_bits(__bfloat162float(x[i])));
+    m = __reduce_max_sync(0xffffffffu, m);
+    if ((threadIdx.x & 31) == 0) atomicMax(out, m);
+}
+
 // CTAs of `kernel` that are resident at once (asked once per device), at most `need`.
 template <typename K>
 cudaError_t resident_grid(K kernel, std::atomic<int> (&cached)[64], long long need, int &blocks) {
@@ -505,6 +514,12 @@ cudaError_t launch_mx4_dequant(const uint8_t *codes, const uint8_t *scales, int 
                                void *out, int type, long long ld, cudaStream_t s) {
     if (rows < 1) return cudaSuccess;
     MX4_BY_TYPE(dequant_typed, type, nv, codes, scales, rows, cols, ts, out, ld, s);
+}
+cudaError_t launch_amax_bf16(const bf16 *x, size_t n, unsigned *out, cudaStream_t s) {
+    cudaError_t e = cudaMemsetAsync(out, 0, sizeof(unsigned), s);
+    if (e != cudaSuccess) return e;
+    amax_bf16_kernel<<<256, 256, 0, s>>>(x, n, out);
+    return cudaGetLastError();
 }
 cudaError_t launch_mx4_norm(const Mx4NormArgs &a, cudaStream_t s, bool pdl) {
     if (a.q.rows < 1) return cudaSuccess;

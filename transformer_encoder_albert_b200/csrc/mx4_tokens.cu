@@ -17,9 +17,9 @@
 // result columns that nobody reads.
 #include <type_traits>
 
-#include "kernels.h"
 #include "mx4.cuh"
-#include "sm100_ptx.cuh"
+#include "mx4.h"
+#include "mx4_ptx.cuh"
 
 namespace albert {
 namespace {
