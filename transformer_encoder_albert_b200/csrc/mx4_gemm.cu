@@ -70,18 +70,6 @@ struct Ctrl {
     int *misc;
 };
 
-template <typename T>
-__device__ __forceinline__ void add_row(const T *p, int n, bool vec, float (&v)[32]) {
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        float r[8];
-        const int left = n - 8 * q;
-        load8<T>(p + 8 * q, left > 0 ? left : 0, vec, r);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[8 * q + i] += r[i];
-    }
-}
-
 // Byte offset of 16-byte chunk q of row r in a 32x32 16-bit tile stored with the TMA
 // 64-byte swizzle.
 __device__ __forceinline__ uint32_t stg_off(int r, int q) {
@@ -95,6 +83,12 @@ __device__ __forceinline__ uint4 ld_shared_u4(uint32_t a) {
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
     return v;
 }
+__device__ __forceinline__ void st_shared_u1(uint32_t a, uint32_t v) {
+    asm volatile("st.shared.b32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+__device__ __forceinline__ void st_shared_u16(uint32_t a, uint16_t v) {
+    asm volatile("st.shared.u16 [%0], %1;" ::"r"(a), "h"(v) : "memory");
+}
 __device__ __forceinline__ uint32_t ld_shared_u1(uint32_t a) {
     uint32_t v;
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
@@ -106,12 +100,27 @@ __device__ __forceinline__ uint16_t ld_shared_u16(uint32_t a) {
     return v;
 }
 
+// v += row `lane` of a 16-bit 32x32 tile.
+__device__ __forceinline__ void add_tile16(uint32_t tile, int lane, bool f16, float (&v)[32]) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        const uint4 w = ld_shared_u4(tile + stg_off(lane, q));
+        const uint32_t w4[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 f = f16 ? unpack_x2<__half>(w4[e]) : unpack_x2<bf16>(w4[e]);
+            v[8 * q + 2 * e] += f.x;
+            v[8 * q + 2 * e + 1] += f.y;
+        }
+    }
+}
+
 template <bool NV, bool PAIR, bool QOUT>
 __global__ void __launch_bounds__(kThreads, 1)
 mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                 const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
                 const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ CUtensorMap tmRes, const Mx4GemmArgs p,
-                int n_sub, int tma_out, int tma_res, int vec_res) {
+                int n_sub, int tma_out, int tma_res) {
     using P = Plan<NV, PAIR>;
     constexpr int NST = P::NST, TN = P::TN, ST = P::ST;
     extern __shared__ uint8_t smem_raw[];
@@ -243,6 +252,7 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             auto wait = [&](uint64_t *bar, uint32_t parity) {
                 return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, c.abort_flag)) != 0;
             };
+            const uint64_t da0 = sw128_kmajor_desc(smem_u32(sA)), db0 = sw128_kmajor_desc(smem_u32(sB));
             uint32_t stage = 0, t = 0;  // t: tiles issued by this CTA
             uint32_t it = 0;                       // stages consumed
             bool ok = true;
@@ -259,15 +269,22 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                     // waited for the stage, arrives on the same barrier as its copies
                     if (!wait(&c.sfull[it & 1], (it >> 1) & 1)) { ok = false; break; }
                     tc_fence_after();
-                    const uint32_t a0 = smem_u32(sA) + stage * kRowsBytes, b0 = smem_u32(sB) + stage * kRowsBytes;
+                    // (a descriptor's address field counts 16 bytes: a product's 32 bytes of K are 2)
+                    const uint64_t da = da0 + stage * (kRowsBytes >> 4), db = db0 + stage * (kRowsBytes >> 4);
                     const uint32_t ca = tmem + P::SFCOL + (it & 1) * P::SFBUF, cb = ca + 4 * ST;
-                    const int left = p.K - kb * kMx4StageCols;  // products past the last column are left out
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
+                    auto product = [&](int k, uint32_t who, uint32_t acc) {
                         const int g = NV ? k : k >> 1;
-                        umma_mx4<NV, PAIR>(k * 64 < left ? leader : 0u, d, sw128_kmajor_desc(a0 + k * 32),
-                                           sw128_kmajor_desc(b0 + k * 32), idesc_mx4<NV>(P::UM, TN, NV ? 0 : 2 * (k & 1)),
-                                           ca + 4 * g, cb + g * (TN / 128) * 4, (kb | k) != 0);
+                        umma_mx4<NV, PAIR>(who, d, da + 2 * k, db + 2 * k, idesc_mx4<NV>(P::UM, TN, NV ? 0 : 2 * (k & 1)),
+                                           ca + 4 * g, cb + g * (TN / 128) * 4, acc);
+                    };
+                    product(0, leader, kb != 0);
+                    const int left = p.K - kb * kMx4StageCols;
+                    if (left > 3 * 64) {
+#pragma unroll
+                        for (int k = 1; k < 4; ++k) product(k, leader, 1);
+                    } else {  // products past the last column are left out
+#pragma unroll
+                        for (int k = 1; k < 4; ++k) product(k, k * 64 < left ? leader : 0u, 1);
                     }
                     umma_commit_elected<PAIR>(leader, smem_u32(c.empty) + 8 * stage, 3);
                     if (++stage == NST) stage = 0;
@@ -285,6 +302,7 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             auto wait = [&](uint64_t *bar, uint32_t parity) {
                 return __all_sync(0xffffffffu, mbar_wait(smem_u32(bar), parity, c.abort_flag)) != 0;
             };
+            const uint64_t da0 = scale_tile_desc(smem_u32(sSA)), db0 = scale_tile_desc(smem_u32(sSB));
             uint32_t stage = 0, phase = 0, it = 0;
             uint32_t es = 0, eph = 0;  // stage and phase of the stage before last
             bool ok = true;
@@ -297,15 +315,15 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                         if (++es == NST) { es = 0; eph ^= 1; }
                     }
                     tc_fence_after();
-                    const uint32_t fa = smem_u32(sSA) + stage * P::SFA, fs = smem_u32(sSB) + stage * P::SFB;
+                    const uint64_t da = da0 + stage * (P::SFA >> 4), db = db0 + stage * (P::SFB >> 4);
                     const uint32_t ca = tmem + P::SFCOL + (it & 1) * P::SFBUF, cb = ca + 4 * ST;
 #pragma unroll
                     for (int g = 0; g < ST; ++g) {
-                        tmem_cp_scales<PAIR>(leader, ca + 4 * g, scale_tile_desc(fa + g * kMx4TileBytes));
+                        tmem_cp_scales<PAIR>(leader, ca + 4 * g, da + g * (kMx4TileBytes >> 4));
 #pragma unroll
                         for (int h = 0; h < TN / 128; ++h)
                             tmem_cp_scales<PAIR>(leader, cb + (g * (TN / 128) + h) * 4,
-                                                 scale_tile_desc(fs + h * P::SFA + g * kMx4TileBytes));
+                                                 db + ((h * P::SFA + g * kMx4TileBytes) >> 4));
                     }
                     umma_commit_elected<PAIR>(leader, smem_u32(&c.sfull[it & 1]), 1);
                     if (lane == 0) mbar_arrive(smem_u32(&c.sfull[it & 1]));
@@ -439,27 +457,41 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                             if (!__all_sync(0xffffffffu, rok)) { ok = false; break; }
                             rph ^= 1;
                             res_pending = false;
-                            const bool f16 = p.out_type == kElemF16;
-#pragma unroll
-                            for (int q = 0; q < 4; ++q) {
-                                const uint4 w = ld_shared_u4(stg + kTile + stg_off(lane, q));
-                                const uint32_t w4[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    const float2 f = f16 ? unpack_x2<__half>(w4[e]) : unpack_x2<bf16>(w4[e]);
-                                    v[8 * q + 2 * e] += f.x;
-                                    v[8 * q + 2 * e + 1] += f.y;
-                                }
-                            }
+                            add_tile16(stg + kTile, lane, p.out_type == kElemF16, v);
                             __syncwarp();
                             if (i + 1 < PER) res_issue(u, t, i + 1);
                             else if (u + nslots < units) res_issue(u + nslots, t + 1, 0);
-                        } else if (row_ok && left > 0) {
-                            const size_t ro = (size_t)row * p.ld_res + col0;
-                            const int cnt = left < 32 ? left : 32;
-                            if (f32) add_row(static_cast<const float *>(p.res) + ro, cnt, vec_res, v);
-                            else if (p.out_type == kElemF16) add_row(static_cast<const __half *>(p.res) + ro, cnt, vec_res, v);
-                            else add_row(static_cast<const bf16 *>(p.res) + ro, cnt, vec_res, v);
+                        } else {
+                            // fp32 and unaligned rows: a column per lane into the staging tiles
+                            if (lane == 0) bulk_wait_read0();
+                            __syncwarp();
+                            const int rows = n_rows - row0 < 32 ? n_rows - row0 : 32;
+                            if (lane < left) {
+                                const size_t ro = (size_t)row0 * p.ld_res + col0 + lane;
+#pragma unroll 8
+                                for (int y = 0; y < rows; ++y) {
+                                    if (f32)
+                                        st_shared_u1(stg + (lane >> 4) * kTile + stg_off(y, (lane >> 2) & 3) + (lane & 3) * 4,
+                                                     __ldg(static_cast<const uint32_t *>(p.res) + ro + (size_t)y * p.ld_res));
+                                    else
+                                        st_shared_u16(stg + kTile + stg_off(y, lane >> 3) + (lane & 7) * 2,
+                                                      __ldg(static_cast<const unsigned short *>(p.res) + ro + (size_t)y * p.ld_res));
+                                }
+                            }
+                            __syncwarp();
+                            if (f32) {
+#pragma unroll
+                                for (int q = 0; q < 8; ++q) {
+                                    const uint4 w = ld_shared_u4(stg + (q >> 2) * kTile + stg_off(lane, q & 3));
+                                    v[4 * q] += __uint_as_float(w.x);
+                                    v[4 * q + 1] += __uint_as_float(w.y);
+                                    v[4 * q + 2] += __uint_as_float(w.z);
+                                    v[4 * q + 3] += __uint_as_float(w.w);
+                                }
+                            } else {
+                                add_tile16(stg + kTile, lane, p.out_type == kElemF16, v);
+                            }
+                            __syncwarp();
                         }
                     }
                     // the chunk through shared memory: a 16-bit 32x32 tile, or two fp32 tiles of 16
@@ -561,7 +593,7 @@ cudaError_t launch_tile(const Mx4GemmArgs &a, int num_sms, cudaStream_t s, bool 
     const int es = a.out_type == kElemF32 ? 4 : 2;
     auto ok16 = [&](const void *q, long long ld) { return q && (reinterpret_cast<uintptr_t>(q) & 15) == 0 && ld * es % 16 == 0; };
     CUtensorMap tmOut = tmA, tmRes = tmA;
-    const int vec_res = ok16(a.res, a.ld_res), tma_res = vec_res && a.out_type != kElemF32, tma_out = ok16(a.out, a.ld_out);
+    const int tma_res = ok16(a.res, a.ld_res) && a.out_type != kElemF32, tma_out = ok16(a.out, a.ld_out);
     if ((tma_out && make_tmap_tile32(&tmOut, a.out, a.out_type, a.M, a.N, a.ld_out)) ||
         (tma_res && make_tmap_tile32(&tmRes, a.res, a.out_type, a.M, a.N, a.ld_res)))
         return cudaErrorInvalidValue;
@@ -585,7 +617,7 @@ cudaError_t launch_tile(const Mx4GemmArgs &a, int num_sms, cudaStream_t s, bool 
     cfg.attrs = attr;
     cfg.numAttrs = na;
     return cudaLaunchKernelEx(&cfg, mx4_gemm_kernel<NV, PAIR, QOUT>, tmA, tmB, tmSA, tmSB, tmOut, tmRes, a, n_sub, tma_out,
-                              tma_res, vec_res);
+                              tma_res);
 }
 
 template <bool NV, bool QOUT>
