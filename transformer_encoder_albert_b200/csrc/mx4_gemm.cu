@@ -63,6 +63,26 @@ struct Plan {
     static_assert((2 * NST + 8 + kEpiWarps) * 8 + 32 <= 512, "barriers");
 };
 
+// Walk over a CTA's tiles, unit u = tile (u / n_sub, u % n_sub), by additions.
+struct TileWalk {
+    int u, m, n, step, dm, dn, n_sub;
+    __device__ __forceinline__ TileWalk(int first, int step_, int n_sub_) : u(first), step(step_), n_sub(n_sub_) {
+        m = first / n_sub_;
+        n = first - m * n_sub_;
+        dm = step_ / n_sub_;
+        dn = step_ - dm * n_sub_;
+    }
+    __device__ __forceinline__ void next() {
+        u += step;
+        m += dm;
+        n += dn;
+        if (n >= n_sub) {
+            n -= n_sub;
+            ++m;
+        }
+    }
+};
+
 struct Ctrl {
     uint64_t *full, *empty, *sfull, *tfull, *tfree, *drain, *sdrain, *rbar;
     uint32_t *tmem_slot;
@@ -195,7 +215,7 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     const bool skip = c.misc[1] != 0 || c.misc[0] < 0 || c.misc[0] > p.M;
     const int n_rows = skip ? 0 : c.misc[0];
     const int m_blocks = (n_rows + P::UM - 1) / P::UM;
-    const long long units = (long long)m_blocks * n_sub;
+    const int units = m_blocks * n_sub;  // (the host has checked that they and a step past them fit)
     const int kblocks = mx4_stages(p.K);
 
     if (warp == 0) {
@@ -204,9 +224,9 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             int stage = 0, issued = 0;
             uint32_t phase = 0;
             bool ok = true;
-            const long long loaded = p.withhold_loads ? 0 : units;
-            for (long long u = slot; u < loaded && ok; u += nslots) {
-                const int m = (int)(u / n_sub), n = (int)(u % n_sub);
+            const int loaded = p.withhold_loads ? 0 : units;
+            for (TileWalk w(slot, nslots, n_sub); w.u < loaded && ok; w.next()) {
+                const int m = w.m, n = w.n;
                 for (int kb = 0; kb < kblocks; ++kb) {
                     if (!mbar_wait(smem_u32(&c.empty[stage]), phase ^ 1, c.abort_flag)) {
                         ok = false;
@@ -256,7 +276,7 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             uint32_t stage = 0, t = 0;  // t: tiles issued by this CTA
             uint32_t it = 0;                       // stages consumed
             bool ok = true;
-            for (long long u = slot; u < units && ok; u += nslots, ++t) {
+            for (int u = slot; u < units && ok; u += nslots, ++t) {
                 if (PAIR) {
                     // the previous tile's columns of the overlap have been read
                     if (t >= 1 && !wait(&c.tfree[(t - 1) & 1], ((t - 1) >> 1) & 1)) break;
@@ -306,7 +326,7 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             uint32_t stage = 0, phase = 0, it = 0;
             uint32_t es = 0, eph = 0;  // stage and phase of the stage before last
             bool ok = true;
-            for (long long u = slot; u < units && ok; u += nslots) {
+            for (int u = slot; u < units && ok; u += nslots) {
                 for (int kb = 0; kb < kblocks; ++kb, ++it) {
                     if (!wait(&c.full[stage], phase)) { ok = false; break; }
                     if (it >= 2) {
@@ -347,26 +367,28 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         // upper end, the second from its lower end, so that the overlap comes first
         auto chunk_of = [&](uint32_t tt, int i) { return (PAIR && (tt & 1) == 0) ? (TN / 32 - 1 - part) - 4 * i : part + 4 * i; };
         // residual tiles use the second staging tile, results then only the first
-        auto res_issue = [&](long long u, uint32_t tt, int i) {
+        auto res_issue = [&](const TileWalk &w, uint32_t tt, int i) {
             if (lane == 0) {
                 mbar_arrive_expect_tx(rbar, kTile);
-                tma_load_2d(stg + kTile, &tmRes, rbar, (int)(u % n_sub) * TN + chunk_of(tt, i) * 32,
-                            (int)(u / n_sub) * P::UM + (int)rank * 128 + quad * 32);
+                tma_load_2d(stg + kTile, &tmRes, rbar, w.n * TN + chunk_of(tt, i) * 32,
+                            w.m * P::UM + (int)rank * 128 + quad * 32);
             }
             res_pending = true;
         };
-        auto bias_load = [&](long long u, uint32_t tt, int i) {
-            const int col = (int)(u % n_sub) * TN + chunk_of(tt, i) * 32 + lane;
+        auto bias_load = [&](const TileWalk &w, uint32_t tt, int i) {
+            const int col = w.n * TN + chunk_of(tt, i) * 32 + lane;
             return (p.bias && col < p.N) ? __ldg(p.bias + col) : 0.f;
         };
         float bnext = 0.f;
-        if (slot < units) {
-            bnext = bias_load(slot, 0, 0);
-            if (res && tma_res) res_issue(slot, 0, 0);
+        TileWalk w(slot, nslots, n_sub), wn = w;  // this tile, the next
+        if (w.u < units) {
+            bnext = bias_load(w, 0, 0);
+            if (res && tma_res) res_issue(w, 0, 0);
         }
         bool ok = true;
-        for (long long u = slot; u < units && ok; u += nslots, ++t) {
-            const int m = (int)(u / n_sub), n = (int)(u % n_sub);
+        for (; w.u < units && ok; w = wn, ++t) {
+            wn.next();
+            const int m = w.m, n = w.n;
             const int row0 = m * P::UM + (int)rank * 128 + quad * 32, row = row0 + lane;
             const bool row_ok = row < n_rows;
             bool got = mbar_wait(smem_u32(&c.tfull[t & 1]), (t >> 1) & 1, c.abort_flag);
@@ -388,8 +410,8 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                     if (PAIR) mbar_arrive_cluster(mapa_shared(smem_u32(&c.tfree[t & 1]), 0));
                     else mbar_arrive(smem_u32(&c.tfree[t & 1]));
                 }
-                if (i + 1 < PER) bnext = bias_load(u, t, i + 1);
-                else if (u + nslots < units) bnext = bias_load(u + nslots, t + 1, 0);
+                if (i + 1 < PER) bnext = bias_load(w, t, i + 1);
+                else if (wn.u < units) bnext = bias_load(wn, t + 1, 0);
                 const int col0 = n * TN + ch * 32;
                 const int left = p.N - col0;  // columns of this chunk that exist
                 uint64_t v2[16];  // columns col0 + 2j, col0 + 2j + 1
@@ -459,8 +481,8 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                             res_pending = false;
                             add_tile16(stg + kTile, lane, p.out_type == kElemF16, v);
                             __syncwarp();
-                            if (i + 1 < PER) res_issue(u, t, i + 1);
-                            else if (u + nslots < units) res_issue(u + nslots, t + 1, 0);
+                            if (i + 1 < PER) res_issue(w, t, i + 1);
+                            else if (wn.u < units) res_issue(wn, t + 1, 0);
                         } else {
                             // fp32 and unaligned rows: a column per lane into the staging tiles
                             if (lane == 0) bulk_wait_read0();
@@ -588,6 +610,7 @@ cudaError_t launch_tile(const Mx4GemmArgs &a, int num_sms, cudaStream_t s, bool 
     // a 4-bit result's scale tiles reach to a multiple of 256 columns
     const int n_sub = ((QOUT ? mx4_stages(a.N) * kMx4StageCols : a.N) + P::TN - 1) / P::TN;
     const long long units = (long long)((a.M + P::UM - 1) / P::UM) * n_sub;
+    if (units > 0x7fffff00LL - num_sms) return cudaErrorInvalidValue;
     const int slots = PAIR ? num_sms / 2 : num_sms;
     const int grid = (PAIR ? 2 : 1) * (int)(units < slots ? units : slots);
     const int es = a.out_type == kElemF32 ? 4 : 2;
