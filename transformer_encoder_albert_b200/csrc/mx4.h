@@ -63,9 +63,9 @@ struct Mx4GemmArgs {
 // Map of a byte row-major [rows, cols] tensor with a {box_cols, box_rows} box.
 int make_tmap_u8(CUtensorMap *tm, const void *base, uint64_t rows, uint64_t cols, uint32_t box_cols, uint32_t box_rows,
                  bool swizzle128);
-// Map of [rows, cols] elements of an ElemType, rows ld elements apart, with a box of
-// 32 rows of 64 bytes (32 16-bit or 16 fp32 columns) and the 64-byte swizzle.
-int make_tmap_tile32(CUtensorMap *tm, const void *base, int type, uint64_t rows, uint64_t cols, uint64_t ld);
+// Map of [rows, cols] 16-bit elements, rows ld elements apart, with a 32x32 box and the
+// 64-byte swizzle.
+int make_tmap_tile16(CUtensorMap *tm, const void *base, int type, uint64_t rows, uint64_t cols, uint64_t ld);
 
 cudaError_t launch_mx4_gemm(const Mx4GemmArgs &a, int num_sms, cudaStream_t s, bool pdl);
 

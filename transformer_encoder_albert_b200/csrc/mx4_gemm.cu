@@ -15,9 +15,9 @@
 //   warps 4..19 : epilogue, four warps per lane quadrant, each every fourth 32-column
 //                 chunk (a chunk is some 190 dependent instructions: with two warps per
 //                 quadrant it took 1330 cycles, and K = 768 only gives a tile 1536);
-//                 rows leave through swizzled staging tiles by TMA (or coalesced stores
-//                 where they are not 16-byte aligned), 16-bit residual tiles arrive by
-//                 TMA a chunk ahead.
+//                 16-bit rows leave through swizzled staging tiles by TMA, their residual
+//                 tiles arrive by TMA a chunk ahead; fp32 and rows that are not 16-byte
+//                 aligned go a column per lane.
 // Two tile shapes:
 //   * a CTA pair per 256x256 tile (cta_group::2): each CTA stages 128 rows of A and of
 //     W and the scales of its A rows and of all W rows.  Two 256-column accumulators
@@ -118,6 +118,13 @@ __device__ __forceinline__ uint16_t ld_shared_u16(uint32_t a) {
     uint16_t v;
     asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
     return v;
+}
+
+// tma_store_2d of the lane whose predicate holds, without a branch.
+__device__ __forceinline__ void tma_store_if(bool on, const void *tmap, uint32_t src, int x, int y) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %4, 0;\n\t"
+                 "@q cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%2, %3}], [%1];\n\t}"
+                 ::"l"(tmap), "r"(src), "r"(x), "r"(y), "r"((uint32_t)on) : "memory");
 }
 
 // v += row `lane` of a 16-bit 32x32 tile.
@@ -473,102 +480,103 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                         else *sp = (uint8_t)bytes;
                     }
                 } else {
-                    if (res) {
-                        if (tma_res) {
-                            bool rok = mbar_wait(rbar, rph, c.abort_flag);
-                            if (!__all_sync(0xffffffffu, rok)) { ok = false; break; }
-                            rph ^= 1;
-                            res_pending = false;
-                            add_tile16(stg + kTile, lane, p.out_type == kElemF16, v);
-                            __syncwarp();
-                            if (i + 1 < PER) res_issue(w, t, i + 1);
-                            else if (wn.u < units) res_issue(wn, t + 1, 0);
-                        } else {
-                            // fp32 and unaligned rows: a column per lane into the staging tiles
-                            if (lane == 0) bulk_wait_read0();
-                            __syncwarp();
-                            const int rows = n_rows - row0 < 32 ? n_rows - row0 : 32;
-                            if (lane < left) {
-                                const size_t ro = (size_t)row0 * p.ld_res + col0 + lane;
-#pragma unroll 8
-                                for (int y = 0; y < rows; ++y) {
-                                    if (f32)
-                                        st_shared_u1(stg + (lane >> 4) * kTile + stg_off(y, (lane >> 2) & 3) + (lane & 3) * 4,
-                                                     __ldg(static_cast<const uint32_t *>(p.res) + ro + (size_t)y * p.ld_res));
-                                    else
-                                        st_shared_u16(stg + kTile + stg_off(y, lane >> 3) + (lane & 7) * 2,
-                                                      __ldg(static_cast<const unsigned short *>(p.res) + ro + (size_t)y * p.ld_res));
-                                }
-                            }
-                            __syncwarp();
-                            if (f32) {
-#pragma unroll
-                                for (int q = 0; q < 8; ++q) {
-                                    const uint4 w = ld_shared_u4(stg + (q >> 2) * kTile + stg_off(lane, q & 3));
-                                    v[4 * q] += __uint_as_float(w.x);
-                                    v[4 * q + 1] += __uint_as_float(w.y);
-                                    v[4 * q + 2] += __uint_as_float(w.z);
-                                    v[4 * q + 3] += __uint_as_float(w.w);
-                                }
-                            } else {
-                                add_tile16(stg + kTile, lane, p.out_type == kElemF16, v);
-                            }
-                            __syncwarp();
-                        }
-                    }
-                    // the chunk through shared memory: a 16-bit 32x32 tile, or two fp32 tiles of 16
-                    // columns (rows of 64 bytes, 64-byte swizzle)
-                    const uint32_t tile = f32 || (res && tma_res) ? stg : stg + (stores & 1) * kTile;
-                    if (lane == 0) {
-                        if (f32 || res) bulk_wait_read0();
-                        else bulk_wait_read1();
-                    }
-                    __syncwarp();
+                    const int rows = n_rows - row0 < 32 ? n_rows - row0 : 32;  // of this warp's 32 that exist
                     if (f32) {
+                        // through the warp's own 4 KB: two tiles of 16 columns, a column per lane to and
+                        // from global memory
+                        const uint32_t tile = smem_u32(sStg) + ew * kStgBytes;
+                        const uint32_t at = tile + (lane >> 4) * kTile + (lane & 3) * 4;
+                        const int q0 = (lane >> 2) & 3;
+                        __syncwarp();
+                        if (res) {
+                            if (lane < left) {
+                                const uint32_t *src = static_cast<const uint32_t *>(p.res) + (size_t)row0 * p.ld_res + col0 + lane;
+#pragma unroll 8
+                                for (int y = 0; y < rows; ++y) st_shared_u1(at + stg_off(y, q0), __ldg(src + (size_t)y * p.ld_res));
+                            }
+                            __syncwarp();
+#pragma unroll
+                            for (int q = 0; q < 8; ++q) {
+                                const uint4 x = ld_shared_u4(tile + (q >> 2) * kTile + stg_off(lane, q & 3));
+                                v[4 * q] += __uint_as_float(x.x);
+                                v[4 * q + 1] += __uint_as_float(x.y);
+                                v[4 * q + 2] += __uint_as_float(x.z);
+                                v[4 * q + 3] += __uint_as_float(x.w);
+                            }
+                        }
 #pragma unroll
                         for (int q = 0; q < 8; ++q)
                             st_shared_u4(tile + (q >> 2) * kTile + stg_off(lane, q & 3),
                                          make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
                                                     __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3])));
-                    } else if (p.out_type == kElemF16) {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            st_shared_u4(tile + stg_off(lane, q),
-                                         make_uint4(pack_x2<__half>(v[8 * q], v[8 * q + 1]), pack_x2<__half>(v[8 * q + 2], v[8 * q + 3]),
-                                                    pack_x2<__half>(v[8 * q + 4], v[8 * q + 5]), pack_x2<__half>(v[8 * q + 6], v[8 * q + 7])));
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            st_shared_u4(tile + stg_off(lane, q),
-                                         make_uint4(pack_x2<bf16>(v[8 * q], v[8 * q + 1]), pack_x2<bf16>(v[8 * q + 2], v[8 * q + 3]),
-                                                    pack_x2<bf16>(v[8 * q + 4], v[8 * q + 5]), pack_x2<bf16>(v[8 * q + 6], v[8 * q + 7])));
-                    }
-                    // by TMA unless rows past the last one would be written
-                    if (tma_out && (row0 + 32 <= n_rows || n_rows == p.M)) {
-                        fence_proxy_async_smem();
-                        __syncwarp();
-                        if (lane == 0) {
-                            if (left > 0 && row0 < n_rows) {
-                                tma_store_2d(&tmOut, tile, col0, row0);
-                                if (f32 && left > 16) tma_store_2d(&tmOut, tile + kTile, col0 + 16, row0);
-                            }
-                            bulk_commit();
-                        }
-                        ++stores;
-                    } else {
                         __syncwarp();
                         if (lane < left) {
-                            const int rows = n_rows - row0 < 32 ? n_rows - row0 : 32;
-                            for (int y = 0; y < rows; ++y) {
-                                const size_t o = (size_t)(row0 + y) * p.ld_out + col0 + lane;
-                                if (f32)
-                                    static_cast<uint32_t *>(p.out)[o] =
-                                        ld_shared_u1(tile + (lane >> 4) * kTile + stg_off(y, (lane >> 2) & 3) + (lane & 3) * 4);
-                                else
-                                    static_cast<uint16_t *>(p.out)[o] = ld_shared_u16(tile + stg_off(y, lane >> 3) + (lane & 7) * 2);
+                            uint32_t *dst = static_cast<uint32_t *>(p.out) + (size_t)row0 * p.ld_out + col0 + lane;
+                            for (int y = 0; y < rows; ++y) dst[(size_t)y * p.ld_out] = ld_shared_u1(at + stg_off(y, q0));
+                        }
+                    } else {
+                        // a 16-bit 32x32 tile; with a residual that came by TMA into the second tile,
+                        // results use the first
+                        const bool f16 = p.out_type == kElemF16;
+                        const uint32_t rtile = stg + kTile, tile = res ? stg : stg + (stores & 1) * kTile;
+                        if (res) {
+                            if (tma_res) {
+                                bool rok = mbar_wait(rbar, rph, c.abort_flag);
+                                if (!__all_sync(0xffffffffu, rok)) { ok = false; break; }
+                                rph ^= 1;
+                                res_pending = false;
+                            } else {  // (rows that are not 16-byte aligned: a column per lane)
+                                __syncwarp();
+                                if (lane < left) {
+                                    const unsigned short *src =
+                                        static_cast<const unsigned short *>(p.res) + (size_t)row0 * p.ld_res + col0 + lane;
+                                    const uint32_t at = rtile + (lane & 7) * 2;
+#pragma unroll 8
+                                    for (int y = 0; y < rows; ++y)
+                                        st_shared_u16(at + stg_off(y, lane >> 3), __ldg(src + (size_t)y * p.ld_res));
+                                }
+                                __syncwarp();
+                            }
+                            add_tile16(rtile, lane, f16, v);
+                            __syncwarp();
+                            if (tma_res) {
+                                if (i + 1 < PER) res_issue(w, t, i + 1);
+                                else if (wn.u < units) res_issue(wn, t + 1, 0);
                             }
                         }
+                        uint32_t o[16];
+                        if (f16) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) o[j] = pack_x2<__half>(v[2 * j], v[2 * j + 1]);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) o[j] = pack_x2<bf16>(v[2 * j], v[2 * j + 1]);
+                        }
+                        // the store that last used this tile has read it (lane 0 has the stores, the
+                        // other lanes empty groups: no branch)
+                        if (res) bulk_wait_read0();
+                        else bulk_wait_read1();
                         __syncwarp();
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            st_shared_u4(tile + stg_off(lane, q), make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]));
+                        // by TMA unless rows past the last one would be written
+                        if (tma_out && (row0 + 32 <= n_rows || n_rows == p.M)) {
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            tma_store_if(lane == 0 && left > 0 && row0 < n_rows, &tmOut, tile, col0, row0);
+                            bulk_commit();
+                            ++stores;
+                        } else {
+                            __syncwarp();
+                            if (lane < left) {
+                                unsigned short *dst = static_cast<unsigned short *>(p.out) + (size_t)row0 * p.ld_out + col0 + lane;
+                                const uint32_t at = tile + (lane & 7) * 2;
+                                for (int y = 0; y < rows; ++y)
+                                    dst[(size_t)y * p.ld_out] = ld_shared_u16(at + stg_off(y, lane >> 3));
+                            }
+                            __syncwarp();
+                        }
                     }
                 }
             }
@@ -616,9 +624,9 @@ cudaError_t launch_tile(const Mx4GemmArgs &a, int num_sms, cudaStream_t s, bool 
     const int es = a.out_type == kElemF32 ? 4 : 2;
     auto ok16 = [&](const void *q, long long ld) { return q && (reinterpret_cast<uintptr_t>(q) & 15) == 0 && ld * es % 16 == 0; };
     CUtensorMap tmOut = tmA, tmRes = tmA;
-    const int tma_res = ok16(a.res, a.ld_res) && a.out_type != kElemF32, tma_out = ok16(a.out, a.ld_out);
-    if ((tma_out && make_tmap_tile32(&tmOut, a.out, a.out_type, a.M, a.N, a.ld_out)) ||
-        (tma_res && make_tmap_tile32(&tmRes, a.res, a.out_type, a.M, a.N, a.ld_res)))
+    const int tma_res = ok16(a.res, a.ld_res) && a.out_type != kElemF32, tma_out = ok16(a.out, a.ld_out) && a.out_type != kElemF32;
+    if ((tma_out && make_tmap_tile16(&tmOut, a.out, a.out_type, a.M, a.N, a.ld_out)) ||
+        (tma_res && make_tmap_tile16(&tmRes, a.res, a.out_type, a.M, a.N, a.ld_res)))
         return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];

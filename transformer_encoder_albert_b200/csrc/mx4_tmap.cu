@@ -38,17 +38,15 @@ int make_tmap_u8(CUtensorMap *tm, const void *base, uint64_t rows, uint64_t cols
     return r == CUDA_SUCCESS ? 0 : -3;
 }
 
-int make_tmap_tile32(CUtensorMap *tm, const void *base, int type, uint64_t rows, uint64_t cols, uint64_t ld) {
+int make_tmap_tile16(CUtensorMap *tm, const void *base, int type, uint64_t rows, uint64_t cols, uint64_t ld) {
     const EncodeTiled fn = encode_fn();
     if (!fn) return -1;
-    const bool f32 = type == kElemF32;
     cuuint64_t dims[2] = {cols, rows};
-    cuuint64_t strides[1] = {ld * (f32 ? 4 : 2)};
-    cuuint32_t box[2] = {f32 ? 16u : 32u, 32};
+    cuuint64_t strides[1] = {ld * 2};
+    cuuint32_t box[2] = {32, 32};
     cuuint32_t es[2] = {1, 1};
-    CUresult r = fn(tm, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
-                            : type == kElemF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                    2, const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+    CUresult r = fn(tm, type == kElemF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+                    const_cast<void *>(base), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
                     CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? 0 : -3;
 }
