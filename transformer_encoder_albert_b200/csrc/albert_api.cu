@@ -346,7 +346,8 @@ int run_layers_mx4(albert_handle *h, Launch &L, int nseq, int max_len, long long
         q.scales = h->mA_scales;
         q.n_rows = h->n_rows;
         q.status = h->status;
-        return q;  // (trigger 0: see the E4M3 quantizer)
+        q.trigger = 1;  // (its grid is resident at once: the product's CTAs take SMs it has left)
+        return q;
     };
     auto norm = [&](void *y, const float *g, const float *b) -> int {
         Mx4NormArgs a{rows(h->Z), g, b, c.ln_eps, y, kHidden};

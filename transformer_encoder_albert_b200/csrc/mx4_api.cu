@@ -186,6 +186,8 @@ int albert_mx4_linear(const albert_mx4_linear_args *p, void *stream) {
         q.tensor_scale = nv ? p->x_scale : 1.0f;
         q.codes = static_cast<uint8_t *>(p->workspace);
         q.scales = q.codes + up16(codes_bytes(p->rows, p->k));
+        // (its grid is resident at once, so the product's CTAs only take SMs it has left)
+        q.trigger = 1;
         if ((e = launch_mx4_quant(q, s, false)) != cudaSuccess) return ALBERT_ERR_CUDA;
         g.a = q.codes;
         g.a_scales = q.scales;
