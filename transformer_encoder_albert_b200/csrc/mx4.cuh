@@ -256,9 +256,14 @@ __device__ __forceinline__ uint32_t mx4_warp_quant(const float (&v)[8], uint32_t
     m = umax(m, __shfl_xor_sync(0xffffffffu, m, 1));
     if constexpr (!NV) m = umax(m, __shfl_xor_sync(0xffffffffu, m, 2));
     const Mx4Scale s = mx4_block_scale<NV>(m, ts, six_ts);
+    const uint64_t mul2 = f2_make(s.mul, s.mul);
     float y[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = __fmul_rn(v[i], s.mul);
+    for (int i = 0; i < 8; i += 2) {
+        const float2 f = f2_split(f2_mul(f2_make(v[i], v[i + 1]), mul2));
+        y[i] = f.x;
+        y[i + 1] = f.y;
+    }
     uint32_t q = cvt_e2m1x8(y);
     if (s.zero) q = 0;
     constexpr int kLanes = NV ? 2 : 4;  // lanes of a block

@@ -9,6 +9,7 @@
 // compared two at a time; whole chunks take a path without bounds.  A half-warp
 // covers 256 columns of a row, a warp the rows r and r + 32 of a 128-row scale tile,
 // and the next such pair's loads are in flight while one is converted.
+#include <algorithm>
 #include <type_traits>
 
 #include "mx4.cuh"
@@ -51,6 +52,10 @@ struct Walk {
 __device__ __forceinline__ void ld_global_v8(const void *p, uint32_t *w) {
     asm("ld.global.nc.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7]) : "l"(p));
+}
+__device__ __forceinline__ void ld_cached_v8(const float *p, float (&v)[8]) {
+    asm("ld.global.nc.v8.f32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]) : "l"(p));
 }
 __device__ __forceinline__ void st_global_v8(void *p, const uint32_t *w) {
     asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
@@ -249,58 +254,90 @@ mx4_norm_warp_kernel(const T *__restrict__ x, long long ld, const float *__restr
             raw[c] = load_raw8<T>(x + (size_t)r * ld + col, r < nr ? cols - col : 0, vec != 0);
         }
     };
-    if (row < nr) load(row);
-    for (; row < nr; row += stride) {
-        float v[NCH][8];
-        float sum = 0.f;
+    // One row.  WHOLE: all 256 NCH columns exist, so nothing is masked.
+    auto one_row = [&](auto whole) {
+        constexpr bool WHOLE = decltype(whole)::value;
+        uint64_t v[NCH][4];  // fp32 pairs
+        uint64_t s2 = f2_make(0.f, 0.f);
 #pragma unroll
         for (int c = 0; c < NCH; ++c) {
-            raw8_values<T>(raw[c], v[c]);
+            float f[8];
+            raw8_values<T>(raw[c], f);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) sum += v[c][i];
+            for (int i = 0; i < 4; ++i) {
+                v[c][i] = f2_make(f[2 * i], f[2 * i + 1]);
+                s2 = f2_add(s2, v[c][i]);
+            }
         }
         if (row + stride < nr) load(row + stride);
+        const float2 sf = f2_split(s2);
+        float sum = sf.x + sf.y;
 #pragma unroll
         for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         const float mean = sum / (float)cols;
-        float sq = 0.f;
+        const uint64_t nmean2 = f2_make(-mean, -mean);
+        uint64_t q2 = f2_make(0.f, 0.f);
 #pragma unroll
         for (int c = 0; c < NCH; ++c) {
             const int n = cols - c * kMx4StageCols - lane * 8;
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float d = i < n ? v[c][i] - mean : 0.f;
-                v[c][i] = d;
-                sq = fmaf(d, d, sq);
+            for (int i = 0; i < 4; ++i) {
+                v[c][i] = f2_add(v[c][i], nmean2);
+                if (!WHOLE) {
+                    const float2 d = f2_split(v[c][i]);
+                    v[c][i] = f2_make(2 * i < n ? d.x : 0.f, 2 * i + 1 < n ? d.y : 0.f);
+                }
+                q2 = f2_fma(v[c][i], v[c][i], q2);
             }
         }
+        const float2 qf = f2_split(q2);
+        float sq = qf.x + qf.y;
 #pragma unroll
         for (int o = 16; o; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
         const float rstd = rsqrtf(sq / (float)cols + eps);
+        const uint64_t rstd2 = f2_make(rstd, rstd);
 #pragma unroll
         for (int c = 0; c < NCH; ++c) {
-            if (c >= chunks) break;
+            if (!WHOLE && c >= chunks) break;
             const int col = c * kMx4StageCols + lane * 8, n = cols - col;
-            float g[8], b[8];
-            load8<float>(gamma + col, n, vec_g != 0, g);  // (columns past the end: 0, and so the result)
-            load8<float>(beta + col, n, vec_g != 0, b);
-            uint32_t m = 0;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                v[c][i] = fmaf(v[c][i] * rstd, g[i], b[i]);
-                if (i >= n) v[c][i] = 0.f;
-                m = umax(m, abs_bits(v[c][i]));
+            float g[8], b[8], u[8];
+            if (WHOLE) {  // (one 32-byte access a lane: two of 16 bytes cost L1 twice the lines)
+                ld_cached_v8(gamma + col, g);
+                ld_cached_v8(beta + col, b);
+            } else {
+                load8<float>(gamma + col, n, vec_g != 0, g);
+                load8<float>(beta + col, n, vec_g != 0, b);  // (0 past the end, and so the result)
             }
-            if (y) store8<T>(y + (size_t)row * ld_y + col, n, vec_y != 0, v[c]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = f2_split(f2_fma(f2_mul(v[c][i], rstd2), f2_make(g[2 * i], g[2 * i + 1]), f2_make(b[2 * i], b[2 * i + 1])));
+                u[2 * i] = f.x;
+                u[2 * i + 1] = f.y;
+            }
+            if (!WHOLE) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    if (i >= n) u[i] = 0.f;  // (not NaN, where the row's statistics are)
+            }
+            float m = fmax3_abs_nan(u[0], u[1], u[2]);
+            m = fmax3_abs_nan(m, u[3], u[4]);
+            m = fmax3_abs_nan(m, u[5], fmax3_abs_nan(u[6], u[7], 0.f));
+            if (y) store8<T>(y + (size_t)row * ld_y + col, WHOLE ? 8 : n, WHOLE || vec_y != 0, u);
             uint32_t word;
-            const uint32_t q = mx4_warp_quant<NV>(v[c], m, ts, six_ts, lane, word);
-            if (col / 2 < pitch) *reinterpret_cast<uint32_t *>(codes + (size_t)row * pitch + col / 2) = q;
+            const uint32_t q = mx4_warp_quant<NV>(u, abs_bits(m), ts, six_ts, lane, word);
+            if (WHOLE || col / 2 < pitch) *reinterpret_cast<uint32_t *>(codes + (size_t)row * pitch + col / 2) = q;
             constexpr int kTileLanes = Mx4<NV>::kTileCols / 8;
             if (lane % kTileLanes == 0)
                 *reinterpret_cast<uint32_t *>(scales + scale_word_offset(row, c * Mx4<NV>::kStageTiles + lane / kTileLanes,
                                                                          row_tiles)) = word;
         }
-    }
+    };
+    if (row < nr) load(row);
+    const bool whole = cols == NCH * kMx4StageCols && vec && vec_g == 2 && (!y || vec_y);
+    if (whole)
+        for (; row < nr; row += stride) one_row(std::true_type{});
+    else
+        for (; row < nr; row += stride) one_row(std::false_type{});
 }
 
 // The same with one CTA per row, for wider rows and for few of them: each warp holds
@@ -469,7 +506,7 @@ cudaError_t norm_launch(K kernel, std::atomic<int> (&cached)[64], int rows_per_c
     cudaError_t e = resident_grid(kernel, cached, (a.q.rows + rows_per_cta - 1) / rows_per_cta, blocks);
     if (e != cudaSuccess) return e;
     const int vec = aligned16(a.q.x, a.q.ld, sizeof(T)), vec_y = aligned16(a.y, a.ld_y, sizeof(T));
-    const int vec_g = aligned16(a.gamma, 4, 4) && aligned16(a.beta, 4, 4);
+    const int vec_g = std::min(vec_width(a.gamma, 8, 4), vec_width(a.beta, 8, 4));
     const float six = 6.0f * a.q.tensor_scale;
     if (pdl)
         return launch_pdl(kernel, dim3(blocks), dim3(32 * kQWarps), 0, s, static_cast<const T *>(a.q.x), a.q.ld, a.gamma,
