@@ -469,6 +469,16 @@ def length_regulate(logits, feats, cu_seqlens, speed: float = 1.0, max_frames: i
 MX4_FORMATS = {"mxfp4": ALBERT_MXFP4, "nvfp4": ALBERT_NVFP4}
 _MX4_TILES = {"mxfp4": 2, "nvfp4": 4}  # scale tiles per 256 columns
 _mx4_types: dict = {}
+_torch = None  # set with the first tensor (the module itself imports without torch)
+
+
+def _mx4_torch():
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+        _mx4_types.update({torch.bfloat16: ALBERT_BF16, torch.float32: ALBERT_FP32, torch.float16: ALBERT_FP16})
+    return _torch
 
 
 def mx4_shapes(rows: int, cols: int, fmt: str):
@@ -489,7 +499,7 @@ class Mx4Tensor:
     __slots__ = ("_buf", "_codes", "_scales", "_cptr", "_sptr", "_dev", "rows", "cols", "fmt", "tensor_scale")
 
     def __init__(self, codes, scales, rows: int, cols: int, fmt: str = "mxfp4", tensor_scale: float = 1.0):
-        import torch
+        torch = _torch or _mx4_torch()
         cs, ss = mx4_shapes(rows, cols, fmt)
         u8 = torch.uint8
         if codes.shape != cs or codes.dtype != u8 or not codes.is_contiguous():
@@ -541,7 +551,7 @@ def _mx4_scale(fmt: str, tensor_scale) -> float:
 
 def mx4_empty(rows: int, cols: int, fmt: str = "mxfp4", tensor_scale: float = 1.0, device="cuda") -> Mx4Tensor:
     """A 4-bit matrix with uninitialised contents (codes and scales in one allocation)."""
-    import torch
+    torch = _torch or _mx4_torch()
     c, s = mx4_shapes(rows, cols, fmt)
     t = Mx4Tensor.__new__(Mx4Tensor)
     off = (c[0] * c[1] + 127) // 128 * 128
@@ -555,9 +565,6 @@ def mx4_empty(rows: int, cols: int, fmt: str = "mxfp4", tensor_scale: float = 1.
 
 
 def _mx4_type(dtype, what: str) -> int:
-    if not _mx4_types:
-        import torch
-        _mx4_types.update({torch.bfloat16: ALBERT_BF16, torch.float32: ALBERT_FP32, torch.float16: ALBERT_FP16})
     code = _mx4_types.get(dtype)
     if code is None:
         raise ValueError(f"{what} must be bfloat16, float16 or float32, got {dtype}")
@@ -565,7 +572,7 @@ def _mx4_type(dtype, what: str) -> int:
 
 
 def _mx4_grad(t, what: str) -> None:
-    import torch
+    torch = _torch or _mx4_torch()
     if torch.is_grad_enabled():
         raise ValueError(f"{what} requires grad: the 4-bit operators have no backward pass (use torch.no_grad())")
 
@@ -573,6 +580,8 @@ def _mx4_grad(t, what: str) -> None:
 def _mx4_rows(t, what: str, dev: int | None = None, shape=None):
     """Check a matrix of rows on a GPU (unit column stride, any row stride without
     overlap); (rows, cols, row stride, device ordinal)."""
+    if _torch is None:
+        _mx4_torch()
     where = t.get_device()
     if where < 0 or t.dim() != 2:
         raise ValueError(f"{what} must be a 2-D CUDA tensor, got {tuple(t.shape)} on {t.device}")
@@ -591,7 +600,7 @@ def _mx4_rows(t, what: str, dev: int | None = None, shape=None):
 
 
 def _mx4_vector(t, n: int, what: str, dev: int) -> int:
-    import torch
+    torch = _torch or _mx4_torch()
     if t.shape != (n,) or t.dtype != torch.float32 or t.get_device() != dev or (n > 1 and t.stride(0) != 1):
         raise ValueError(f"{what} must be a contiguous float32 tensor of shape ({n},) on cuda:{dev}, "
                          f"got {tuple(t.shape)} {t.dtype} on {t.device}")
@@ -602,14 +611,13 @@ def _mx4_vector(t, n: int, what: str, dev: int) -> int:
 
 def _mx4_away(dev: int, stream) -> bool:
     """Whether a call must first switch to another device or stream."""
-    import torch
     if dev < 0:
         raise ValueError("4-bit matrices must be on a CUDA device")
-    return stream is not None or torch.cuda.current_device() != dev
+    return stream is not None or _torch._C._cuda_getDevice() != dev
 
 
 def _mx4_on(dev: int, stream):
-    import torch
+    torch = _torch or _mx4_torch()
     if stream is None:
         return torch.cuda.device(dev)
     if stream.device.index != dev:
@@ -618,8 +626,7 @@ def _mx4_on(dev: int, stream):
 
 
 def _mx4_stream(dev: int) -> int:
-    import torch
-    return torch._C._cuda_getCurrentRawStream(dev)
+    return _torch._C._cuda_getCurrentRawStream(dev)
 
 
 def mx4_quantize(x, fmt: str = "mxfp4", tensor_scale: float = 1.0, out: Mx4Tensor | None = None, stream=None) -> Mx4Tensor:
@@ -645,7 +652,7 @@ def mx4_quantize(x, fmt: str = "mxfp4", tensor_scale: float = 1.0, out: Mx4Tenso
 
 def mx4_dequantize(t: Mx4Tensor, dtype=None, out=None, stream=None):
     """The values of a 4-bit matrix, rounded once to `dtype` (default bfloat16)."""
-    import torch
+    torch = _torch or _mx4_torch()
     dev = t._dev
     if _mx4_away(dev, stream):
         with _mx4_on(dev, stream):
@@ -669,7 +676,7 @@ def mx4_layer_norm(x, gamma, beta, eps: float = 1e-12, fmt: str = "mxfp4", tenso
                    return_rows: bool = True, stream=None):
     """LayerNorm over the rows of x: (y in x's dtype, or None if not return_rows;
     the 4-bit form of the fp32 result) in one pass (albert_mx4_layer_norm)."""
-    import torch
+    torch = _torch or _mx4_torch()
     rows, cols, ld, dev = _mx4_rows(x, "x")
     typ = _mx4_type(x.dtype, "x")
     if _mx4_away(dev, stream):
@@ -686,7 +693,7 @@ def mx4_layer_norm(x, gamma, beta, eps: float = 1e-12, fmt: str = "mxfp4", tenso
 
 
 def _mx4_linear(x, w: Mx4Tensor, bias, residual, gelu, x_scale, stream, out, dtype, q_scale):
-    import torch
+    torch = _torch or _mx4_torch()
     packed = isinstance(x, Mx4Tensor)
     if packed:
         rows, k, dev = x.rows, x.cols, x._dev
@@ -750,7 +757,7 @@ def mx4_linear(x, w: Mx4Tensor, bias=None, residual=None, gelu: bool = False, dt
     mx4_quantize does, or a 4-bit matrix of w's format.  w: [n, k] 4-bit weights.
     bias [n] fp32; residual [rows, n] of the result's dtype (default bfloat16)."""
     if out is None and dtype is None:
-        import torch
+        torch = _torch or _mx4_torch()
         dtype = torch.bfloat16
     return _mx4_linear(x, w, bias, residual, gelu, x_scale, stream, out, dtype, None)
 

@@ -63,51 +63,69 @@ __device__ __forceinline__ void st_shared_u1(uint32_t a, uint32_t v) {
 // Rows r0 .. r0 + 2 PAIRS - 1 of a 256-column stage of the tokens, by a warp: a
 // half-warp per row, 16 columns a lane; the row pairs' loads and chains of dependent
 // instructions overlap (rows past the last read as 0 and are not stored).
-template <typename T, bool NV, int PAIRS>
-__device__ __forceinline__ void stage_rows(const Mx4TokArgs &p, int r0, int col, uint32_t codes, uint32_t scales, int sub,
-                                           int half) {
+template <typename T, int PAIRS>
+struct TokenRows {
     Raw8<T> a[PAIRS], b[PAIRS];
+    __device__ __forceinline__ void load(const Mx4TokArgs &p, int r0, int kb, int lane) {
+        const int col = kb * kMx4StageCols + (lane & 15) * 16;
 #pragma unroll
-    for (int i = 0; i < PAIRS; ++i) {
-        const int row = r0 + 2 * i + half;
-        const T *src = static_cast<const T *>(p.x) + (size_t)row * p.ld_x + col;
-        const int n = row < p.M ? p.K - col : 0;
-        a[i] = load_raw8<T>(src, n, p.vec_x != 0);
-        b[i] = load_raw8<T>(src + 8, n - 8, p.vec_x != 0);
-    }
-#pragma unroll
-    for (int i = 0; i < PAIRS; ++i) {
-        const int row = r0 + 2 * i + half;
-        uint32_t m = umax(raw8_amax<T>(a[i]), raw8_amax<T>(b[i]));
-        if constexpr (!NV) m = umax(m, __shfl_xor_sync(0xffffffffu, m, 1));
-        const Mx4Scale s = mx4_block_scale<NV>(amax_f32_bits<T>(m), p.x_ts, 6.0f * p.x_ts);
-        float v[8], u[8];
-        raw8_values<T>(a[i], v);
-        raw8_values<T>(b[i], u);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            v[e] = __fmul_rn(v[e], s.mul);
-            u[e] = __fmul_rn(u[e], s.mul);
-        }
-        const uint2 q = s.zero ? make_uint2(0, 0) : make_uint2(cvt_e2m1x8(v), cvt_e2m1x8(u));
-        constexpr int kLanes = NV ? 1 : 2, kTileLanes = 4 * kLanes;
-        uint32_t word = s.byte << (8 * ((sub / kLanes) & 3));
-        word |= __shfl_xor_sync(0xffffffffu, word, kLanes);
-        word |= __shfl_xor_sync(0xffffffffu, word, 2 * kLanes);
-        if (row < p.M) {
-            // 128-byte rows with the 128-byte swizzle (16-byte chunk index XOR row % 8)
-            st_shared_u2(codes + row * 128 + (((sub >> 1) ^ (row & 7)) << 4) + (sub & 1) * 8, q);
-            if (sub % kTileLanes == 0) st_shared_u1(scales + (sub / kTileLanes) * kMx4TileBytes + row * 16, word);
+        for (int i = 0; i < PAIRS; ++i) {
+            const int row = r0 + 2 * i + (lane >> 4);
+            const T *src = static_cast<const T *>(p.x) + (size_t)row * p.ld_x + col;
+            const int n = row < p.M ? p.K - col : 0;
+            a[i] = load_raw8<T>(src, n, p.vec_x != 0);
+            b[i] = load_raw8<T>(src + 8, n - 8, p.vec_x != 0);
         }
     }
-}
-template <typename T, bool NV>
-__device__ __forceinline__ void stage_tokens(const Mx4TokArgs &p, int kb, uint32_t codes, uint32_t scales, int lane) {
-    const int sub = lane & 15, half = lane >> 4, col = kb * kMx4StageCols + sub * 16;
-    if (p.M <= 2) {
-        stage_rows<T, NV, 1>(p, 0, col, codes, scales, sub, half);
-    } else {
-        for (int r0 = 0; r0 < p.M; r0 += 8) stage_rows<T, NV, 4>(p, r0, col, codes, scales, sub, half);
+    template <bool NV>
+    __device__ __forceinline__ void quantize(const Mx4TokArgs &p, int r0, uint32_t codes, uint32_t scales, int lane) const {
+        const int sub = lane & 15;
+#pragma unroll
+        for (int i = 0; i < PAIRS; ++i) {
+            const int row = r0 + 2 * i + (lane >> 4);
+            uint32_t m = umax(raw8_amax<T>(a[i]), raw8_amax<T>(b[i]));
+            if constexpr (!NV) m = umax(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            const Mx4Scale s = mx4_block_scale<NV>(amax_f32_bits<T>(m), p.x_ts, 6.0f * p.x_ts);
+            float v[8], u[8];
+            raw8_values<T>(a[i], v);
+            raw8_values<T>(b[i], u);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                v[e] = __fmul_rn(v[e], s.mul);
+                u[e] = __fmul_rn(u[e], s.mul);
+            }
+            const uint2 q = s.zero ? make_uint2(0, 0) : make_uint2(cvt_e2m1x8(v), cvt_e2m1x8(u));
+            constexpr int kLanes = NV ? 1 : 2, kTileLanes = 4 * kLanes;
+            uint32_t word = s.byte << (8 * ((sub / kLanes) & 3));
+            word |= __shfl_xor_sync(0xffffffffu, word, kLanes);
+            word |= __shfl_xor_sync(0xffffffffu, word, 2 * kLanes);
+            if (row < p.M) {
+                // 128-byte rows with the 128-byte swizzle (16-byte chunk index XOR row % 8)
+                st_shared_u2(codes + row * 128 + (((sub >> 1) ^ (row & 7)) << 4) + (sub & 1) * 8, q);
+                if (sub % kTileLanes == 0) st_shared_u1(scales + (sub / kTileLanes) * kMx4TileBytes + row * 16, word);
+            }
+        }
+    }
+};
+
+// A warp's stages i = first, first + ring, ... of the tokens.  The first rows of the
+// next stage load while the current one is converted and while its slot is still being
+// read: reading them after the wait left each stage to the latency of L2.
+template <typename T, bool NV, int PAIRS, typename Slot>
+__device__ __forceinline__ void feed_tokens(const Mx4TokArgs &p, int first, int kb0, int nkb, int ring, int lane, Slot slot) {
+    TokenRows<T, PAIRS> now, next;
+    if (first < nkb) next.load(p, 0, kb0 + first, lane);
+    for (int i = first; i < nkb; i += ring) {
+        now = next;
+        if (i + ring < nkb) next.load(p, 0, kb0 + i + ring, lane);
+        uint32_t codes, scales;
+        if (!slot.take(codes, scales)) return;
+        now.template quantize<NV>(p, 0, codes, scales, lane);
+        for (int r0 = 2 * PAIRS; r0 < p.M; r0 += 2 * PAIRS) {
+            now.load(p, r0, kb0 + i, lane);
+            now.template quantize<NV>(p, r0, codes, scales, lane);
+        }
+        slot.give();
     }
 }
 template <bool NV>
@@ -129,7 +147,7 @@ __device__ __forceinline__ void stage_packed(const Mx4TokArgs &p, int kb, uint32
 template <bool NV, int NT>
 __global__ void __launch_bounds__(kTokThreads)
 mx4_tokens_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmSW, const Mx4TokArgs p,
-                  int ring, int nclu) {
+                  int ring, int nclu, int stream_w) {
     using P = TokPlan<NV, NT>;
     constexpr int ST = P::ST;
     extern __shared__ uint8_t smem_raw[];
@@ -156,7 +174,7 @@ mx4_tokens_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
             mbar_init(smem_u32(&full[i]), 1);
             mbar_init(smem_u32(&empty[i]), 1);
             mbar_init(smem_u32(&ready[i]), 32);
-            mbar_init(smem_u32(&scaled[i]), 1);
+            mbar_init(smem_u32(&scaled[i]), 2);
         }
         mbar_init(smem_u32(done), 2);
         fence_mbar_init();
@@ -172,6 +190,7 @@ mx4_tokens_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
 
     if (warp == 0) {
         if (lane == 0) {
+            const uint64_t once = policy_evict_first();
             int stage = 0, issued = 0;
             uint32_t phase = 0;
             bool ok = true;
@@ -179,7 +198,10 @@ mx4_tokens_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
                 if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1, abort_flag)) { ok = false; break; }
                 const uint32_t fb = smem_u32(&full[stage]);
                 mbar_arrive_expect_tx(fb, P::RING);
-                tma_load_2d(smem_u32(sW) + stage * kWBytes, &tmW, fb, kb * 128, tile * 128);
+                if (stream_w)
+                    tma_load_2d_hint(smem_u32(sW) + stage * kWBytes, &tmW, fb, kb * 128, tile * 128, once);
+                else
+                    tma_load_2d(smem_u32(sW) + stage * kWBytes, &tmW, fb, kb * 128, tile * 128);
                 tma_load_2d(smem_u32(sSW) + stage * ST * kMx4TileBytes, &tmSW, fb, 0, (tile * stages + kb) * 2 * ST);
                 ++issued;
                 if (++stage == ring) { stage = 0; phase ^= 1; }
@@ -198,10 +220,9 @@ mx4_tokens_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
         };
         uint32_t stage = 0, phase = 0;
         for (int i = 0; i < nkb; ++i) {
-            // (both warps: what the copies read, the products read too)
-            if (!wait(&ready[stage], phase) || !wait(&full[stage], phase)) break;
             const uint32_t ca = tmem + NT + stage * P::SFCOLS, cb = ca + 4 * ST;
             if (warp == 1) {
+                // the scale warp, which has waited for the stage's operands, arrives here too
                 if (!wait(&scaled[stage], phase)) break;
                 tc_fence_after();
                 const uint32_t w0 = smem_u32(sW) + stage * kWBytes, t0 = smem_u32(sT) + stage * NT * 128;
@@ -213,6 +234,7 @@ mx4_tokens_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
                 }
                 umma_commit_elected<false>(leader, smem_u32(empty) + 8 * stage, 0);
             } else {
+                if (!wait(&full[stage], phase) || !wait(&ready[stage], phase)) break;
                 tc_fence_after();
                 const uint32_t fw = smem_u32(sSW) + stage * ST * kMx4TileBytes, ft = smem_u32(sST) + stage * ST * kMx4TileBytes;
 #pragma unroll
@@ -221,6 +243,7 @@ mx4_tokens_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
                     tmem_cp_scales<false>(leader, cb + 4 * g, scale_tile_desc(ft + g * kMx4TileBytes));
                 }
                 umma_commit_elected<false>(leader, smem_u32(scaled) + 8 * stage, 0);
+                if (lane == 0) mbar_arrive(smem_u32(scaled) + 8 * stage);
             }
             if (++stage == (uint32_t)ring) { stage = 0; phase ^= 1; }
         }
@@ -232,17 +255,40 @@ mx4_tokens_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
         const int wk = warp - 2;
         // warp `stage` fills that ring stage every time, so that it never waits for a phase
         // two ahead of the barrier's (more warps than stages would)
-        const int stage = wk;
-        uint32_t phase = 1;
-        for (int i = wk; wk < ring && i < nkb; i += ring, phase ^= 1) {
-            if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&empty[stage]), phase, abort_flag))) break;
-            const uint32_t codes = smem_u32(sT) + stage * NT * 128, scales = smem_u32(sST) + stage * ST * kMx4TileBytes;
-            if (!p.x) stage_packed<NV>(p, kb0 + i, codes, scales, lane);
-            else if (p.x_type == kElemF32) stage_tokens<float, NV>(p, kb0 + i, codes, scales, lane);
-            else if (p.x_type == kElemF16) stage_tokens<__half, NV>(p, kb0 + i, codes, scales, lane);
-            else stage_tokens<bf16, NV>(p, kb0 + i, codes, scales, lane);
-            fence_proxy_async_smem();  // the products read this through the async proxy
-            mbar_arrive(smem_u32(&ready[stage]));
+        struct Slot {
+            uint32_t codes, scales, empty, ready, phase;
+            volatile int *abort_flag;
+            __device__ bool take(uint32_t &c, uint32_t &s) {
+                c = codes;
+                s = scales;
+                const bool ok = __all_sync(0xffffffffu, mbar_wait(empty, phase, abort_flag));
+                phase ^= 1;
+                return ok;
+            }
+            __device__ void give() {
+                fence_proxy_async_smem();  // the products read this through the async proxy
+                mbar_arrive(ready);
+            }
+        } sl{smem_u32(sT) + wk * NT * 128, smem_u32(sST) + wk * ST * kMx4TileBytes, smem_u32(&empty[wk]),
+             smem_u32(&ready[wk]), 1, abort_flag};
+        if (wk < ring) {
+            if (!p.x) {
+                for (int i = wk; i < nkb; i += ring) {
+                    uint32_t codes, scales;
+                    if (!sl.take(codes, scales)) break;
+                    stage_packed<NV>(p, kb0 + i, codes, scales, lane);
+                    sl.give();
+                }
+            } else if (p.x_type == kElemF32) {
+                if (p.M <= 2) feed_tokens<float, NV, 1>(p, wk, kb0, nkb, ring, lane, sl);
+                else feed_tokens<float, NV, 2>(p, wk, kb0, nkb, ring, lane, sl);
+            } else if (p.x_type == kElemF16) {
+                if (p.M <= 2) feed_tokens<__half, NV, 1>(p, wk, kb0, nkb, ring, lane, sl);
+                else feed_tokens<__half, NV, 4>(p, wk, kb0, nkb, ring, lane, sl);
+            } else {
+                if (p.M <= 2) feed_tokens<bf16, NV, 1>(p, wk, kb0, nkb, ring, lane, sl);
+                else feed_tokens<bf16, NV, 4>(p, wk, kb0, nkb, ring, lane, sl);
+            }
         }
     }
     // ------------------------------------------------------------- epilogue --
@@ -336,6 +382,10 @@ cudaError_t launch_tok(const Mx4TokArgs &a, int num_sms, cudaStream_t s) {
     const uint64_t st = (uint64_t)((a.N + 127) / 128) * stages * P::ST;
     if (make_tmap_u8(&tmW, a.w, a.N, pitch, 128, 128, true) || make_tmap_u8(&tmSW, a.w_scales, 2 * st, 256, 256, 2 * P::ST, false))
         return cudaErrorInvalidValue;
+    // A matrix of more than a quarter of L2 (126 MB) does not last there until its next use,
+    // behind the layers in between: it passes through (16384 x 8192: 18.0 us against 19.2);
+    // a smaller one stays.
+    const int stream_w = (long long)a.N * pitch > 32ll << 20;
     static std::atomic<unsigned long long> done{0};
     cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(mx4_tokens_kernel<NV, NT>), P::smem(kMaxRing), done);
     if (e != cudaSuccess) return e;
@@ -351,7 +401,7 @@ cudaError_t launch_tok(const Mx4TokArgs &a, int num_sms, cudaStream_t s) {
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = nclu > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, mx4_tokens_kernel<NV, NT>, tmW, tmSW, a, ring, nclu);
+    return cudaLaunchKernelEx(&cfg, mx4_tokens_kernel<NV, NT>, tmW, tmSW, a, ring, nclu, stream_w);
 }
 
 }  // namespace
