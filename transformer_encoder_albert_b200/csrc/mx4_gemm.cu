@@ -653,9 +653,17 @@ cudaError_t launch_tile(const Mx4GemmArgs &a, int num_sms, cudaStream_t s, bool 
 
 template <bool NV, bool QOUT>
 cudaError_t launch_fmt(const Mx4GemmArgs &a, int num_sms, cudaStream_t s, bool pdl) {
-    // pairs when their tiles fill the machine
-    const long long pair_units = (long long)((a.M + 255) / 256) * ((a.N + 255) / 256);
-    if (pair_units >= num_sms / 2) return launch_tile<NV, true, QOUT>(a, num_sms, s, pdl);
+    // The cheaper of the two shapes by their waves: measured over 256..9000 rows, N 768..4096,
+    // K 768..4096 (stages 3, 8, 16), a launch takes about 4.4 us + waves (0.6 + 0.30 stages)
+    // on single 128x128 tiles and 5.6 us + waves (0.7 + 0.44 stages) on pairs' 256x256 tiles
+    // (3000x2304x768: 9.1 against 9.7; 4096x2304x768: 10.3 against 10.0; 2048x4096x4096:
+    // 25.7 against 20.8).
+    const int stages = mx4_stages(a.K);
+    const long long single = (long long)((a.M + 127) / 128) * ((a.N + 127) / 128);
+    const long long pair = (long long)((a.M + 255) / 256) * ((a.N + 255) / 256);
+    const long long waves1 = (single + num_sms - 1) / num_sms, waves2 = (pair + num_sms / 2 - 1) / (num_sms / 2);
+    if (560 + waves2 * (70 + 44 * stages) < 440 + waves1 * (60 + 30 * stages))
+        return launch_tile<NV, true, QOUT>(a, num_sms, s, pdl);
     return launch_tile<NV, false, QOUT>(a, num_sms, s, pdl);
 }
 

@@ -112,27 +112,40 @@ struct TokenRows {
 // next stage load while the current one is converted and while its slot is still being
 // read: reading them after the wait left each stage to the latency of L2.
 template <typename T, bool NV, int PAIRS, typename Slot>
-__device__ __forceinline__ void feed_tokens(const Mx4TokArgs &p, int first, int kb0, int nkb, int ring, int lane, Slot slot) {
+__device__ __forceinline__ void feed_tokens(const Mx4TokArgs &p, int first, int kb0, int nkb, int ring, int part, int parts,
+                                            int lane, Slot slot) {
     TokenRows<T, PAIRS> now, next;
-    if (first < nkb) next.load(p, 0, kb0 + first, lane);
+    const int own = part * 2 * PAIRS, step = parts * 2 * PAIRS;  // this warp's rows of a stage
+    if (first < nkb) next.load(p, own, kb0 + first, lane);
     for (int i = first; i < nkb; i += ring) {
         now = next;
-        if (i + ring < nkb) next.load(p, 0, kb0 + i + ring, lane);
+        if (i + ring < nkb) next.load(p, own, kb0 + i + ring, lane);
         uint32_t codes, scales;
         if (!slot.take(codes, scales)) return;
-        now.template quantize<NV>(p, 0, codes, scales, lane);
-        for (int r0 = 2 * PAIRS; r0 < p.M; r0 += 2 * PAIRS) {
+        if (own < p.M) now.template quantize<NV>(p, own, codes, scales, lane);
+        for (int r0 = own + step; r0 < p.M; r0 += step) {
             now.load(p, r0, kb0 + i, lane);
             now.template quantize<NV>(p, r0, codes, scales, lane);
         }
         slot.give();
     }
 }
+// No more row pairs per warp than the tokens need: a chain of four pairs takes about
+// 1.5 us, of one 0.5 us.
+template <typename T, bool NV, typename Slot>
+__device__ __forceinline__ void feed_any(const Mx4TokArgs &p, int first, int kb0, int nkb, int ring, int part, int parts,
+                                         int lane, Slot slot) {
+    if (p.M <= 2 * parts) feed_tokens<T, NV, 1>(p, first, kb0, nkb, ring, part, parts, lane, slot);
+    else if (p.M <= 4 * parts || sizeof(T) == 4) feed_tokens<T, NV, 2>(p, first, kb0, nkb, ring, part, parts, lane, slot);
+    else feed_tokens<T, NV, 4>(p, first, kb0, nkb, ring, part, parts, lane, slot);
+}
+
 template <bool NV>
-__device__ __forceinline__ void stage_packed(const Mx4TokArgs &p, int kb, uint32_t codes, uint32_t scales, int lane) {
+__device__ __forceinline__ void stage_packed(const Mx4TokArgs &p, int kb, int first, int step, uint32_t codes,
+                                             uint32_t scales, int lane) {
     constexpr int ST = Mx4<NV>::kStageTiles;
     const int sub = lane & 15, half = lane >> 4, pitch = mx4_code_pitch(p.K), byte = kb * 128 + sub * 8;
-    for (int r0 = 0; r0 < p.M; r0 += 2) {
+    for (int r0 = first; r0 < p.M; r0 += step) {
         const int row = r0 + half;
         if (row >= p.M) continue;
         uint2 q = make_uint2(0, 0);
@@ -173,7 +186,7 @@ mx4_tokens_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
         for (int i = 0; i < ring; ++i) {
             mbar_init(smem_u32(&full[i]), 1);
             mbar_init(smem_u32(&empty[i]), 1);
-            mbar_init(smem_u32(&ready[i]), 32);
+            mbar_init(smem_u32(&ready[i]), 32 * (kWorkers / ring));
             mbar_init(smem_u32(&scaled[i]), 2);
         }
         mbar_init(smem_u32(done), 2);
@@ -253,8 +266,9 @@ mx4_tokens_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
     } else {
         // ------------------------------------------------------------ tokens --
         const int wk = warp - 2;
-        // warp `stage` fills that ring stage every time, so that it never waits for a phase
-        // two ahead of the barrier's (more warps than stages would)
+        // a warp fills the same ring stage every time, so that it never waits for a phase two
+        // ahead of the barrier's; where the ring is short, several warps share a stage's rows
+        const int own = wk % ring, part = wk / ring, parts = kWorkers / ring;
         struct Slot {
             uint32_t codes, scales, empty, ready, phase;
             volatile int *abort_flag;
@@ -269,25 +283,22 @@ mx4_tokens_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
                 fence_proxy_async_smem();  // the products read this through the async proxy
                 mbar_arrive(ready);
             }
-        } sl{smem_u32(sT) + wk * NT * 128, smem_u32(sST) + wk * ST * kMx4TileBytes, smem_u32(&empty[wk]),
-             smem_u32(&ready[wk]), 1, abort_flag};
-        if (wk < ring) {
+        } sl{smem_u32(sT) + own * NT * 128, smem_u32(sST) + own * ST * kMx4TileBytes, smem_u32(&empty[own]),
+             smem_u32(&ready[own]), 1, abort_flag};
+        if (part < parts) {
             if (!p.x) {
-                for (int i = wk; i < nkb; i += ring) {
+                for (int i = own; i < nkb; i += ring) {
                     uint32_t codes, scales;
                     if (!sl.take(codes, scales)) break;
-                    stage_packed<NV>(p, kb0 + i, codes, scales, lane);
+                    stage_packed<NV>(p, kb0 + i, 2 * part, 2 * parts, codes, scales, lane);
                     sl.give();
                 }
             } else if (p.x_type == kElemF32) {
-                if (p.M <= 2) feed_tokens<float, NV, 1>(p, wk, kb0, nkb, ring, lane, sl);
-                else feed_tokens<float, NV, 2>(p, wk, kb0, nkb, ring, lane, sl);
+                feed_any<float, NV>(p, own, kb0, nkb, ring, part, parts, lane, sl);
             } else if (p.x_type == kElemF16) {
-                if (p.M <= 2) feed_tokens<__half, NV, 1>(p, wk, kb0, nkb, ring, lane, sl);
-                else feed_tokens<__half, NV, 4>(p, wk, kb0, nkb, ring, lane, sl);
+                feed_any<__half, NV>(p, own, kb0, nkb, ring, part, parts, lane, sl);
             } else {
-                if (p.M <= 2) feed_tokens<bf16, NV, 1>(p, wk, kb0, nkb, ring, lane, sl);
-                else feed_tokens<bf16, NV, 4>(p, wk, kb0, nkb, ring, lane, sl);
+                feed_any<bf16, NV>(p, own, kb0, nkb, ring, part, parts, lane, sl);
             }
         }
     }
@@ -374,8 +385,10 @@ cudaError_t launch_tok(const Mx4TokArgs &a, int num_sms, cudaStream_t s) {
     const int stages = mx4_stages(a.K), pitch = mx4_code_pitch(a.K);
     // a 4-bit result's scale tiles reach to a multiple of 256 columns
     const int tiles = ((a.out ? a.N : mx4_stages(a.N) * kMx4StageCols) + 127) / 128;
-    int nclu = 1;
-    while (nclu < kMaxCluster && 2 * nclu <= stages && 2 * nclu * tiles <= num_sms) nclu *= 2;
+    // as many CTAs per tile as there are SMs for, stages of K, and the portable cluster size
+    int nclu = tiles < num_sms ? num_sms / tiles : 1;
+    nclu = nclu < stages ? nclu : stages;
+    nclu = nclu < kMaxCluster ? nclu : kMaxCluster;
     const int slice = (stages + nclu - 1) / nclu;
     const int ring = slice < kMaxRing ? slice : kMaxRing;
     CUtensorMap tmW, tmSW;
