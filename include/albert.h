@@ -356,9 +356,11 @@ size_t albert_length_regulate_scratch_bytes(int n_tok);
  * the current device, which must be the one the buffers are on.  Row strides
  * (ld*) are in elements and at least the row length; rows of x, y, residual and
  * out may have any alignment of their element type.  rows == 0 does nothing.
- * Host errors: ALBERT_ERR_NULL; ALBERT_ERR_SHAPE (rows < 0, a width outside
- * [1, 2^24], an ld below the row length); ALBERT_ERR_CONFIG (unknown format or
- * type, a tensor scale out of range, unaligned codes or scales). */
+ * A first call on a device loads the kernels; make one before capturing into a
+ * graph.  Scale bytes that a caller writes itself have a zero sign bit.
+ * Host errors: ALBERT_ERR_NULL; ALBERT_ERR_SHAPE (rows outside [0, 2^30], a width
+ * outside [1, 2^24], an ld below the row length); ALBERT_ERR_CONFIG (unknown format
+ * or type, a tensor scale out of range, unaligned codes or scales). */
 size_t albert_mx4_codes_bytes(int rows, int cols);
 size_t albert_mx4_scales_bytes(int rows, int cols, int fmt);
 
@@ -383,7 +385,11 @@ int albert_mx4_layer_norm(const void *x, int x_type, long long ld_x, const float
  * then out = z rounded once to out_type, or the 4-bit form of z (q_codes,
  * q_scales).  A [rows, k] is either 4-bit (a_codes, a_scales) or x of x_type,
  * which is quantized as albert_mx4_quantize does (same result as calling it).
- * W [n, k] is 4-bit, as albert_mx4_quantize leaves a weight matrix. */
+ * W [n, k] is 4-bit, as albert_mx4_quantize leaves a weight matrix.  residual and
+ * out may be the same rows.  Each row's result depends on that row alone.  At most
+ * 32 rows run in one kernel that quantizes x itself (no workspace); more take a
+ * quantization pass into the workspace, then the product.
+ * Further ALBERT_ERR_CONFIG: x_scale * w_scale outside [2^-100, 2^100]. */
 typedef struct {
     const void *x;             /* rows to quantize, or NULL                      */
     const void *a_codes;       /* 4-bit rows (x == NULL)                         */

@@ -319,6 +319,59 @@ def test_scales_over_their_range(fmt):
         assert np.all(np.abs(got - ref[:rows]) <= (tol + 2.0 ** -24 * np.abs(ref))[:rows])
 
 
+@pytest.mark.parametrize("rows", [9, 140])
+def test_far_apart_power_of_two_scales_cancel(rows):
+    """mxfp4 rows scaled by 2^e against weights scaled by 2^-e, e up to 100: the products are
+    those of e = 0."""
+    rng = np.random.default_rng(8)
+    x, w = rng.normal(0, 1, (rows, 320)).astype(np.float32), rng.normal(0, 1, (200, 320)).astype(np.float32)
+    ref = None
+    for e in (0, 100, -100):
+        xt = torch.tensor(x * np.float32(2.0 ** e)).cuda()
+        wt = tea.mx4_quantize(torch.tensor(w * np.float32(2.0 ** -e)).cuda(), "mxfp4")
+        y = tea.mx4_linear(xt, wt, dtype=torch.float32)
+        ref = y if ref is None else ref
+        assert torch.equal(y, ref)
+
+
+@pytest.mark.parametrize("rows", [6, 200])
+def test_gelu_far_from_zero(rows):
+    """GELU of +-1, +-30, +-1e5, +-1e20 next to one another in every order: x or 0, and no
+    value disturbs its neighbour."""
+    v = torch.tensor([1.0, -1.0, 30.0, -30.0, 1e5, -1e5, 1e20, -1e20, 0.0])
+    bias = torch.stack([torch.stack([a, b]) for a in v for b in v]).reshape(-1).cuda()
+    w = tea.mx4_quantize(torch.zeros(bias.numel(), 64, device="cuda"), "mxfp4")
+    y = _np(tea.mx4_linear(torch.randn(rows, 64, device="cuda"), w, bias=bias, gelu=True, dtype=torch.float32))
+    b = _np(bias)
+    ref = np.where(np.abs(b) > 10, np.maximum(b, 0), mq.gelu(np.where(np.abs(b) > 10, 0, b)))
+    assert np.all(np.abs(y - ref) <= 2.0 ** -17 * np.maximum(np.abs(b) * (np.abs(b) < 10), np.abs(ref)) + np.abs(b) * 2.0 ** -60)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("rows", [7, 300, 5000])
+def test_residual_in_place_equals_a_separate_result(rows, fmt):
+    x = torch.randn(rows, 256, device="cuda", dtype=torch.bfloat16)
+    w = tea.mx4_quantize(torch.randn(1040, 256, device="cuda"), fmt, 0.002)
+    r = torch.randn(rows, 1040, device="cuda", dtype=torch.bfloat16)
+    ref = tea.mx4_linear(x, w, residual=r, x_scale=TS[fmt])
+    same = r.clone()
+    out = tea.mx4_linear(x, w, residual=same, out=same, x_scale=TS[fmt])
+    assert out.data_ptr() == same.data_ptr() and torch.equal(out, ref)
+    assert torch.equal(ref, tea.mx4_linear(x, w, residual=r, x_scale=TS[fmt]))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_rows_of_a_batch_do_not_depend_on_its_size(fmt):
+    """The same rows in batches that take each kernel (few tokens, single tiles, pairs)."""
+    x = torch.randn(6000, 768, device="cuda", dtype=torch.bfloat16)
+    w = tea.mx4_quantize(torch.randn(2304, 768, device="cuda") * 0.05, fmt, 1e-4)
+    whole = tea.mx4_linear(x, w, x_scale=TS[fmt], dtype=torch.float32)
+    for n in (1, 20, 64, 300, 3000):
+        part = tea.mx4_linear(x[:n], w, x_scale=TS[fmt], dtype=torch.float32)
+        # sums of 768 products in another order: (K + 3) 2^-23 of their magnitudes, here as norms
+        assert torch.linalg.norm(part - whole[:n]) <= 771 * 2.0 ** -23 * torch.linalg.norm(whole[:n])
+
+
 def test_a_run_of_the_operators_as_a_feed_forward_block():
     """LayerNorm -> 4 bits -> up + GELU -> 4 bits -> down + residual, as used together, for one
     token, a few, and many; every row alone gives the row of the batch."""

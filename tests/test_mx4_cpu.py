@@ -144,12 +144,13 @@ def test_linear_refuses_on_the_host(lib):
     for kw in ({"w_codes": None}, {"w_scales": None}, {"a_codes": None}, {"a_scales": None}, {"out": None},
                {"out": None, "q_codes": P}, {"rows": 4000, "x": P, "ld_x": 64}):
         assert f(**kw) == NULL, kw
-    for kw in ({"rows": -1}, {"n": 0}, {"k": 0}, {"ld_out": 47}, {"residual": P, "ld_residual": 47},
+    for kw in ({"rows": -1}, {"rows": (1 << 30) + 1}, {"n": 0}, {"k": 0}, {"ld_out": 47}, {"residual": P, "ld_residual": 47},
                {"x": P, "ld_x": 63, "workspace": P}):
         assert f(**kw) == SHAPE, kw
     for kw in ({"fmt": 0}, {"out_type": 7}, {"x": P, "ld_x": 64, "x_type": 7, "workspace": P}, {"gelu": 2},
                {"w_codes": P + 8}, {"w_scales": P + 8}, {"a_codes": P + 8}, {"bias": P + 2}, {"out": P + 1},
                {"residual": P + 1, "ld_residual": 48}, {"fmt": 4, "w_scale": 0.0}, {"fmt": 4, "x_scale": float("nan")},
+               {"fmt": 4, "x_scale": 2.0 ** 60, "w_scale": 2.0 ** 60}, {"fmt": 4, "x_scale": 2.0 ** -60, "w_scale": 2.0 ** -60},
                {"out": None, "q_codes": P + 4, "q_scales": P}, {"fmt": 4, "out": None, "q_codes": P, "q_scales": P, "q_scale": -1.0}):
         assert f(**kw) == CONFIG, kw
     assert f(rows=0) == 0

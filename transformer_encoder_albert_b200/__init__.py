@@ -485,8 +485,8 @@ def mx4_shapes(rows: int, cols: int, fmt: str):
     """Shapes of the code and scale tensors of a [rows, cols] 4-bit matrix."""
     if fmt not in MX4_FORMATS:
         raise ValueError(f"format must be one of {sorted(MX4_FORMATS)}, got {fmt!r}")
-    if rows < 0 or not 1 <= cols <= 1 << 24:
-        raise ValueError(f"a 4-bit matrix has rows >= 0 and 1 <= cols <= 2^24, got [{rows}, {cols}]")
+    if not 0 <= rows <= 1 << 30 or not 1 <= cols <= 1 << 24:
+        raise ValueError(f"a 4-bit matrix has 0 <= rows <= 2^30 and 1 <= cols <= 2^24, got [{rows}, {cols}]")
     return (rows, (cols + 31) // 32 * 16), ((rows + 127) // 128, (cols + 255) // 256 * _MX4_TILES[fmt], 512)
 
 

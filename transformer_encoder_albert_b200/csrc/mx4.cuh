@@ -217,7 +217,7 @@ __device__ __forceinline__ uint64_t gelu_f2(uint64_t x) {
     const float2 df = f2_split(d);
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(df.x * df.y));
-    return f2_mul(f2_mul(x, f2_make(df.y, df.x)), f2_make(r, r));
+    return f2_mul(x, f2_mul(f2_make(df.y, df.x), f2_make(r, r)));  // (1 / d first: x d could overflow)
 }
 
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }

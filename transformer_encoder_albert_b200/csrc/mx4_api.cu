@@ -14,7 +14,7 @@ namespace {
 // Status word of the linear layers' bounded waits, one per device.
 __device__ int g_mx4_status;
 
-constexpr int kMaxCols = 1 << 24;
+constexpr int kMaxCols = 1 << 24, kMaxRows = 1 << 30;
 constexpr float kMinScale = 7.888609052210118e-31f, kMaxScale = 1.2676506002282294e30f;  // 2^-100, 2^100
 
 bool is_format(int fmt) { return fmt == ALBERT_MXFP4 || fmt == ALBERT_NVFP4; }
@@ -23,6 +23,7 @@ int elem_size(int t) { return t == ALBERT_FP32 ? 4 : 2; }
 bool scale_ok(int fmt, float ts) { return fmt == ALBERT_MXFP4 || (ts >= kMinScale && ts <= kMaxScale); }
 bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 bool cols_ok(int c) { return c >= 1 && c <= kMaxCols; }
+bool rows_ok(int r) { return r >= 0 && r <= kMaxRows; }
 
 size_t scales_bytes(int rows, int cols, bool nv) {
     return (size_t)((rows + 127) / 128) * mx4_stages(cols) * (nv ? 4 : 2) * kMx4TileBytes;
@@ -58,7 +59,7 @@ cudaError_t device_info(int &sms, int *&status) {
 // Checks shared by the entries that write a 4-bit tensor from rows of x.
 int check_rows(const void *x, int x_type, long long ld, int rows, int cols, int fmt, float ts, const void *codes,
                const void *scales) {
-    if (rows < 0 || !cols_ok(cols) || ld < cols) return ALBERT_ERR_SHAPE;
+    if (!rows_ok(rows) || !cols_ok(cols) || ld < cols) return ALBERT_ERR_SHAPE;
     if (!is_format(fmt) || !is_type(x_type) || !scale_ok(fmt, ts)) return ALBERT_ERR_CONFIG;
     if (!aligned(x, elem_size(x_type)) || !aligned(codes, 16) || !aligned(scales, 16)) return ALBERT_ERR_CONFIG;
     return ALBERT_OK;
@@ -68,10 +69,10 @@ int check_rows(const void *x, int x_type, long long ld, int rows, int cols, int 
 
 extern "C" {
 
-size_t albert_mx4_codes_bytes(int rows, int cols) { return rows < 1 || !cols_ok(cols) ? 0 : codes_bytes(rows, cols); }
+size_t albert_mx4_codes_bytes(int rows, int cols) { return rows < 1 || !rows_ok(rows) || !cols_ok(cols) ? 0 : codes_bytes(rows, cols); }
 
 size_t albert_mx4_scales_bytes(int rows, int cols, int fmt) {
-    return rows < 1 || !cols_ok(cols) || !is_format(fmt) ? 0 : scales_bytes(rows, cols, fmt == ALBERT_NVFP4);
+    return rows < 1 || !rows_ok(rows) || !cols_ok(cols) || !is_format(fmt) ? 0 : scales_bytes(rows, cols, fmt == ALBERT_NVFP4);
 }
 
 int albert_mx4_quantize(const void *x, int x_type, long long ld_x, int rows, int cols, int fmt, float tensor_scale,
@@ -120,13 +121,13 @@ int albert_mx4_layer_norm(const void *x, int x_type, long long ld_x, const float
 }
 
 size_t albert_mx4_linear_workspace_bytes(int rows, int k, int fmt) {
-    if (rows < 1 || !cols_ok(k) || !is_format(fmt) || rows <= kMx4MaxTokens) return 0;
+    if (rows < 1 || !rows_ok(rows) || !cols_ok(k) || !is_format(fmt) || rows <= kMx4MaxTokens) return 0;
     return up16(codes_bytes(rows, k)) + scales_bytes(rows, k, fmt == ALBERT_NVFP4);
 }
 
 int albert_mx4_linear(const albert_mx4_linear_args *p, void *stream) {
     if (!p) return ALBERT_ERR_NULL;
-    if (p->rows < 0 || !cols_ok(p->n) || !cols_ok(p->k)) return ALBERT_ERR_SHAPE;
+    if (!rows_ok(p->rows) || !cols_ok(p->n) || !cols_ok(p->k)) return ALBERT_ERR_SHAPE;
     if (p->rows == 0) return ALBERT_OK;
     if (!p->w_codes || !p->w_scales) return ALBERT_ERR_NULL;
     if (!p->x && (!p->a_codes || !p->a_scales)) return ALBERT_ERR_NULL;
@@ -146,6 +147,9 @@ int albert_mx4_linear(const albert_mx4_linear_args *p, void *stream) {
         (p->out ? !aligned(p->out, elem_size(p->out_type)) : !aligned(p->q_codes, 16) || !aligned(p->q_scales, 16)))
         return ALBERT_ERR_CONFIG;
     if (p->gelu != 0 && p->gelu != 1) return ALBERT_ERR_CONFIG;
+    // the product of the tensor scales multiplies the fp32 sum: far from fp32's limits
+    if (p->fmt == ALBERT_NVFP4 && !(p->x_scale * p->w_scale >= kMinScale && p->x_scale * p->w_scale <= kMaxScale))
+        return ALBERT_ERR_CONFIG;
 
     const bool nv = p->fmt == ALBERT_NVFP4;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
