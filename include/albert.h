@@ -356,8 +356,8 @@ size_t albert_length_regulate_scratch_bytes(int n_tok);
  * the current device, which must be the one the buffers are on.  Row strides
  * (ld*) are in elements and at least the row length; rows of x, y, residual and
  * out may have any alignment of their element type.  rows == 0 does nothing.
- * A first call on a device loads the kernels; make one before capturing into a
- * graph.  Scale bytes that a caller writes itself have a zero sign bit.
+ * They may be captured into graphs.  Scale bytes that a caller writes itself have
+ * a zero sign bit.
  * Host errors: ALBERT_ERR_NULL; ALBERT_ERR_SHAPE (rows outside [0, 2^30], a width
  * outside [1, 2^24], an ld below the row length); ALBERT_ERR_CONFIG (unknown format
  * or type, a tensor scale out of range, unaligned codes or scales). */
