@@ -458,3 +458,24 @@ def test_wrappers_refuse_mismatched_tensors():
         tea.mx4_quantize(x, "nvfp4", 0.0)
     with torch.no_grad():
         tea.mx4_linear(x.clone().requires_grad_(), w)
+
+
+def test_block_scales_of_many_magnitudes_and_tensor_scales():
+    """nvfp4: amax / (6 ts) correctly rounded before E4M3, over random magnitudes, E4M3's
+    midpoints (and their fp32 neighbours) times 6 ts, and tensor scales of any mantissa."""
+    rng = np.random.default_rng(77)
+    g = mq.e4m3_grid()
+    mids = ((g[:-1] + g[1:]) / 2).astype(np.float32)
+    for ts in (1.0, 0.0093, 7e-5, 0.33333334, 1.9999999, 2.0 ** -90, 3e20):
+        with np.errstate(over="ignore"):
+            near = (mids * (np.float32(6) * np.float32(ts))).astype(np.float32)
+        a = np.concatenate([near, np.nextafter(near, np.float32(0)), np.nextafter(near, np.float32(np.inf)),
+                            (np.exp(rng.uniform(-12, 8, 4000)) * 6 * ts).astype(np.float32)])
+        a = a[np.isfinite(a)]
+        x = np.zeros((a.size, 16), np.float32)
+        x[:, 3] = a
+        q = tea.mx4_quantize(torch.tensor(x).cuda(), "nvfp4", ts)
+        codes, byte = _stored(q)
+        want_c, want_b = mq.quantize(x, "nvfp4", ts)
+        np.testing.assert_array_equal(byte, want_b)
+        np.testing.assert_array_equal(codes, want_c)

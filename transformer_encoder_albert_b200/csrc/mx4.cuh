@@ -7,7 +7,7 @@
 // for bit:
 //   mxfp4: byte = max(biased exponent of amax - 2, 0); q = E2M1(x * 2^(127 - byte)),
 //          the power of two exact, so the only rounding is E2M1's;
-//   nvfp4: byte = E4M3(fl(amax / six_ts)), d = fl(E4M3 value * ts), q = E2M1(fl(x * fl(1 / d))).
+//   nvfp4: byte = E4M3(fl(amax / fl(6 ts))), d = fl(E4M3 value * ts), q = E2M1(fl(x * fl(1 / d))).
 #pragma once
 #include <cstdint>
 #include <cuda_bf16.h>
@@ -81,8 +81,25 @@ struct Mx4Scale {
     float mul;
     bool zero;  // codes are 0 whatever the values
 };
+// fl(a / b) for a >= 0 from y = fl(1 / b): Markstein's correction (IBM J. Res. Dev. 34,
+// 1990) twice -- the first makes the quotient faithful, the second correctly rounded,
+// each remainder being exact in an fma.  Quotients from 1024 on all saturate; those
+// below fp32's normals all round to an E4M3 zero.
+__device__ __forceinline__ float mx4_quotient(float a, float b, float y) {
+    const float q0 = a * y;
+    const float q1 = fmaf(fmaf(-q0, b, a), y, q0);
+    const float q2 = fmaf(fmaf(-q1, b, a), y, q1);
+    return q0 < 1024.0f ? q2 : 1024.0f;
+}
+
+// The constants of a tensor scale that a block needs.
+struct Mx4Ts {
+    float ts, six, inv_six;
+};
+__device__ __forceinline__ Mx4Ts mx4_ts(float ts) { return Mx4Ts{ts, 6.0f * ts, __frcp_rn(6.0f * ts)}; }
+
 template <bool NV>
-__device__ __forceinline__ Mx4Scale mx4_block_scale(uint32_t amax_bits, float ts, float six_ts) {
+__device__ __forceinline__ Mx4Scale mx4_block_scale(uint32_t amax_bits, const Mx4Ts &ts) {
     Mx4Scale s;
     const bool bad = amax_bits >= 0x7f800000u;
     if constexpr (!NV) {
@@ -91,12 +108,12 @@ __device__ __forceinline__ Mx4Scale mx4_block_scale(uint32_t amax_bits, float ts
         s.mul = __uint_as_float((254u - (bad ? 127u : s.byte)) << 23);
         s.zero = bad;
     } else {
-        const float t = __fdiv_rn(__uint_as_float(bad ? 0u : amax_bits), six_ts);
+        const float t = mx4_quotient(__uint_as_float(bad ? 0u : amax_bits), ts.six, ts.inv_six);
         uint16_t c;
         asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(0.0f), "f"(t));
         s.byte = bad ? 0x7fu : (uint32_t)(c & 0xffu);
         s.zero = bad || s.byte == 0u;
-        const float d = __fmul_rn(e4m3_value(s.byte), ts);
+        const float d = __fmul_rn(e4m3_value(s.byte), ts.ts);
         s.mul = __frcp_rn(s.zero ? 1.0f : d);  // = fl(1 / d); zero: the codes are dropped anyway
     }
     return s;
@@ -251,11 +268,10 @@ __device__ __forceinline__ uint32_t amax_f32_bits(uint32_t m) {
 // values, fp32 bits) by shuffles.  Returns the lane's codes; `word` becomes the four
 // scale bytes of the lane's tile (every lane of the tile holds it).
 template <bool NV>
-__device__ __forceinline__ uint32_t mx4_warp_quant(const float (&v)[8], uint32_t m, float ts, float six_ts, int lane,
-                                                   uint32_t &word) {
+__device__ __forceinline__ uint32_t mx4_warp_quant(const float (&v)[8], uint32_t m, const Mx4Ts &ts, int lane, uint32_t &word) {
     m = umax(m, __shfl_xor_sync(0xffffffffu, m, 1));
     if constexpr (!NV) m = umax(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    const Mx4Scale s = mx4_block_scale<NV>(m, ts, six_ts);
+    const Mx4Scale s = mx4_block_scale<NV>(m, ts);
     const uint64_t mul2 = f2_make(s.mul, s.mul);
     float y[8];
 #pragma unroll

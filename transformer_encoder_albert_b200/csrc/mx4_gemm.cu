@@ -386,6 +386,7 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             const int col = w.n * TN + chunk_of(tt, i) * 32 + lane;
             return (p.bias && col < p.N) ? __ldg(p.bias + col) : 0.f;
         };
+        const Mx4Ts q_ts = mx4_ts(p.q_ts);
         float bnext = 0.f;
         TileWalk w(slot, nslots, n_sub), wn = w;  // this tile, the next
         if (w.u < units) {
@@ -455,7 +456,7 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 #pragma unroll
                         for (int j = 1; j + 1 < kB; j += 2) mx = fmax3_abs_nan(mx, v[b * kB + j], v[b * kB + j + 1]);
                         mx = fmax3_abs_nan(mx, v[b * kB + kB - 1], 0.f);
-                        const Mx4Scale s = mx4_block_scale<NV>(abs_bits(mx), p.q_ts, 6.0f * p.q_ts);
+                        const Mx4Scale s = mx4_block_scale<NV>(abs_bits(mx), q_ts);
                         const uint64_t mul2 = f2_make(s.mul, s.mul);
                         bytes |= s.byte << (8 * b);
 #pragma unroll

@@ -93,11 +93,12 @@ __device__ __forceinline__ Raw16<T> load_raw16(const T *p, int n, int vec) {
 
 template <typename T, bool NV>
 __global__ void __launch_bounds__(32 * kQWarps)
-mx4_quant_kernel(const T *__restrict__ x, long long ld, int rows, int cols, const int *n_rows, float ts, float six_ts,
+mx4_quant_kernel(const T *__restrict__ x, long long ld, int rows, int cols, const int *n_rows, float ts,
                  uint8_t *__restrict__ codes, uint8_t *__restrict__ scales, int vec, long long pairs, const int *status,
                  int trigger) {
     if (trigger) griddep_launch_dependents();
     griddep_wait();
+    const Mx4Ts tsc = mx4_ts(ts);
     if (status && *reinterpret_cast<const volatile int *>(status) != 0) return;
     const int lane = threadIdx.x & 31, sub = lane & 15, lower = lane >> 4;  // lower: the row 32 below
     int nr = n_rows ? *reinterpret_cast<const volatile int *>(n_rows) : rows;
@@ -121,7 +122,7 @@ mx4_quant_kernel(const T *__restrict__ x, long long ld, int rows, int cols, cons
             m = umax(m2 & 0xffffu, m2 >> 16);
         }
         if constexpr (!NV) m = umax(m, __shfl_xor_sync(0xffffffffu, m, 1));  // a block is two lanes
-        const Mx4Scale s = mx4_block_scale<NV>(amax_f32_bits<T>(m), ts, six_ts);
+        const Mx4Scale s = mx4_block_scale<NV>(amax_f32_bits<T>(m), tsc);
         const uint64_t mul2 = f2_make(s.mul, s.mul);
         uint32_t q[2];
 #pragma unroll
@@ -235,10 +236,11 @@ template <typename T, bool NV, int NCH>
 __global__ void __launch_bounds__(32 * kQWarps)
 mx4_norm_warp_kernel(const T *__restrict__ x, long long ld, const float *__restrict__ gamma,
                      const float *__restrict__ beta, float eps, int rows, int cols, const int *n_rows, float ts,
-                     float six_ts, T *__restrict__ y, long long ld_y, uint8_t *__restrict__ codes,
+                     T *__restrict__ y, long long ld_y, uint8_t *__restrict__ codes,
                      uint8_t *__restrict__ scales, int vec, int vec_y, int vec_g, const int *status, int trigger) {
     if (trigger) griddep_launch_dependents();
     griddep_wait();
+    const Mx4Ts tsc = mx4_ts(ts);
     if (status && *reinterpret_cast<const volatile int *>(status) != 0) return;
     int nr = n_rows ? *reinterpret_cast<const volatile int *>(n_rows) : rows;
     nr = nr < rows ? nr : rows;
@@ -324,7 +326,7 @@ mx4_norm_warp_kernel(const T *__restrict__ x, long long ld, const float *__restr
             m = fmax3_abs_nan(m, u[5], fmax3_abs_nan(u[6], u[7], 0.f));
             if (y) store8<T>(y + (size_t)row * ld_y + col, WHOLE ? 8 : n, WHOLE || vec_y != 0, u);
             uint32_t word;
-            const uint32_t q = mx4_warp_quant<NV>(u, abs_bits(m), ts, six_ts, lane, word);
+            const uint32_t q = mx4_warp_quant<NV>(u, abs_bits(m), tsc, lane, word);
             if (WHOLE || col / 2 < pitch) *reinterpret_cast<uint32_t *>(codes + (size_t)row * pitch + col / 2) = q;
             constexpr int kTileLanes = Mx4<NV>::kTileCols / 8;
             if (lane % kTileLanes == 0)
@@ -358,11 +360,12 @@ template <typename T, bool NV, int HELD>
 __global__ void __launch_bounds__(32 * kQWarps)
 mx4_norm_cta_kernel(const T *__restrict__ x, long long ld, const float *__restrict__ gamma,
                     const float *__restrict__ beta, float eps, int rows, int cols, const int *n_rows, float ts,
-                    float six_ts, T *__restrict__ y, long long ld_y, uint8_t *__restrict__ codes,
+                    T *__restrict__ y, long long ld_y, uint8_t *__restrict__ codes,
                     uint8_t *__restrict__ scales, int vec, int vec_y, int vec_g, const int *status, int trigger) {
     __shared__ float red[2][kQWarps];  // one per sum: a row's second barrier separates its first from the next row's
     if (trigger) griddep_launch_dependents();
     griddep_wait();
+    const Mx4Ts tsc = mx4_ts(ts);
     if (status && *reinterpret_cast<const volatile int *>(status) != 0) return;
     int nr = n_rows ? *reinterpret_cast<const volatile int *>(n_rows) : rows;
     nr = nr < rows ? nr : rows;
@@ -420,7 +423,7 @@ mx4_norm_cta_kernel(const T *__restrict__ x, long long ld, const float *__restri
             }
             if (y) store8<T>(y + (size_t)row * ld_y + col, n, vec_y != 0, v);
             uint32_t word;
-            const uint32_t q = mx4_warp_quant<NV>(v, m, ts, six_ts, lane, word);
+            const uint32_t q = mx4_warp_quant<NV>(v, m, tsc, lane, word);
             if (col / 2 < pitch) *reinterpret_cast<uint32_t *>(codes + (size_t)row * pitch + col / 2) = q;
             constexpr int kTileLanes = Mx4<NV>::kTileCols / 8;
             if (lane % kTileLanes == 0)
@@ -475,13 +478,12 @@ cudaError_t quant_typed(const Mx4QuantArgs &a, cudaStream_t s, bool pdl) {
     cudaError_t e = resident_grid(mx4_quant_kernel<T, NV>, cached, (items + kQWarps - 1) / kQWarps, blocks);
     if (e != cudaSuccess) return e;
     const int vec = vec_width(a.x, a.ld, sizeof(T));
-    const float six = 6.0f * a.tensor_scale;
     if (pdl)
         return launch_pdl(mx4_quant_kernel<T, NV>, dim3(blocks), dim3(32 * kQWarps), 0, s, static_cast<const T *>(a.x),
-                          a.ld, a.rows, a.cols, a.n_rows, a.tensor_scale, six, a.codes, a.scales, vec, pairs, a.status,
+                          a.ld, a.rows, a.cols, a.n_rows, a.tensor_scale, a.codes, a.scales, vec, pairs, a.status,
                           a.trigger);
     mx4_quant_kernel<T, NV><<<blocks, 32 * kQWarps, 0, s>>>(static_cast<const T *>(a.x), a.ld, a.rows, a.cols, a.n_rows,
-                                                            a.tensor_scale, six, a.codes, a.scales, vec, pairs, a.status,
+                                                            a.tensor_scale, a.codes, a.scales, vec, pairs, a.status,
                                                             a.trigger);
     return cudaGetLastError();
 }
@@ -507,13 +509,12 @@ cudaError_t norm_launch(K kernel, std::atomic<int> (&cached)[64], int rows_per_c
     if (e != cudaSuccess) return e;
     const int vec = aligned16(a.q.x, a.q.ld, sizeof(T)), vec_y = aligned16(a.y, a.ld_y, sizeof(T));
     const int vec_g = std::min(vec_width(a.gamma, 8, 4), vec_width(a.beta, 8, 4));
-    const float six = 6.0f * a.q.tensor_scale;
     if (pdl)
         return launch_pdl(kernel, dim3(blocks), dim3(32 * kQWarps), 0, s, static_cast<const T *>(a.q.x), a.q.ld, a.gamma,
-                          a.beta, a.eps, a.q.rows, a.q.cols, a.q.n_rows, a.q.tensor_scale, six, static_cast<T *>(a.y),
+                          a.beta, a.eps, a.q.rows, a.q.cols, a.q.n_rows, a.q.tensor_scale, static_cast<T *>(a.y),
                           a.ld_y, a.q.codes, a.q.scales, vec, vec_y, vec_g, a.q.status, a.q.trigger);
     kernel<<<blocks, 32 * kQWarps, 0, s>>>(static_cast<const T *>(a.q.x), a.q.ld, a.gamma, a.beta, a.eps, a.q.rows,
-                                           a.q.cols, a.q.n_rows, a.q.tensor_scale, six, static_cast<T *>(a.y), a.ld_y,
+                                           a.q.cols, a.q.n_rows, a.q.tensor_scale, static_cast<T *>(a.y), a.ld_y,
                                            a.q.codes, a.q.scales, vec, vec_y, vec_g, a.q.status, a.q.trigger);
     return cudaGetLastError();
 }

@@ -80,12 +80,13 @@ struct TokenRows {
     template <bool NV>
     __device__ __forceinline__ void quantize(const Mx4TokArgs &p, int r0, uint32_t codes, uint32_t scales, int lane) const {
         const int sub = lane & 15;
+        const Mx4Ts ts = mx4_ts(p.x_ts);
 #pragma unroll
         for (int i = 0; i < PAIRS; ++i) {
             const int row = r0 + 2 * i + (lane >> 4);
             uint32_t m = umax(raw8_amax<T>(a[i]), raw8_amax<T>(b[i]));
             if constexpr (!NV) m = umax(m, __shfl_xor_sync(0xffffffffu, m, 1));
-            const Mx4Scale s = mx4_block_scale<NV>(amax_f32_bits<T>(m), p.x_ts, 6.0f * p.x_ts);
+            const Mx4Scale s = mx4_block_scale<NV>(amax_f32_bits<T>(m), ts);
             float v[8], u[8];
             raw8_values<T>(a[i], v);
             raw8_values<T>(b[i], u);
@@ -323,6 +324,7 @@ mx4_tokens_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
         const int wk = warp - 2, f = (wk & 3) * 32 + lane, feat = tile * 128 + f;
         const float bias = p.bias && feat < p.N ? __ldg(p.bias + feat) : 0.f;
         const uint32_t own = smem_u32(sum);
+        const Mx4Ts q_ts = mx4_ts(p.q_ts);
         // this CTA's tokens: rank, rank + nclu, ..., the two groups of four warps alternating
         for (int t = (int)rank + (wk >> 2) * nclu; t < p.M; t += 2 * nclu) {
             float acc = 0.f;
@@ -353,7 +355,7 @@ mx4_tokens_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
                 uint32_t m = abs_bits(v);
 #pragma unroll
                 for (int o = 1; o < Mx4<NV>::kBlock; o <<= 1) m = umax(m, __shfl_xor_sync(0xffffffffu, m, o));
-                const Mx4Scale s = mx4_block_scale<NV>(m, p.q_ts, 6.0f * p.q_ts);
+                const Mx4Scale s = mx4_block_scale<NV>(m, q_ts);
                 float y[8];
                 y[0] = __fmul_rn(v, s.mul);
 #pragma unroll
