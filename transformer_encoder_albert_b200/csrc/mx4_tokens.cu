@@ -8,11 +8,11 @@
 // SMs without work, and adds the partial sums over distributed shared memory in rank
 // order (no atomics, the same bits every time, no workspace).
 //   warp 0      : TMA ring of weight stages (all in flight before any product);
-//   warp 10     : copies a stage's scales to tensor memory.  A ring stage has scale
+//   warp 14     : copies a stage's scales to tensor memory.  A ring stage has scale
 //                 columns of its own there, so the stage's barrier guards them too;
 //   warp 1      : products;
-//   warps 2..9  : quantize (or copy) the tokens into a stage's second operand (warp 2 + i
-//                 stage i of the ring), then the epilogue.
+//   warps 2..13 : quantize (or copy) the tokens into a stage's second operand, then the
+//                 epilogue.
 // Rows of the token operand past the last token are never written: they only reach
 // result columns that nobody reads.
 #include <type_traits>
@@ -24,7 +24,7 @@
 namespace albert {
 namespace {
 
-constexpr int kWorkers = 8;
+constexpr int kWorkers = 12;  // two per stage of a full ring (one left 16 tokens at 2.5 TB/s of weights)
 constexpr int kTokThreads = 32 * (3 + kWorkers);
 constexpr int kWBytes = 128 * 128;   // codes of a weight stage
 constexpr int kMaxRing = 6;            // at most kWorkers
@@ -325,8 +325,8 @@ mx4_tokens_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
         const float bias = p.bias && feat < p.N ? __ldg(p.bias + feat) : 0.f;
         const uint32_t own = smem_u32(sum);
         const Mx4Ts q_ts = mx4_ts(p.q_ts);
-        // this CTA's tokens: rank, rank + nclu, ..., the two groups of four warps alternating
-        for (int t = (int)rank + (wk >> 2) * nclu; t < p.M; t += 2 * nclu) {
+        // this CTA's tokens: rank, rank + nclu, ..., the groups of four warps in turn
+        for (int t = (int)rank + (wk >> 2) * nclu; t < p.M; t += kWorkers / 4 * nclu) {
             float acc = 0.f;
             if (nclu == 1) {
                 acc = sum[t * 128 + f];
