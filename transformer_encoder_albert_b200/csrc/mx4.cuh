@@ -240,6 +240,12 @@ __device__ __forceinline__ uint64_t gelu_f2(uint64_t x) {
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 __device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
 
+__device__ __forceinline__ uint32_t umax_x2(uint32_t a, uint32_t b) {  // two 16-bit maxima
+    uint32_t r;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
 // The largest magnitude of eight values, as bits that order like it (16-bit types:
 // their own bits, two at a time), and those bits as fp32 bits.
 template <typename T>
@@ -252,7 +258,7 @@ __device__ __forceinline__ uint32_t raw8_amax(const Raw8<T> &r) {
     } else {
         uint32_t m = r.w[0] & 0x7fff7fffu;
 #pragma unroll
-        for (int i = 1; i < 4; ++i) m = __vmaxu2(m, r.w[i] & 0x7fff7fffu);
+        for (int i = 1; i < 4; ++i) m = umax_x2(m, r.w[i] & 0x7fff7fffu);
         return umax(m & 0xffffu, m >> 16);
     }
 }

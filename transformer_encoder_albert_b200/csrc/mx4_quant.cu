@@ -31,14 +31,14 @@ __device__ __forceinline__ size_t scale_word_offset(int row, int tile, int row_t
 // 64 (g / 32 % 2) + g % 32 and the row 32 below.
 struct Walk {
     int chunk, chunks, dc;
-    long long pair, dp;
-    __device__ Walk(int chunks_, long long first, long long stride) : chunks(chunks_) {
+    int pair, dp;  // (rows <= 2^30: pairs, and a step past them, fit)
+    __device__ __forceinline__ Walk(int chunks_, int first, int stride) : chunks(chunks_) {
         pair = first / chunks_;
-        chunk = (int)(first - pair * chunks_);
+        chunk = first - pair * chunks_;
         dp = stride / chunks_;
-        dc = (int)(stride - dp * chunks_);
+        dc = stride - dp * chunks_;
     }
-    __device__ void next() {
+    __device__ __forceinline__ void next() {
         chunk += dc;
         pair += dp;
         if (chunk >= chunks) {
@@ -46,7 +46,7 @@ struct Walk {
             ++pair;
         }
     }
-    __device__ int row0() const { return (int)(pair >> 6) * 128 + (int)((pair >> 5) & 1) * 64 + (int)(pair & 31); }
+    __device__ __forceinline__ int row0() const { return (pair >> 6) * 128 + ((pair >> 5) & 1) * 64 + (pair & 31); }
 };
 
 __device__ __forceinline__ void ld_global_v8(const void *p, uint32_t *w) {
@@ -94,7 +94,7 @@ __device__ __forceinline__ Raw16<T> load_raw16(const T *p, int n, int vec) {
 template <typename T, bool NV>
 __global__ void __launch_bounds__(32 * kQWarps)
 mx4_quant_kernel(const T *__restrict__ x, long long ld, int rows, int cols, const int *n_rows, float ts,
-                 uint8_t *__restrict__ codes, uint8_t *__restrict__ scales, int vec, long long pairs, const int *status,
+                 uint8_t *__restrict__ codes, uint8_t *__restrict__ scales, int vec, int pairs, const int *status,
                  int trigger) {
     if (trigger) griddep_launch_dependents();
     griddep_wait();
@@ -105,7 +105,7 @@ mx4_quant_kernel(const T *__restrict__ x, long long ld, int rows, int cols, cons
     nr = nr < rows ? nr : rows;
     const int chunks = mx4_stages(cols), pitch = mx4_code_pitch(cols);
     const int row_tiles = chunks * Mx4<NV>::kStageTiles;
-    Walk w(chunks, (long long)blockIdx.x * kQWarps + (threadIdx.x >> 5), (long long)gridDim.x * kQWarps);
+    Walk w(chunks, blockIdx.x * kQWarps + (threadIdx.x >> 5), gridDim.x * kQWarps);
     auto load = [&]() {
         const int row = w.row0() + 32 * lower, col = w.chunk * kMx4StageCols + sub * 16;
         return load_raw16<T>(x + (size_t)row * ld + col, w.pair < pairs && row < nr ? cols - col : 0, vec);
@@ -118,7 +118,7 @@ mx4_quant_kernel(const T *__restrict__ x, long long ld, int rows, int cols, cons
         } else {
             uint32_t m2 = r.h[0].w[0] & 0x7fff7fffu;
 #pragma unroll
-            for (int i = 1; i < 8; ++i) m2 = __vmaxu2(m2, r.h[i >> 2].w[i & 3] & 0x7fff7fffu);
+            for (int i = 1; i < 8; ++i) m2 = umax_x2(m2, r.h[i >> 2].w[i & 3] & 0x7fff7fffu);
             m = umax(m2 & 0xffffu, m2 >> 16);
         }
         if constexpr (!NV) m = umax(m, __shfl_xor_sync(0xffffffffu, m, 1));  // a block is two lanes
@@ -167,11 +167,11 @@ mx4_quant_kernel(const T *__restrict__ x, long long ld, int rows, int cols, cons
 template <typename T, bool NV>
 __global__ void __launch_bounds__(32 * kQWarps)
 mx4_dequant_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales, int rows, int cols, float ts,
-                   T *__restrict__ out, long long ld, int vec, long long pairs) {
+                   T *__restrict__ out, long long ld, int vec, int pairs) {
     const int lane = threadIdx.x & 31, sub = lane & 15, lower = lane >> 4;
     const int chunks = mx4_stages(cols), pitch = mx4_code_pitch(cols);
     const int row_tiles = chunks * Mx4<NV>::kStageTiles;
-    Walk w(chunks, (long long)blockIdx.x * kQWarps + (threadIdx.x >> 5), (long long)gridDim.x * kQWarps);
+    Walk w(chunks, blockIdx.x * kQWarps + (threadIdx.x >> 5), gridDim.x * kQWarps);
     auto load = [&](uint2 &q, uint32_t &sb) {
         const int row = w.row0() + 32 * lower, col = w.chunk * kMx4StageCols + sub * 16, blk = col / Mx4<NV>::kBlock;
         q = make_uint2(0, 0);
@@ -472,7 +472,8 @@ inline int vec_width(const void *p, long long ld, int elem) {
 template <typename T, bool NV>
 cudaError_t quant_typed(const Mx4QuantArgs &a, cudaStream_t s, bool pdl) {
     // (all row pairs of the last tile, whose scale bytes are written whole)
-    const long long pairs = (long long)((a.rows + 127) / 128) * 64, items = pairs * mx4_stages(a.cols);
+    const int pairs = (a.rows + 127) / 128 * 64;
+    const long long items = (long long)pairs * mx4_stages(a.cols);
     static std::atomic<int> cached[64];
     int blocks = 0;
     cudaError_t e = resident_grid(mx4_quant_kernel<T, NV>, cached, (items + kQWarps - 1) / kQWarps, blocks);
@@ -491,7 +492,8 @@ cudaError_t quant_typed(const Mx4QuantArgs &a, cudaStream_t s, bool pdl) {
 template <typename T, bool NV>
 cudaError_t dequant_typed(const uint8_t *codes, const uint8_t *scales, int rows, int cols, float ts, void *out,
                           long long ld, cudaStream_t s) {
-    const long long pairs = (long long)((rows + 127) / 128) * 64, items = pairs * mx4_stages(cols);
+    const int pairs = (rows + 127) / 128 * 64;
+    const long long items = (long long)pairs * mx4_stages(cols);
     static std::atomic<int> cached[64];
     int blocks = 0;
     cudaError_t e = resident_grid(mx4_dequant_kernel<T, NV>, cached, (items + kQWarps - 1) / kQWarps, blocks);
