@@ -71,7 +71,7 @@ def test_storage_sizes_agree(lib, fmt, rows, cols):
     assert lib.albert_mx4_codes_bytes(rows, cols) == p.size
     assert lib.albert_mx4_scales_bytes(rows, cols, tea.MX4_FORMATS[fmt]) == t.size
     ws = lib.albert_mx4_linear_workspace_bytes(rows, cols, tea.MX4_FORMATS[fmt])
-    assert ws == 0 or ws >= p.size + t.size
+    assert (ws == 0) == (rows <= tea._MX4_MAX_TOKENS) and (ws == 0 or ws >= p.size + t.size)
 
 
 def test_storage_sizes_of_invalid_shapes_are_zero(lib):

@@ -468,15 +468,19 @@ def length_regulate(logits, feats, cu_seqlens, speed: float = 1.0, max_frames: i
 
 MX4_FORMATS = {"mxfp4": ALBERT_MXFP4, "nvfp4": ALBERT_NVFP4}
 _MX4_TILES = {"mxfp4": 2, "nvfp4": 4}  # scale tiles per 256 columns
+_MX4_MAX_TOKENS = 32                   # up to so many rows albert_mx4_linear needs no workspace
 _mx4_types: dict = {}
-_torch = None  # set with the first tensor (the module itself imports without torch)
+# set with the first tensor (the module itself imports without torch)
+_torch = _empty = _u8 = _device_now = _raw_stream = None
 
 
 def _mx4_torch():
-    global _torch
+    global _torch, _empty, _u8, _device_now, _raw_stream
     if _torch is None:
         import torch
         _torch = torch
+        _empty, _u8 = torch.empty_strided, torch.uint8  # (0.8 us less per tensor than torch.empty)
+        _device_now, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
         _mx4_types.update({torch.bfloat16: ALBERT_BF16, torch.float32: ALBERT_FP32, torch.float16: ALBERT_FP16})
     return _torch
 
@@ -551,11 +555,12 @@ def _mx4_scale(fmt: str, tensor_scale) -> float:
 
 def mx4_empty(rows: int, cols: int, fmt: str = "mxfp4", tensor_scale: float = 1.0, device="cuda") -> Mx4Tensor:
     """A 4-bit matrix with uninitialised contents (codes and scales in one allocation)."""
-    torch = _torch or _mx4_torch()
+    if _torch is None:
+        _mx4_torch()
     c, s = mx4_shapes(rows, cols, fmt)
     t = Mx4Tensor.__new__(Mx4Tensor)
     off = (c[0] * c[1] + 127) // 128 * 128
-    t._buf = b = torch.empty(off + s[0] * s[1] * s[2], dtype=torch.uint8, device=device)
+    t._buf = b = _empty((off + s[0] * s[1] * 512,), (1,), dtype=_u8, device=device)
     t._codes = t._scales = None
     t._dev = b.get_device()
     t._cptr = b.data_ptr()
@@ -613,7 +618,7 @@ def _mx4_away(dev: int, stream) -> bool:
     """Whether a call must first switch to another device or stream."""
     if dev < 0:
         raise ValueError("4-bit matrices must be on a CUDA device")
-    return stream is not None or _torch._C._cuda_getDevice() != dev
+    return stream is not None or _device_now() != dev
 
 
 def _mx4_on(dev: int, stream):
@@ -623,10 +628,6 @@ def _mx4_on(dev: int, stream):
     if stream.device.index != dev:
         raise ValueError(f"stream of {stream.device} for tensors on cuda:{dev}")
     return torch.cuda.stream(stream)
-
-
-def _mx4_stream(dev: int) -> int:
-    return _torch._C._cuda_getCurrentRawStream(dev)
 
 
 def mx4_quantize(x, fmt: str = "mxfp4", tensor_scale: float = 1.0, out: Mx4Tensor | None = None, stream=None) -> Mx4Tensor:
@@ -643,8 +644,8 @@ def mx4_quantize(x, fmt: str = "mxfp4", tensor_scale: float = 1.0, out: Mx4Tenso
         raise ValueError(f"out must be a {fmt} matrix of shape {(rows, cols)} on {x.device}")
     else:
         out.tensor_scale = _mx4_scale(fmt, tensor_scale)
-    rc = lib().albert_mx4_quantize(x.data_ptr(), typ, ld, rows, cols, MX4_FORMATS[fmt], out.tensor_scale, out._cptr,
-                                   out._sptr, _mx4_stream(dev))
+    rc = (_lib or lib()).albert_mx4_quantize(x.data_ptr(), typ, ld, rows, cols, MX4_FORMATS[fmt], out.tensor_scale, out._cptr,
+                                   out._sptr, _raw_stream(dev))
     if rc:
         raise AlbertError(rc, "albert_mx4_quantize")
     return out
@@ -659,14 +660,14 @@ def mx4_dequantize(t: Mx4Tensor, dtype=None, out=None, stream=None):
             return mx4_dequantize(t, dtype, out)
     rows, cols = t.rows, t.cols
     if out is None:
-        out = torch.empty((rows, cols), dtype=torch.bfloat16 if dtype is None else dtype, device=t.device)
+        out = _empty((rows, cols), (cols, 1), dtype=torch.bfloat16 if dtype is None else dtype, device=t.device)
         ld = cols
     else:
         if dtype is not None and out.dtype != dtype:
             raise ValueError(f"out is {out.dtype}, dtype is {dtype}")
         ld = _mx4_rows(out, "out", dev, (rows, cols))[2]
-    rc = lib().albert_mx4_dequantize(t._cptr, t._sptr, rows, cols, MX4_FORMATS[t.fmt], t.tensor_scale, out.data_ptr(),
-                                     _mx4_type(out.dtype, "out"), ld, _mx4_stream(dev))
+    rc = (_lib or lib()).albert_mx4_dequantize(t._cptr, t._sptr, rows, cols, MX4_FORMATS[t.fmt], t.tensor_scale, out.data_ptr(),
+                                     _mx4_type(out.dtype, "out"), ld, _raw_stream(dev))
     if rc:
         raise AlbertError(rc, "albert_mx4_dequantize")
     return out
@@ -676,43 +677,39 @@ def mx4_layer_norm(x, gamma, beta, eps: float = 1e-12, fmt: str = "mxfp4", tenso
                    return_rows: bool = True, stream=None):
     """LayerNorm over the rows of x: (y in x's dtype, or None if not return_rows;
     the 4-bit form of the fp32 result) in one pass (albert_mx4_layer_norm)."""
-    torch = _torch or _mx4_torch()
     rows, cols, ld, dev = _mx4_rows(x, "x")
     typ = _mx4_type(x.dtype, "x")
     if _mx4_away(dev, stream):
         with _mx4_on(dev, stream):
             return mx4_layer_norm(x, gamma, beta, eps, fmt, tensor_scale, return_rows)
     g, b = _mx4_vector(gamma, cols, "gamma", dev), _mx4_vector(beta, cols, "beta", dev)
-    y = torch.empty((rows, cols), dtype=x.dtype, device=x.device) if return_rows else None
+    y = _empty((rows, cols), (cols, 1), dtype=x.dtype, device=x.device) if return_rows else None
     q = mx4_empty(rows, cols, fmt, tensor_scale, x.device)
-    rc = lib().albert_mx4_layer_norm(x.data_ptr(), typ, ld, g, b, eps, rows, cols, MX4_FORMATS[fmt], q.tensor_scale,
-                                     None if y is None else y.data_ptr(), cols, q._cptr, q._sptr, _mx4_stream(dev))
+    rc = (_lib or lib()).albert_mx4_layer_norm(x.data_ptr(), typ, ld, g, b, eps, rows, cols, MX4_FORMATS[fmt], q.tensor_scale,
+                                     None if y is None else y.data_ptr(), cols, q._cptr, q._sptr, _raw_stream(dev))
     if rc:
         raise AlbertError(rc, "albert_mx4_layer_norm")
     return y, q
 
 
 def _mx4_linear(x, w: Mx4Tensor, bias, residual, gelu, x_scale, stream, out, dtype, q_scale):
-    torch = _torch or _mx4_torch()
-    packed = isinstance(x, Mx4Tensor)
-    if packed:
+    a = albert_mx4_linear_args()
+    if type(x) is Mx4Tensor:
         rows, k, dev = x.rows, x.cols, x._dev
         if x.fmt != w.fmt:
             raise ValueError(f"x is {x.fmt}, w is {w.fmt}")
+        a.a_codes, a.a_scales, a.x_scale = x._cptr, x._sptr, x.tensor_scale
     else:
         rows, k, ld, dev = _mx4_rows(x, "x")
+        a.x, a.ld_x, a.x_type, a.x_scale = x.data_ptr(), ld, _mx4_type(x.dtype, "x"), x_scale
     n = w.rows
     if w.cols != k or n < 1 or w._dev != dev:
         raise ValueError(f"x is [{rows}, {k}] on device {dev}, w is [{n}, {w.cols}] on device {w._dev}: "
                          f"w must be [n >= 1, {k}] on the same device")
-    if _mx4_away(dev, stream):
+    if stream is not None or dev < 0 or _device_now() != dev:
+        _mx4_away(dev, stream)
         with _mx4_on(dev, stream):
             return _mx4_linear(x, w, bias, residual, gelu, x_scale, None, out, dtype, q_scale)
-    a = albert_mx4_linear_args()
-    if packed:
-        a.a_codes, a.a_scales, a.x_scale = x._cptr, x._sptr, x.tensor_scale
-    else:
-        a.x, a.ld_x, a.x_type, a.x_scale = x.data_ptr(), ld, _mx4_type(x.dtype, "x"), x_scale
     a.w_codes, a.w_scales, a.w_scale = w._cptr, w._sptr, w.tensor_scale
     a.rows, a.n, a.k = rows, n, k
     a.fmt = fmt = MX4_FORMATS[w.fmt]
@@ -722,7 +719,7 @@ def _mx4_linear(x, w: Mx4Tensor, bias, residual, gelu, x_scale, stream, out, dty
         a.bias = _mx4_vector(bias, n, "bias", dev)
     if q_scale is None:
         if out is None:
-            out = torch.empty((rows, n), dtype=dtype, device=w.device)
+            out = _empty((rows, n), (n, 1), dtype=dtype, device=w.device)
             a.ld_out = n
         else:
             if dtype is not None and out.dtype != dtype:
@@ -737,13 +734,11 @@ def _mx4_linear(x, w: Mx4Tensor, bias, residual, gelu, x_scale, stream, out, dty
     else:
         out = mx4_empty(rows, n, w.fmt, q_scale, w.device)
         a.q_codes, a.q_scales, a.q_scale = out._cptr, out._sptr, out.tensor_scale
-    L = lib()
-    if not packed:
-        ws = L.albert_mx4_linear_workspace_bytes(rows, k, fmt)
-        if ws:
-            work = torch.empty(ws, dtype=torch.uint8, device=w.device)
-            a.workspace = work.data_ptr()
-    rc = L.albert_mx4_linear(C.byref(a), _mx4_stream(dev))
+    L = _lib or lib()
+    if rows > _MX4_MAX_TOKENS and a.x:
+        work = _empty((L.albert_mx4_linear_workspace_bytes(rows, k, fmt),), (1,), dtype=_u8, device=w.device)
+        a.workspace = work.data_ptr()
+    rc = L.albert_mx4_linear(C.byref(a), _raw_stream(dev))
     if rc:
         raise AlbertError(rc, "albert_mx4_linear")
     return out

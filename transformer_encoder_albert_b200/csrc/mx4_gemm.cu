@@ -493,7 +493,7 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                             if (lane < left) {
                                 const uint32_t *src = static_cast<const uint32_t *>(p.res) + (size_t)row0 * p.ld_res + col0 + lane;
 #pragma unroll 8
-                                for (int y = 0; y < rows; ++y) st_shared_u1(at + stg_off(y, q0), __ldg(src + (size_t)y * p.ld_res));
+                                for (int y = 0; y < rows; ++y) st_shared_u1(at + stg_off(y, q0), src[(size_t)y * p.ld_res]);
                             }
                             __syncwarp();
 #pragma unroll
@@ -534,7 +534,7 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                                     const uint32_t at = rtile + (lane & 7) * 2;
 #pragma unroll 8
                                     for (int y = 0; y < rows; ++y)
-                                        st_shared_u16(at + stg_off(y, lane >> 3), __ldg(src + (size_t)y * p.ld_res));
+                                        st_shared_u16(at + stg_off(y, lane >> 3), src[(size_t)y * p.ld_res]);
                                 }
                                 __syncwarp();
                             }

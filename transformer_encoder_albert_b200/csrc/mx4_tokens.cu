@@ -339,7 +339,7 @@ mx4_tokens_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
                 if (feat < p.N) {
                     const size_t ro = (size_t)t * p.ld_res + feat, oo = (size_t)t * p.ld_out + feat;
                     if (p.out_type == kElemF32) {
-                        if (p.res) v += __ldg(static_cast<const float *>(p.res) + ro);
+                        if (p.res) v += static_cast<const float *>(p.res)[ro];
                         static_cast<float *>(p.out)[oo] = v;
                     } else if (p.out_type == kElemF16) {
                         if (p.res) v += __half2float(static_cast<const __half *>(p.res)[ro]);
