@@ -479,3 +479,30 @@ def test_block_scales_of_many_magnitudes_and_tensor_scales():
         want_c, want_b = mq.quantize(x, "nvfp4", ts)
         np.testing.assert_array_equal(byte, want_b)
         np.testing.assert_array_equal(codes, want_c)
+
+
+def test_mixed_calls_on_several_streams_at_once():
+    """Products of every kind (few tokens with and without a cluster, single tiles, pairs, 4-bit
+    results) interleaved on four streams give the bits they give alone."""
+    g = torch.Generator(device="cuda").manual_seed(3)
+    calls = []
+    for fmt, rows, n, k in [("mxfp4", 1, 2304, 768), ("nvfp4", 12, 512, 2048), ("nvfp4", 30, 256, 256),
+                            ("mxfp4", 200, 768, 768), ("nvfp4", 3000, 1024, 512), ("mxfp4", 7, 8192, 1024)]:
+        x = torch.randn(rows, k, device="cuda", generator=g).to(torch.bfloat16)
+        w = tea.mx4_quantize(torch.randn(n, k, device="cuda", generator=g) * 0.05, fmt, 1e-4)
+        calls.append((x, w, TS[fmt]))
+
+    def run(c, s=None):
+        x, w, ts = c
+        return tea.mx4_linear(x, w, x_scale=ts, stream=s), tea.mx4_linear_quant(x, w, gelu=True, x_scale=ts, out_scale=ts,
+                                                                               stream=s)
+
+    alone = [run(c) for c in calls]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    for rep in range(6):
+        outs = [(i, run(calls[i], streams[(i + rep + j) % 4])) for j in range(4) for i in range(len(calls))]
+        torch.cuda.synchronize()
+        for i, (y, q) in outs:
+            assert torch.equal(y, alone[i][0]) and torch.equal(q.codes, alone[i][1].codes)
+    assert tea.mx4_status() == 0
