@@ -38,6 +38,9 @@
 namespace albert {
 namespace {
 
+// What the epilogue leaves (a kernel each: its code stays short).
+enum class Result { k16Bit, kF32, k4Bit };
+
 constexpr int kEpiWarps = 16, kEpi0 = 4;  // epilogue warps, the first of them
 constexpr int kThreads = 32 * (kEpi0 + kEpiWarps);
 constexpr int kTile = 2048;               // a staging tile: 32 rows of 64 bytes
@@ -142,13 +145,14 @@ __device__ __forceinline__ void add_tile16(uint32_t tile, int lane, bool f16, fl
     }
 }
 
-template <bool NV, bool PAIR, bool QOUT>
+template <bool NV, bool PAIR, Result OUT>
 __global__ void __launch_bounds__(kThreads, 1)
 mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                 const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
                 const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ CUtensorMap tmRes, const Mx4GemmArgs p,
                 int n_sub, int tma_out, int tma_res) {
     using P = Plan<NV, PAIR>;
+    constexpr bool QOUT = OUT == Result::k4Bit, f32 = OUT == Result::kF32;
     constexpr int NST = P::NST, TN = P::TN, ST = P::ST;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -367,7 +371,6 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         float *bias_s = sBias + ew * 64;  // two chunks' biases
         const uint32_t stg = smem_u32(sStg + ew * kStgBytes), rbar = smem_u32(&c.rbar[ew]);
         const bool res = !QOUT && p.res != nullptr;
-        const bool f32 = p.out_type == kElemF32;
         uint32_t t = 0, rph = 0, stores = 0, chunks = 0;
         bool res_pending = false;
         // this warp's i-th chunk of a tile: the first accumulator of a pair is read from its
@@ -482,7 +485,7 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                     }
                 } else {
                     const int rows = n_rows - row0 < 32 ? n_rows - row0 : 32;  // of this warp's 32 that exist
-                    if (f32) {
+                    if constexpr (f32) {
                         // through the warp's own 4 KB: two tiles of 16 columns, a column per lane to and
                         // from global memory
                         const uint32_t tile = smem_u32(sStg) + ew * kStgBytes;
@@ -598,13 +601,13 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     if (threadIdx.x == 0 && *c.abort_flag) set_status(p.status, kStatusTimeout);
 }
 
-template <bool NV, bool PAIR, bool QOUT>
+template <bool NV, bool PAIR, Result OUT>
 cudaError_t configure() {
     static std::atomic<unsigned long long> done{0};
-    return ensure_smem_attr(reinterpret_cast<const void *>(mx4_gemm_kernel<NV, PAIR, QOUT>), Plan<NV, PAIR>::SMEM, done);
+    return ensure_smem_attr(reinterpret_cast<const void *>(mx4_gemm_kernel<NV, PAIR, OUT>), Plan<NV, PAIR>::SMEM, done);
 }
 
-template <bool NV, bool PAIR, bool QOUT>
+template <bool NV, bool PAIR, Result OUT>
 cudaError_t launch_tile(const Mx4GemmArgs &a, int num_sms, cudaStream_t s, bool pdl) {
     using P = Plan<NV, PAIR>;
     CUtensorMap tmA, tmB, tmSA, tmSB;
@@ -614,10 +617,10 @@ cudaError_t launch_tile(const Mx4GemmArgs &a, int num_sms, cudaStream_t s, bool 
         make_tmap_u8(&tmSA, a.a_scales, 2 * ta, 256, 256, 2 * P::ST, false) ||
         make_tmap_u8(&tmSB, a.w_scales, 2 * tb, 256, 256, 2 * P::ST, false))
         return cudaErrorInvalidValue;
-    cudaError_t e = configure<NV, PAIR, QOUT>();
+    cudaError_t e = configure<NV, PAIR, OUT>();
     if (e != cudaSuccess) return e;
     // a 4-bit result's scale tiles reach to a multiple of 256 columns
-    const int n_sub = ((QOUT ? mx4_stages(a.N) * kMx4StageCols : a.N) + P::TN - 1) / P::TN;
+    const int n_sub = ((OUT == Result::k4Bit ? mx4_stages(a.N) * kMx4StageCols : a.N) + P::TN - 1) / P::TN;
     const long long units = (long long)((a.M + P::UM - 1) / P::UM) * n_sub;
     if (units > 0x7fffff00LL - num_sms) return cudaErrorInvalidValue;
     const int slots = PAIR ? num_sms / 2 : num_sms;
@@ -648,11 +651,11 @@ cudaError_t launch_tile(const Mx4GemmArgs &a, int num_sms, cudaStream_t s, bool 
     cfg.stream = s;
     cfg.attrs = attr;
     cfg.numAttrs = na;
-    return cudaLaunchKernelEx(&cfg, mx4_gemm_kernel<NV, PAIR, QOUT>, tmA, tmB, tmSA, tmSB, tmOut, tmRes, a, n_sub, tma_out,
+    return cudaLaunchKernelEx(&cfg, mx4_gemm_kernel<NV, PAIR, OUT>, tmA, tmB, tmSA, tmSB, tmOut, tmRes, a, n_sub, tma_out,
                               tma_res);
 }
 
-template <bool NV, bool QOUT>
+template <bool NV, Result OUT>
 cudaError_t launch_fmt(const Mx4GemmArgs &a, int num_sms, cudaStream_t s, bool pdl) {
     // The cheaper of the two shapes by their waves: measured over 256..9000 rows, N 768..4096,
     // K 768..4096 (stages 3, 8, 16), a launch takes about 4.4 us + waves (0.6 + 0.30 stages)
@@ -664,16 +667,23 @@ cudaError_t launch_fmt(const Mx4GemmArgs &a, int num_sms, cudaStream_t s, bool p
     const long long pair = (long long)((a.M + 255) / 256) * ((a.N + 255) / 256);
     const long long waves1 = (single + num_sms - 1) / num_sms, waves2 = (pair + num_sms / 2 - 1) / (num_sms / 2);
     if (560 + waves2 * (70 + 44 * stages) < 440 + waves1 * (60 + 30 * stages))
-        return launch_tile<NV, true, QOUT>(a, num_sms, s, pdl);
-    return launch_tile<NV, false, QOUT>(a, num_sms, s, pdl);
+        return launch_tile<NV, true, OUT>(a, num_sms, s, pdl);
+    return launch_tile<NV, false, OUT>(a, num_sms, s, pdl);
 }
 
 }  // namespace
 
 cudaError_t launch_mx4_gemm(const Mx4GemmArgs &a, int num_sms, cudaStream_t s, bool pdl) {
     if (a.M < 1) return cudaSuccess;
-    if (a.q) return a.nv ? launch_fmt<true, true>(a, num_sms, s, pdl) : launch_fmt<false, true>(a, num_sms, s, pdl);
-    return a.nv ? launch_fmt<true, false>(a, num_sms, s, pdl) : launch_fmt<false, false>(a, num_sms, s, pdl);
+    switch (a.q ? Result::k4Bit : a.out_type == kElemF32 ? Result::kF32 : Result::k16Bit) {
+        case Result::k4Bit:
+            return a.nv ? launch_fmt<true, Result::k4Bit>(a, num_sms, s, pdl) : launch_fmt<false, Result::k4Bit>(a, num_sms, s, pdl);
+        case Result::kF32:
+            return a.nv ? launch_fmt<true, Result::kF32>(a, num_sms, s, pdl) : launch_fmt<false, Result::kF32>(a, num_sms, s, pdl);
+        case Result::k16Bit:
+            return a.nv ? launch_fmt<true, Result::k16Bit>(a, num_sms, s, pdl) : launch_fmt<false, Result::k16Bit>(a, num_sms, s, pdl);
+    }
+    return cudaErrorInvalidValue;
 }
 
 }  // namespace albert
