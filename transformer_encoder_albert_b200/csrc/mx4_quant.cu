@@ -342,9 +342,14 @@ mx4_norm_warp_kernel(const T *__restrict__ x, long long ld, const float *__restr
         for (; row < nr; row += stride) one_row(std::false_type{});
 }
 
-// The same with one CTA per row, for wider rows and for few of them: each warp holds
-// HELD of the row's 256-column chunks (every eighth); chunks beyond those are read
-// again in each pass (from L1 or L2).
+// The same with one CTA of W warps per row, for wider rows and for few of them: each warp
+// holds HELD of the row's 256-column chunks (every W-th); chunks beyond those are read
+// again in each pass (from L1 or L2). Over many rows what bounds it is the quantiser's
+// arithmetic and the two barriers a row, which few resident CTAs hide: 8192 rows of 2048
+// bf16 columns take 21 us with the next row's values under way (33 without), 8192 of 4096
+// 44 with sixteen warps (58 with eight that hold up to four chunks); rows past 4096
+// columns stay with eight that hold four (4096 rows of 8192: 47 us, 53 with 32 warps).
+template <int W>
 __device__ __forceinline__ float block_sum(float v, float *red) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
@@ -352,17 +357,17 @@ __device__ __forceinline__ float block_sum(float v, float *red) {
     __syncthreads();
     float s = 0.f;
 #pragma unroll
-    for (int i = 0; i < kQWarps; ++i) s += red[i];
+    for (int i = 0; i < W; ++i) s += red[i];
     return s;
 }
 
-template <typename T, bool NV, int HELD>
-__global__ void __launch_bounds__(32 * kQWarps)
+template <typename T, bool NV, int W, int HELD>
+__global__ void __launch_bounds__(32 * W)
 mx4_norm_cta_kernel(const T *__restrict__ x, long long ld, const float *__restrict__ gamma,
                     const float *__restrict__ beta, float eps, int rows, int cols, const int *n_rows, float ts,
                     T *__restrict__ y, long long ld_y, uint8_t *__restrict__ codes,
                     uint8_t *__restrict__ scales, int vec, int vec_y, int vec_g, const int *status, int trigger) {
-    __shared__ float red[2][kQWarps];  // one per sum: a row's second barrier separates its first from the next row's
+    __shared__ float red[2][W];  // one per sum: a row's second barrier separates its first from the next row's
     if (trigger) griddep_launch_dependents();
     griddep_wait();
     const Mx4Ts tsc = mx4_ts(ts);
@@ -372,12 +377,69 @@ mx4_norm_cta_kernel(const T *__restrict__ x, long long ld, const float *__restri
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int chunks = mx4_stages(cols), pitch = mx4_code_pitch(cols);
     const int row_tiles = chunks * Mx4<NV>::kStageTiles;
+    constexpr int kTileLanes = Mx4<NV>::kTileCols / 8;
+    if (HELD == 1 && cols % 8 == 0 && vec && vec_g == 2 && (!y || vec_y)) {
+        // A lane's eight columns all exist or none does: its parameters stay in registers, the
+        // next row's values load while this one's sums are joined.
+        const int col = warp * kMx4StageCols + lane * 8;
+        const bool here = col < cols;
+        float g[8] = {}, b[8] = {};
+        if (here) {
+            ld_cached_v8(gamma + col, g);
+            ld_cached_v8(beta + col, b);
+        }
+        int row = blockIdx.x;
+        Raw8<T> raw = load_raw8<T>(x + (size_t)row * ld + col, here && row < nr ? 8 : 0, true);
+        for (; row < nr; row += gridDim.x) {
+            float f[8];
+            raw8_values<T>(raw, f);
+            const int next = row + gridDim.x;
+            if (next < nr) raw = load_raw8<T>(x + (size_t)next * ld + col, here ? 8 : 0, true);
+            uint64_t v[4];
+            uint64_t s2 = f2_make(0.f, 0.f), q2 = s2;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[i] = f2_make(f[2 * i], f[2 * i + 1]);
+                s2 = f2_add(s2, v[i]);
+            }
+            const float2 sf = f2_split(s2);
+            const float mean = block_sum<W>(sf.x + sf.y, red[0]) / (float)cols;
+            const uint64_t nmean2 = f2_make(-mean, -mean);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[i] = f2_add(v[i], nmean2);
+                q2 = f2_fma(v[i], v[i], q2);
+            }
+            const float2 qf = f2_split(q2);
+            const float rstd = rsqrtf(block_sum<W>(here ? qf.x + qf.y : 0.f, red[1]) / (float)cols + eps);
+            const uint64_t rstd2 = f2_make(rstd, rstd);
+            if (warp >= chunks) continue;
+            float u[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 w = f2_split(f2_fma(f2_mul(v[i], rstd2), f2_make(g[2 * i], g[2 * i + 1]), f2_make(b[2 * i], b[2 * i + 1])));
+                u[2 * i] = here ? w.x : 0.f;
+                u[2 * i + 1] = here ? w.y : 0.f;
+            }
+            float m = fmax3_abs_nan(u[0], u[1], u[2]);
+            m = fmax3_abs_nan(m, u[3], u[4]);
+            m = fmax3_abs_nan(m, u[5], fmax3_abs_nan(u[6], u[7], 0.f));
+            if (y && here) store8<T>(y + (size_t)row * ld_y + col, 8, true, u);
+            uint32_t word;
+            const uint32_t q = mx4_warp_quant<NV>(u, abs_bits(m), tsc, lane, word);
+            if (col / 2 < pitch) *reinterpret_cast<uint32_t *>(codes + (size_t)row * pitch + col / 2) = q;
+            if (lane % kTileLanes == 0)
+                *reinterpret_cast<uint32_t *>(scales + scale_word_offset(row, warp * Mx4<NV>::kStageTiles + lane / kTileLanes,
+                                                                         row_tiles)) = word;
+        }
+        return;
+    }
     for (int row = blockIdx.x; row < nr; row += gridDim.x) {
         const T *src = x + (size_t)row * ld;
         Raw8<T> raw[HELD];
 #pragma unroll
         for (int h = 0; h < HELD; ++h) {
-            const int col = (warp + h * kQWarps) * kMx4StageCols + lane * 8;
+            const int col = (warp + h * W) * kMx4StageCols + lane * 8;
             raw[h] = load_raw8<T>(src + col, cols - col, vec != 0);
         }
         // f(chunk, first column, columns left, values): held chunks, then the others
@@ -385,12 +447,12 @@ mx4_norm_cta_kernel(const T *__restrict__ x, long long ld, const float *__restri
             float v[8];
 #pragma unroll
             for (int h = 0; h < HELD; ++h) {
-                const int c = warp + h * kQWarps, col = c * kMx4StageCols + lane * 8;
+                const int c = warp + h * W, col = c * kMx4StageCols + lane * 8;
                 if (c >= chunks) break;
                 raw8_values<T>(raw[h], v);
                 f(c, col, cols - col, v);
             }
-            for (int c = warp + HELD * kQWarps; c < chunks; c += kQWarps) {
+            for (int c = warp + HELD * W; c < chunks; c += W) {
                 const int col = c * kMx4StageCols + lane * 8;
                 load8<T>(src + col, cols - col, vec != 0, v);
                 f(c, col, cols - col, v);
@@ -401,7 +463,7 @@ mx4_norm_cta_kernel(const T *__restrict__ x, long long ld, const float *__restri
 #pragma unroll
             for (int i = 0; i < 8; ++i) sum += v[i];
         });
-        const float mean = block_sum(sum, red[0]) / (float)cols;
+        const float mean = block_sum<W>(sum, red[0]) / (float)cols;
         float sq = 0.f;
         each([&](int, int, int n, const float (&v)[8]) {
 #pragma unroll
@@ -410,7 +472,7 @@ mx4_norm_cta_kernel(const T *__restrict__ x, long long ld, const float *__restri
                 sq = fmaf(d, d, sq);
             }
         });
-        const float rstd = rsqrtf(block_sum(sq, red[1]) / (float)cols + eps);
+        const float rstd = rsqrtf(block_sum<W>(sq, red[1]) / (float)cols + eps);
         each([&](int c, int col, int n, float (&v)[8]) {
             float g[8], b[8];
             load8<float>(gamma + col, n, vec_g != 0, g);
@@ -425,7 +487,6 @@ mx4_norm_cta_kernel(const T *__restrict__ x, long long ld, const float *__restri
             uint32_t word;
             const uint32_t q = mx4_warp_quant<NV>(v, m, tsc, lane, word);
             if (col / 2 < pitch) *reinterpret_cast<uint32_t *>(codes + (size_t)row * pitch + col / 2) = q;
-            constexpr int kTileLanes = Mx4<NV>::kTileCols / 8;
             if (lane % kTileLanes == 0)
                 *reinterpret_cast<uint32_t *>(scales + scale_word_offset(row, c * Mx4<NV>::kStageTiles + lane / kTileLanes,
                                                                          row_tiles)) = word;
@@ -444,7 +505,7 @@ __global__ void amax_bf16_kernel(const bf16 *__restrict__ x, size_t n, unsigned 
 
 // CTAs of `kernel` that are resident at once (asked once per device), at most `need`.
 template <typename K>
-cudaError_t resident_grid(K kernel, std::atomic<int> (&cached)[64], long long need, int &blocks) {
+cudaError_t resident_grid(K kernel, std::atomic<int> (&cached)[64], long long need, int &blocks, int warps = kQWarps) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
@@ -452,7 +513,7 @@ cudaError_t resident_grid(K kernel, std::atomic<int> (&cached)[64], long long ne
     if (cap == 0) {
         int sms = 0, per_sm = 0;
         e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, 32 * kQWarps, 0);
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, 32 * warps, 0);
         if (e != cudaSuccess) return e;
         cap = (per_sm > 0 ? per_sm : 1) * sms;
         if (dev < 64) cached[dev].store(cap, std::memory_order_release);
@@ -504,18 +565,18 @@ cudaError_t dequant_typed(const uint8_t *codes, const uint8_t *scales, int rows,
 }
 
 template <typename T, bool NV, typename K>
-cudaError_t norm_launch(K kernel, std::atomic<int> (&cached)[64], int rows_per_cta, const Mx4NormArgs &a, cudaStream_t s,
+cudaError_t norm_launch(K kernel, std::atomic<int> (&cached)[64], int rows_per_cta, int warps, const Mx4NormArgs &a, cudaStream_t s,
                         bool pdl) {
     int blocks = 0;
-    cudaError_t e = resident_grid(kernel, cached, (a.q.rows + rows_per_cta - 1) / rows_per_cta, blocks);
+    cudaError_t e = resident_grid(kernel, cached, (a.q.rows + rows_per_cta - 1) / rows_per_cta, blocks, warps);
     if (e != cudaSuccess) return e;
     const int vec = aligned16(a.q.x, a.q.ld, sizeof(T)), vec_y = aligned16(a.y, a.ld_y, sizeof(T));
     const int vec_g = std::min(vec_width(a.gamma, 8, 4), vec_width(a.beta, 8, 4));
     if (pdl)
-        return launch_pdl(kernel, dim3(blocks), dim3(32 * kQWarps), 0, s, static_cast<const T *>(a.q.x), a.q.ld, a.gamma,
+        return launch_pdl(kernel, dim3(blocks), dim3(32 * warps), 0, s, static_cast<const T *>(a.q.x), a.q.ld, a.gamma,
                           a.beta, a.eps, a.q.rows, a.q.cols, a.q.n_rows, a.q.tensor_scale, static_cast<T *>(a.y),
                           a.ld_y, a.q.codes, a.q.scales, vec, vec_y, vec_g, a.q.status, a.q.trigger);
-    kernel<<<blocks, 32 * kQWarps, 0, s>>>(static_cast<const T *>(a.q.x), a.q.ld, a.gamma, a.beta, a.eps, a.q.rows,
+    kernel<<<blocks, 32 * warps, 0, s>>>(static_cast<const T *>(a.q.x), a.q.ld, a.gamma, a.beta, a.eps, a.q.rows,
                                            a.q.cols, a.q.n_rows, a.q.tensor_scale, static_cast<T *>(a.y), a.ld_y,
                                            a.q.codes, a.q.scales, vec, vec_y, vec_g, a.q.status, a.q.trigger);
     return cudaGetLastError();
@@ -525,13 +586,14 @@ template <typename T, bool NV>
 cudaError_t norm_typed(const Mx4NormArgs &a, cudaStream_t s, bool pdl) {
     // A warp per row once the rows fill the machine's warps several times over; a CTA per
     // row for few rows (5 rows of 1000: 4.4 us against 7.9) and for rows a warp cannot hold
-    // in half its registers.
-    static std::atomic<int> c1[64], c3[64], w1[64], w4[64];
-    if (a.q.cols <= 256) return norm_launch<T, NV>(mx4_norm_warp_kernel<T, NV, 1>, c1, kQWarps, a, s, pdl);
+    // in half its registers; both sides of the widths at the kernel above.
+    static std::atomic<int> c1[64], c3[64], w8[64], w16[64], w8x4[64];
+    if (a.q.cols <= 256) return norm_launch<T, NV>(mx4_norm_warp_kernel<T, NV, 1>, c1, kQWarps, kQWarps, a, s, pdl);
     if (a.q.cols <= 768 && a.q.rows >= 512)
-        return norm_launch<T, NV>(mx4_norm_warp_kernel<T, NV, 3>, c3, kQWarps, a, s, pdl);
-    if (a.q.cols <= 2048) return norm_launch<T, NV>(mx4_norm_cta_kernel<T, NV, 1>, w1, 1, a, s, pdl);
-    return norm_launch<T, NV>(mx4_norm_cta_kernel<T, NV, 4>, w4, 1, a, s, pdl);
+        return norm_launch<T, NV>(mx4_norm_warp_kernel<T, NV, 3>, c3, kQWarps, kQWarps, a, s, pdl);
+    if (a.q.cols <= 2048) return norm_launch<T, NV>(mx4_norm_cta_kernel<T, NV, 8, 1>, w8, 1, 8, a, s, pdl);
+    if (a.q.cols <= 4096) return norm_launch<T, NV>(mx4_norm_cta_kernel<T, NV, 16, 1>, w16, 1, 16, a, s, pdl);
+    return norm_launch<T, NV>(mx4_norm_cta_kernel<T, NV, 8, 4>, w8x4, 1, 8, a, s, pdl);
 }
 
 }  // namespace
