@@ -58,12 +58,14 @@ struct Plan {
     static constexpr int NST = 4;
     static constexpr int ACC1 = PAIR ? 160 : 128;            // first column of the second accumulator
     static constexpr int SFCOL = PAIR ? 416 : 256;           // first scale column
-    static constexpr int SFBUF = 4 * ST * (1 + TN / 128);    // scale columns per stage
+    static constexpr int UNITS = ST / 2;                     // scale units per stage: two tiles of each 128 rows
+    static constexpr int SFUNIT = 8 * (1 + TN / 128);        // scale columns per unit
+    static constexpr int SFR = 4;                            // units in tensor memory
     static constexpr int PER = TN / 128;                     // 32-column chunks per epilogue warp
     static constexpr int SMEM = 1024 + NST * STAGE + kEpiWarps * (kStgBytes + 256) + 512;
-    static_assert(SFCOL + 2 * SFBUF <= 512, "tensor memory columns");
+    static_assert(SFCOL + SFR * SFUNIT <= 512, "tensor memory columns");
     static_assert(SMEM + 64 <= 232448, "shared memory per CTA, the wait limit included");
-    static_assert((2 * NST + 8 + kEpiWarps) * 8 + 32 <= 512, "barriers");
+    static_assert((2 * NST + 12 + kEpiWarps) * 8 + 32 <= 512, "barriers");
 };
 
 // Walk over a CTA's tiles, unit u = tile (u / n_sub, u % n_sub), by additions.
@@ -87,7 +89,7 @@ struct TileWalk {
 };
 
 struct Ctrl {
-    uint64_t *full, *empty, *sfull, *tfull, *tfree, *drain, *sdrain, *rbar;
+    uint64_t *full, *empty, *sfull, *half, *tfull, *tfree, *drain, *sdrain, *rbar;
     uint32_t *tmem_slot;
     volatile int *abort_flag;
     int *misc;
@@ -164,12 +166,13 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
     c.full = bars;
     c.empty = bars + NST;
     c.sfull = bars + 2 * NST;
-    c.tfull = bars + 2 * NST + 2;
-    c.tfree = bars + 2 * NST + 4;
-    c.drain = bars + 2 * NST + 6;
-    c.sdrain = bars + 2 * NST + 7;
-    c.rbar = bars + 2 * NST + 8;
-    uint32_t *u32 = reinterpret_cast<uint32_t *>(bars + 2 * NST + 8 + kEpiWarps);
+    c.half = bars + 2 * NST + 4;
+    c.tfull = bars + 2 * NST + 6;
+    c.tfree = bars + 2 * NST + 8;
+    c.drain = bars + 2 * NST + 10;
+    c.sdrain = bars + 2 * NST + 11;
+    c.rbar = bars + 2 * NST + 12;
+    uint32_t *u32 = reinterpret_cast<uint32_t *>(bars + 2 * NST + 12 + kEpiWarps);
     c.tmem_slot = u32;
     c.abort_flag = reinterpret_cast<volatile int *>(u32 + 1);
     c.misc = reinterpret_cast<int *>(u32 + 2);
@@ -187,8 +190,9 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             mbar_init(smem_u32(&c.full[i]), 1);
             mbar_init(smem_u32(&c.empty[i]), 1);
         }
+        for (int i = 0; i < P::SFR; ++i) mbar_init(smem_u32(&c.sfull[i]), 2);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_u32(&c.sfull[i]), 2);
+            mbar_init(smem_u32(&c.half[i]), 1);
             mbar_init(smem_u32(&c.tfull[i]), 1);
             mbar_init(smem_u32(&c.tfree[i]), (PAIR ? 2 : 1) * kEpiWarps);
         }
@@ -231,48 +235,39 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 
     if (warp == 0) {
         // ------------------------------------------------------ TMA producer --
-        if (lane == 0) {
-            int stage = 0, issued = 0;
-            uint32_t phase = 0;
-            bool ok = true;
-            const int loaded = p.withhold_loads ? 0 : units;
-            for (TileWalk w(slot, nslots, n_sub); w.u < loaded && ok; w.next()) {
-                const int m = w.m, n = w.n;
-                for (int kb = 0; kb < kblocks; ++kb) {
-                    if (!mbar_wait(smem_u32(&c.empty[stage]), phase ^ 1, c.abort_flag)) {
-                        ok = false;
-                        break;
-                    }
-                    const uint32_t fb = smem_u32(&c.full[stage]);
-                    const uint32_t a = smem_u32(sA + stage * kRowsBytes), b = smem_u32(sB + stage * kRowsBytes);
-                    const uint32_t fa = smem_u32(sSA + stage * P::SFA), fs = smem_u32(sSB + stage * P::SFB);
-                    // scale maps: rows of 256 bytes, a stage of one 128-row tile is 2 ST of them
-                    const int ma = m * (P::UM / 128) + (int)rank;
-                    const int ya = (ma * kblocks + kb) * 2 * ST;
-                    if (PAIR) {
-                        const uint32_t fb0 = mapa_shared(fb, 0);
-                        if (rank == 0) mbar_arrive_expect_tx(fb, 2 * P::STAGE);
-                        tma_load_2d_pair(a, &tmA, fb0, kb * 128, ma * 128);
-                        tma_load_2d_pair(b, &tmB, fb0, kb * 128, n * TN + (int)rank * 128);
-                        tma_load_2d_pair(fa, &tmSA, fb0, 0, ya);
-                        tma_load_2d_pair(fs, &tmSB, fb0, 0, ((n * 2) * kblocks + kb) * 2 * ST);
-                        tma_load_2d_pair(fs + P::SFA, &tmSB, fb0, 0, ((n * 2 + 1) * kblocks + kb) * 2 * ST);
-                    } else {
-                        mbar_arrive_expect_tx(fb, P::STAGE);
-                        tma_load_2d(a, &tmA, fb, kb * 128, m * 128);
-                        tma_load_2d(b, &tmB, fb, kb * 128, n * TN);
-                        tma_load_2d(fa, &tmSA, fb, 0, ya);
-                        tma_load_2d(fs, &tmSB, fb, 0, (n * kblocks + kb) * 2 * ST);
-                    }
-                    ++issued;
-                    if (++stage == NST) { stage = 0; phase ^= 1; }
+        // (the whole warp in step here too)
+        const uint32_t leader = elect_leader();
+        int stage = 0, issued = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        const int loaded = p.withhold_loads ? 0 : units;
+        for (TileWalk w(slot, nslots, n_sub); w.u < loaded && ok; w.next()) {
+            // scale maps: rows of 256 bytes, a stage of one 128-row tile is 2 ST of them
+            const int ma = w.m * (P::UM / 128) + (int)rank, nb = w.n * TN + (int)rank * 128;
+            int ya = ma * kblocks * 2 * ST, yb = w.n * (TN / 128) * kblocks * 2 * ST;
+            for (int kb = 0; kb < kblocks; ++kb, ya += 2 * ST, yb += 2 * ST) {
+                if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&c.empty[stage]), phase ^ 1, c.abort_flag))) {
+                    ok = false;
+                    break;
                 }
+                const uint32_t full = smem_u32(c.full) + 8 * stage;
+                const uint32_t fb = PAIR ? mapa_shared(full, 0) : full;
+                if (leader && rank == 0) mbar_arrive_expect_tx(full, (PAIR ? 2 : 1) * P::STAGE);
+                __syncwarp();
+                const uint32_t fs = smem_u32(sSB) + stage * P::SFB;
+                tma_load_elected<PAIR>(leader, smem_u32(sA) + stage * kRowsBytes, &tmA, fb, kb * 128, ma * 128);
+                tma_load_elected<PAIR>(leader, smem_u32(sB) + stage * kRowsBytes, &tmB, fb, kb * 128, nb);
+                tma_load_elected<PAIR>(leader, smem_u32(sSA) + stage * P::SFA, &tmSA, fb, 0, ya);
+                tma_load_elected<PAIR>(leader, fs, &tmSB, fb, 0, yb);
+                if (PAIR) tma_load_elected<PAIR>(leader, fs + P::SFA, &tmSB, fb, 0, yb + kblocks * 2 * ST);
+                ++issued;
+                if (++stage == NST) { stage = 0; phase ^= 1; }
             }
-            if (!ok && rank == 0) {
-                for (int i = 0; i < NST && i < issued; ++i) {
-                    if (--stage < 0) { stage = NST - 1; phase ^= 1; }
-                    mbar_wait_drain(smem_u32(&c.full[stage]), phase);
-                }
+        }
+        if (!ok && rank == 0) {
+            for (int i = 0; i < NST && i < issued; ++i) {
+                if (--stage < 0) { stage = NST - 1; phase ^= 1; }
+                mbar_wait_drain(smem_u32(&c.full[stage]), phase);
             }
         }
     } else if (warp == 1) {
@@ -296,27 +291,33 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 }
                 const uint32_t d = tmem + (t & 1) * P::ACC1;
                 for (int kb = 0; kb < kblocks; ++kb, ++it) {
-                    // scales in tensor memory, operands in shared memory: the scale warp, which has
-                    // waited for the stage, arrives on the same barrier as its copies
-                    if (!wait(&c.sfull[it & 1], (it >> 1) & 1)) { ok = false; break; }
-                    tc_fence_after();
                     // (a descriptor's address field counts 16 bytes: a product's 32 bytes of K are 2)
                     const uint64_t da = da0 + stage * (kRowsBytes >> 4), db = db0 + stage * (kRowsBytes >> 4);
-                    const uint32_t ca = tmem + P::SFCOL + (it & 1) * P::SFBUF, cb = ca + 4 * ST;
-                    auto product = [&](int k, uint32_t who, uint32_t acc) {
-                        const int g = NV ? k : k >> 1;
-                        umma_mx4<NV, PAIR>(who, d, da + 2 * k, db + 2 * k, idesc_mx4<NV>(P::UM, TN, NV ? 0 : 2 * (k & 1)),
-                                           ca + 4 * g, cb + g * (TN / 128) * 4, acc);
-                    };
-                    product(0, leader, kb != 0);
                     const int left = p.K - kb * kMx4StageCols;
-                    if (left > 3 * 64) {
 #pragma unroll
-                        for (int k = 1; k < 4; ++k) product(k, leader, 1);
-                    } else {  // products past the last column are left out
+                    for (int h = 0; h < P::UNITS; ++h) {
+                        // scales in tensor memory, operands in shared memory: the scale warp, which has
+                        // waited for the stage, arrives on the same barrier as its copies
+                        const uint32_t j = it * P::UNITS + h;
+                        if (!wait(&c.sfull[j % P::SFR], (j / P::SFR) & 1)) { ok = false; break; }
+                        tc_fence_after();
+                        const uint32_t ca = tmem + P::SFCOL + (j % P::SFR) * P::SFUNIT, cb = ca + 8;
+                        auto product = [&](int i, uint32_t who, uint32_t acc) {
+                            const int g = NV ? i : i >> 1, k = h * (4 / P::UNITS) + i;
+                            umma_mx4<NV, PAIR>(who, d, da + 2 * k, db + 2 * k, idesc_mx4<NV>(P::UM, TN, NV ? 0 : 2 * (k & 1)),
+                                               ca + 4 * g, cb + g * (TN / 128) * 4, acc);
+                        };
+                        if (left > 3 * 64) {
 #pragma unroll
-                        for (int k = 1; k < 4; ++k) product(k, k * 64 < left ? leader : 0u, 1);
+                            for (int i = 0; i < 4 / P::UNITS; ++i) product(i, leader, h + i != 0 || kb != 0);
+                        } else {  // products past the last column are left out
+#pragma unroll
+                            for (int i = 0; i < 4 / P::UNITS; ++i)
+                                product(i, (h * (4 / P::UNITS) + i) * 64 < left ? leader : 0u, h + i != 0 || kb != 0);
+                        }
+                        if (h + 1 < P::UNITS) umma_commit_elected<PAIR>(leader, smem_u32(&c.half[it & 1]), 1);
                     }
+                    if (!ok) break;
                     umma_commit_elected<PAIR>(leader, smem_u32(c.empty) + 8 * stage, 3);
                     if (++stage == NST) stage = 0;
                 }
@@ -340,24 +341,36 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             for (int u = slot; u < units && ok; u += nslots) {
                 for (int kb = 0; kb < kblocks; ++kb, ++it) {
                     if (!wait(&c.full[stage], phase)) { ok = false; break; }
-                    if (it >= 2) {
-                        // the products that read these columns two stages ago have completed
-                        if (!wait(&c.empty[es], eph)) { ok = false; break; }
-                        if (++es == NST) { es = 0; eph ^= 1; }
-                    }
-                    tc_fence_after();
                     const uint64_t da = da0 + stage * (P::SFA >> 4), db = db0 + stage * (P::SFB >> 4);
-                    const uint32_t ca = tmem + P::SFCOL + (it & 1) * P::SFBUF, cb = ca + 4 * ST;
 #pragma unroll
-                    for (int g = 0; g < ST; ++g) {
-                        tmem_cp_scales<PAIR>(leader, ca + 4 * g, da + g * (kMx4TileBytes >> 4));
+                    for (int h = 0; h < P::UNITS; ++h) {
+                        // The products that read these columns four units ago have completed: one unit per
+                        // stage, and the full stage tells; two, and their own commits do.
+                        static_assert(P::UNITS == 2 || P::SFR >= NST, "a unit's columns outlive its stage");
+                        if (P::UNITS == 2 && it >= 2) {
+                            if (h == 0) {
+                                if (!wait(&c.half[it & 1], ((it - 2) >> 1) & 1)) { ok = false; break; }
+                            } else {
+                                if (!wait(&c.empty[es], eph)) { ok = false; break; }
+                                if (++es == NST) { es = 0; eph ^= 1; }
+                            }
+                        }
+                        tc_fence_after();
+                        const uint32_t j = it * P::UNITS + h;
+                        const uint32_t ca = tmem + P::SFCOL + (j % P::SFR) * P::SFUNIT, cb = ca + 8;
 #pragma unroll
-                        for (int h = 0; h < TN / 128; ++h)
-                            tmem_cp_scales<PAIR>(leader, cb + (g * (TN / 128) + h) * 4,
-                                                 db + ((h * P::SFA + g * kMx4TileBytes) >> 4));
+                        for (int i = 0; i < 2; ++i) {
+                            const int g = 2 * h + i;
+                            tmem_cp_scales<PAIR>(leader, ca + 4 * i, da + g * (kMx4TileBytes >> 4));
+#pragma unroll
+                            for (int b = 0; b < TN / 128; ++b)
+                                tmem_cp_scales<PAIR>(leader, cb + (i * (TN / 128) + b) * 4,
+                                                     db + ((b * P::SFA + g * kMx4TileBytes) >> 4));
+                        }
+                        umma_commit_elected<PAIR>(leader, smem_u32(&c.sfull[j % P::SFR]), 1);
+                        if (lane == 0) mbar_arrive(smem_u32(&c.sfull[j % P::SFR]));
                     }
-                    umma_commit_elected<PAIR>(leader, smem_u32(&c.sfull[it & 1]), 1);
-                    if (lane == 0) mbar_arrive(smem_u32(&c.sfull[it & 1]));
+                    if (!ok) break;
                     if (++stage == NST) { stage = 0; phase ^= 1; }
                 }
             }

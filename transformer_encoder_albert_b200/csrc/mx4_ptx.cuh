@@ -65,6 +65,21 @@ __device__ __forceinline__ void umma_commit_elected(uint32_t leader, uint32_t ba
                      ::"r"(bar), "r"(leader) : "memory");
 }
 
+// tma_load_2d / tma_load_2d_pair of the elected lane.
+template <bool PAIR>
+__device__ __forceinline__ void tma_load_elected(uint32_t leader, uint32_t dst, const void *tmap, uint32_t bar, int x, int y) {
+    if constexpr (PAIR)
+        asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+                     "@q cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+                     " [%0], [%1, {%3, %4}], [%2];\n\t}"
+                     ::"r"(dst), "l"(tmap), "r"(bar), "r"(x), "r"(y), "r"(leader) : "memory");
+    else
+        asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+                     "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+                     " [%0], [%1, {%3, %4}], [%2];\n\t}"
+                     ::"r"(dst), "l"(tmap), "r"(bar), "r"(x), "r"(y), "r"(leader) : "memory");
+}
+
 // Shared-memory descriptor of a scale tile: rows of 16 bytes, no swizzle, 8-row
 // groups 128 bytes apart (fields as in sw128_kmajor_desc).
 __device__ __forceinline__ uint64_t scale_tile_desc(uint32_t smem_addr) {
