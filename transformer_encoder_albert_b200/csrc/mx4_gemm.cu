@@ -39,15 +39,14 @@ namespace albert {
 namespace {
 
 // What the epilogue leaves (a kernel each: its code stays short).
-enum class Result { k16Bit, kF32, k4Bit };
+enum class Result { k16Bit, k16BitRes, kF32, k4Bit };  // (Res: + residual)
 
 constexpr int kEpiWarps = 16, kEpi0 = 4;  // epilogue warps, the first of them
 constexpr int kThreads = 32 * (kEpi0 + kEpiWarps);
 constexpr int kTile = 2048;               // a staging tile: 32 rows of 64 bytes
-constexpr int kStgBytes = 2 * kTile;      // per epilogue warp
 constexpr int kRowsBytes = 128 * 128;  // 128 rows x 256 columns of codes
 
-template <bool NV, bool PAIR>
+template <bool NV, bool PAIR, Result OUT>
 struct Plan {
     static constexpr int TN = PAIR ? 256 : 128;              // columns of a tile
     static constexpr int UM = PAIR ? 256 : 128;              // rows of a tile
@@ -55,16 +54,22 @@ struct Plan {
     static constexpr int SFA = ST * kMx4TileBytes;
     static constexpr int SFB = (TN / 128) * SFA;
     static constexpr int STAGE = 2 * kRowsBytes + SFA + SFB;  // bytes per CTA and stage
-    static constexpr int NST = 4;
+    static constexpr int STG = (OUT == Result::k4Bit ? 0 : OUT == Result::k16Bit ? 1 : 2) * kTile;  // per epilogue warp
+    static constexpr int BIAS = OUT == Result::k4Bit ? 64 : 32;  // biases per epilogue warp
+    // As many stages as fit beside the staging tiles, at most six: a fifth takes 8192^3 from
+    // 197 to 190 us (mxfp4) and 18797 rows of 2048 -> 768 from 17.6 to 17.1.
+    static constexpr int ROOM = (232448 - 64 - 1024 - 512 - kEpiWarps * (STG + 4 * BIAS)) / STAGE;
+    static constexpr int NST = ROOM < 6 ? ROOM : 6;
     static constexpr int ACC1 = PAIR ? 160 : 128;            // first column of the second accumulator
     static constexpr int SFCOL = PAIR ? 416 : 256;           // first scale column
     static constexpr int UNITS = ST / 2;                     // scale units per stage: two tiles of each 128 rows
     static constexpr int SFUNIT = 8 * (1 + TN / 128);        // scale columns per unit
     static constexpr int SFR = 4;                            // units in tensor memory
     static constexpr int PER = TN / 128;                     // 32-column chunks per epilogue warp
-    static constexpr int SMEM = 1024 + NST * STAGE + kEpiWarps * (kStgBytes + 256) + 512;
+    static constexpr int SMEM = 1024 + NST * STAGE + kEpiWarps * (STG + 4 * BIAS) + 512;
     static_assert(SFCOL + SFR * SFUNIT <= 512, "tensor memory columns");
     static_assert(SMEM + 64 <= 232448, "shared memory per CTA, the wait limit included");
+    static_assert(NST >= 4, "stages");
     static_assert((2 * NST + 12 + kEpiWarps) * 8 + 32 <= 512, "barriers");
 };
 
@@ -153,15 +158,15 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 const __grid_constant__ CUtensorMap tmSA, const __grid_constant__ CUtensorMap tmSB,
                 const __grid_constant__ CUtensorMap tmOut, const __grid_constant__ CUtensorMap tmRes, const Mx4GemmArgs p,
                 int n_sub, int tma_out, int tma_res) {
-    using P = Plan<NV, PAIR>;
-    constexpr bool QOUT = OUT == Result::k4Bit, f32 = OUT == Result::kF32;
+    using P = Plan<NV, PAIR, OUT>;
+    constexpr bool QOUT = OUT == Result::k4Bit, f32 = OUT == Result::kF32, RES = OUT == Result::k16BitRes;
     constexpr int NST = P::NST, TN = P::TN, ST = P::ST;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t *sA = base, *sB = sA + NST * kRowsBytes, *sSA = sB + NST * kRowsBytes, *sSB = sSA + NST * P::SFA;
     uint8_t *sStg = sSB + NST * P::SFB;  // (a multiple of 1024 from base: the stages and scale tiles are)
-    float *sBias = reinterpret_cast<float *>(sStg + kEpiWarps * kStgBytes);
-    uint64_t *bars = reinterpret_cast<uint64_t *>(reinterpret_cast<uint8_t *>(sBias) + kEpiWarps * 256);
+    float *sBias = reinterpret_cast<float *>(sStg + kEpiWarps * P::STG);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(reinterpret_cast<uint8_t *>(sBias) + kEpiWarps * 4 * P::BIAS);
     Ctrl c;
     c.full = bars;
     c.empty = bars + NST;
@@ -336,7 +341,7 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             };
             const uint64_t da0 = scale_tile_desc(smem_u32(sSA)), db0 = scale_tile_desc(smem_u32(sSB));
             uint32_t stage = 0, phase = 0, it = 0;
-            uint32_t es = 0, eph = 0;  // stage and phase of the stage before last
+            uint32_t es = 0, eph = 0;  // stage and phase of the stage whose scale columns come free next
             bool ok = true;
             for (int u = slot; u < units && ok; u += nslots) {
                 for (int kb = 0; kb < kblocks; ++kb, ++it) {
@@ -344,11 +349,11 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                     const uint64_t da = da0 + stage * (P::SFA >> 4), db = db0 + stage * (P::SFB >> 4);
 #pragma unroll
                     for (int h = 0; h < P::UNITS; ++h) {
-                        // The products that read these columns four units ago have completed: one unit per
-                        // stage, and the full stage tells; two, and their own commits do.
-                        static_assert(P::UNITS == 2 || P::SFR >= NST, "a unit's columns outlive its stage");
-                        if (P::UNITS == 2 && it >= 2) {
-                            if (h == 0) {
+                        // the products that read these columns four units ago have completed (with four
+                        // stages of one unit each, the full stage tells)
+                        constexpr uint32_t kAgo = P::SFR / P::UNITS;  // in stages
+                        if ((P::UNITS == 2 || NST > P::SFR) && it >= kAgo) {
+                            if (h + 1 < P::UNITS) {
                                 if (!wait(&c.half[it & 1], ((it - 2) >> 1) & 1)) { ok = false; break; }
                             } else {
                                 if (!wait(&c.empty[es], eph)) { ok = false; break; }
@@ -381,15 +386,15 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         // ---------------------------------------------------------- epilogue --
         constexpr int PER = P::PER;
         const int ew = warp - kEpi0, quad = warp & 3, part = ew >> 2;
-        float *bias_s = sBias + ew * 64;  // two chunks' biases
-        const uint32_t stg = smem_u32(sStg + ew * kStgBytes), rbar = smem_u32(&c.rbar[ew]);
-        const bool res = !QOUT && p.res != nullptr;
-        uint32_t t = 0, rph = 0, stores = 0, chunks = 0;
+        float *bias_s = sBias + ew * P::BIAS;  // one or two chunks' biases
+        const uint32_t stg = smem_u32(sStg + ew * P::STG), rbar = smem_u32(&c.rbar[ew]);
+        const bool res = RES || (f32 && p.res != nullptr);
+        uint32_t t = 0, rph = 0, chunks = 0;
         bool res_pending = false;
         // this warp's i-th chunk of a tile: the first accumulator of a pair is read from its
         // upper end, the second from its lower end, so that the overlap comes first
         auto chunk_of = [&](uint32_t tt, int i) { return (PAIR && (tt & 1) == 0) ? (TN / 32 - 1 - part) - 4 * i : part + 4 * i; };
-        // residual tiles use the second staging tile, results then only the first
+        // residual tiles use the second staging tile, results the first
         auto res_issue = [&](const TileWalk &w, uint32_t tt, int i) {
             if (lane == 0) {
                 mbar_arrive_expect_tx(rbar, kTile);
@@ -407,7 +412,7 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         TileWalk w(slot, nslots, n_sub), wn = w;  // this tile, the next
         if (w.u < units) {
             bnext = bias_load(w, 0, 0);
-            if (res && tma_res) res_issue(w, 0, 0);
+            if (RES && tma_res) res_issue(w, 0, 0);
         }
         bool ok = true;
         for (; w.u < units && ok; w = wn, ++t) {
@@ -424,7 +429,7 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 const int ch = chunk_of(t, i);
                 uint32_t r[32];
                 tmem_ld32(tb + ch * 32, r);
-                float *bs = bias_s + (chunks & 1) * 32;  // (its readers, two chunks ago, have passed a __syncwarp since)
+                float *bs = bias_s + (P::BIAS == 64 ? (chunks & 1) * 32 : 0);  // (its readers have passed a __syncwarp since)
                 bs[lane] = bnext;
                 tmem_ld_wait();
                 if (i == 0) tc_fence_before();
@@ -501,7 +506,7 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                     if constexpr (f32) {
                         // through the warp's own 4 KB: two tiles of 16 columns, a column per lane to and
                         // from global memory
-                        const uint32_t tile = smem_u32(sStg) + ew * kStgBytes;
+                        const uint32_t tile = stg;
                         const uint32_t at = tile + (lane >> 4) * kTile + (lane & 3) * 4;
                         const int q0 = (lane >> 2) & 3;
                         __syncwarp();
@@ -532,11 +537,10 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                             for (int y = 0; y < rows; ++y) dst[(size_t)y * p.ld_out] = ld_shared_u1(at + stg_off(y, q0));
                         }
                     } else {
-                        // a 16-bit 32x32 tile; with a residual that came by TMA into the second tile,
-                        // results use the first
+                        // a 16-bit 32x32 tile
                         const bool f16 = p.out_type == kElemF16;
-                        const uint32_t rtile = stg + kTile, tile = res ? stg : stg + (stores & 1) * kTile;
-                        if (res) {
+                        const uint32_t rtile = stg + kTile, tile = stg;
+                        if constexpr (RES) {
                             if (tma_res) {
                                 bool rok = mbar_wait(rbar, rph, c.abort_flag);
                                 if (!__all_sync(0xffffffffu, rok)) { ok = false; break; }
@@ -571,8 +575,7 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                         }
                         // the store that last used this tile has read it (lane 0 has the stores, the
                         // other lanes empty groups: no branch)
-                        if (res) bulk_wait_read0();
-                        else bulk_wait_read1();
+                        bulk_wait_read0();
                         __syncwarp();
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
@@ -583,7 +586,6 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                             __syncwarp();
                             tma_store_if(lane == 0 && left > 0 && row0 < n_rows, &tmOut, tile, col0, row0);
                             bulk_commit();
-                            ++stores;
                         } else {
                             __syncwarp();
                             if (lane < left) {
@@ -617,12 +619,12 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 template <bool NV, bool PAIR, Result OUT>
 cudaError_t configure() {
     static std::atomic<unsigned long long> done{0};
-    return ensure_smem_attr(reinterpret_cast<const void *>(mx4_gemm_kernel<NV, PAIR, OUT>), Plan<NV, PAIR>::SMEM, done);
+    return ensure_smem_attr(reinterpret_cast<const void *>(mx4_gemm_kernel<NV, PAIR, OUT>), Plan<NV, PAIR, OUT>::SMEM, done);
 }
 
 template <bool NV, bool PAIR, Result OUT>
 cudaError_t launch_tile(const Mx4GemmArgs &a, int num_sms, cudaStream_t s, bool pdl) {
-    using P = Plan<NV, PAIR>;
+    using P = Plan<NV, PAIR, OUT>;
     CUtensorMap tmA, tmB, tmSA, tmSB;
     const int pitch = mx4_code_pitch(a.K), stages = mx4_stages(a.K);
     const uint64_t ta = (uint64_t)((a.M + 127) / 128) * stages * P::ST, tb = (uint64_t)((a.N + 127) / 128) * stages * P::ST;
@@ -688,11 +690,13 @@ cudaError_t launch_fmt(const Mx4GemmArgs &a, int num_sms, cudaStream_t s, bool p
 
 cudaError_t launch_mx4_gemm(const Mx4GemmArgs &a, int num_sms, cudaStream_t s, bool pdl) {
     if (a.M < 1) return cudaSuccess;
-    switch (a.q ? Result::k4Bit : a.out_type == kElemF32 ? Result::kF32 : Result::k16Bit) {
+    switch (a.q ? Result::k4Bit : a.out_type == kElemF32 ? Result::kF32 : a.res ? Result::k16BitRes : Result::k16Bit) {
         case Result::k4Bit:
             return a.nv ? launch_fmt<true, Result::k4Bit>(a, num_sms, s, pdl) : launch_fmt<false, Result::k4Bit>(a, num_sms, s, pdl);
         case Result::kF32:
             return a.nv ? launch_fmt<true, Result::kF32>(a, num_sms, s, pdl) : launch_fmt<false, Result::kF32>(a, num_sms, s, pdl);
+        case Result::k16BitRes:
+            return a.nv ? launch_fmt<true, Result::k16BitRes>(a, num_sms, s, pdl) : launch_fmt<false, Result::k16BitRes>(a, num_sms, s, pdl);
         case Result::k16Bit:
             return a.nv ? launch_fmt<true, Result::k16Bit>(a, num_sms, s, pdl) : launch_fmt<false, Result::k16Bit>(a, num_sms, s, pdl);
     }
