@@ -60,7 +60,8 @@ def _weight(rng, n, k, fmt, std=0.05):
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("dtype", list(DTYPES))
 @pytest.mark.parametrize("rows,cols,pad", [(1, 1, 0), (1, 768, 0), (3, 16, 0), (5, 33, 0), (129, 256, 0), (130, 1000, 8),
-                                            (257, 257, 3), (64, 2048, 0)])
+                                            (257, 257, 3), (64, 2048, 0), (1300, 1001, 0), (70, 511, 2), (33, 770, 1),
+                                            (3, 2, 1)])
 def test_codes_and_scales_are_bit_exact(rows, cols, pad, dtype, fmt):
     rng = np.random.default_rng(rows * 7 + cols)
     x, t = _rows(rng, rows, cols + pad, dtype, 2.0)
@@ -145,6 +146,35 @@ def test_read_back_leaves_the_bytes_between_rows_alone():
     tea.mx4_dequantize(q, out=buf[:, :70])
     assert torch.all(buf[:, 70:] == 7)
     assert torch.equal(buf[:, :70], tea.mx4_dequantize(q, dtype=torch.float16))
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("cols,width,offset", [(1, 3, 1), (255, 257, 1), (256, 259, 2), (257, 261, 3), (513, 514, 0),
+                                               (512, 515, 1), (770, 784, 8)])
+def test_rows_at_any_offset_of_a_wider_buffer(cols, width, offset, dtype):
+    """Odd offsets and strides: the values of the same rows laid out whole, nothing beside them."""
+    rng = np.random.default_rng(cols + offset)
+    _, t = _rows(rng, 67, width, dtype)
+    part = t[:, offset:offset + cols]
+    q, whole = tea.mx4_quantize(part, "nvfp4", 0.01), tea.mx4_quantize(part.contiguous(), "nvfp4", 0.01)
+    assert torch.equal(q.codes, whole.codes) and torch.equal(q.scales, whole.scales)
+    buf = torch.full((67, width), 7.0, device="cuda", dtype=DTYPES[dtype])
+    tea.mx4_dequantize(q, out=buf[:, offset:offset + cols])
+    wide = torch.zeros((67, -(-cols // 16) * 16), device="cuda", dtype=DTYPES[dtype])
+    tea.mx4_dequantize(q, out=wide[:, :cols])   # (aligned rows)
+    assert torch.equal(buf[:, offset:offset + cols], wide[:, :cols])
+    buf[:, offset:offset + cols] = 7
+    assert torch.all(buf == 7) and torch.all(wide[:, cols:] == 0)
+    g, b = torch.randn(cols, device="cuda"), torch.randn(cols, device="cuda")
+    y, z = tea.mx4_layer_norm(part, g, b, 1e-5, "mxfp4")
+    wide[:, :cols] = part
+    y2, z2 = tea.mx4_layer_norm(wide[:, :cols], g, b, 1e-5, "mxfp4")
+    # each within the bound of the next test of the formula's value, then rounded to x's type
+    xd = part.double()
+    rstd = (xd.var(1, unbiased=False, keepdim=True) + 1e-5).rsqrt()
+    tol = (cols / 256 + 16) * 2.0 ** -23 * (xd.abs().amax(1, keepdim=True) * rstd * g.abs() + 4 * y2.double().abs() + b.abs())
+    step = _eps(dtype) * (y.double().abs() + y2.double().abs()) + (2.0 ** -24 if dtype == "fp16" else 0)
+    assert torch.all((y.double() - y2.double()).abs() <= 2 * tol + step)
 
 
 # ----------------------------------------------------------------- LayerNorm --

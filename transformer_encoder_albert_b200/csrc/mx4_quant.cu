@@ -91,11 +91,109 @@ __device__ __forceinline__ Raw16<T> load_raw16(const T *p, int n, int vec) {
     return r;
 }
 
-template <typename T, bool NV>
+// Rows that are aligned to their type only (an odd row stride): a warp moves 256 columns of
+// one row in consecutive 4-byte words, aligned down for 16-bit types, and hands them over
+// through shared memory -- one value per access cost a lane 16 loads or stores 32 bytes
+// apart (8192 x 1001 bf16: quantised in 11.9 us, 8.7 now; read back in 54, 7.1 now).
+template <typename T>
+constexpr int kSegWords = sizeof(T) == 4 ? 256 : 132;  // (16-bit: 129, up to a multiple of 16 bytes)
+template <typename T>
+struct Seg {
+    uint32_t w[sizeof(T) == 4 ? 8 : 5];
+};
+// 1 if a 16-bit row starts in the upper half of a 4-byte word.
+template <typename T>
+__device__ __forceinline__ int seg_shift(const T *p) {
+    return sizeof(T) == 4 ? 0 : (int)(reinterpret_cast<uintptr_t>(p) >> 1) & 1;
+}
+// The first n (at most 256) values at src; the others are 0.
+template <typename T>
+__device__ __forceinline__ Seg<T> seg_load(const T *src, int n, int lane) {
+    Seg<T> r;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            r.w[i] = lane + 32 * i < n ? __ldg(reinterpret_cast<const uint32_t *>(src) + lane + 32 * i) : 0u;
+    } else {
+        n = n < kMx4StageCols ? n : kMx4StageCols;
+        const int s = seg_shift(src);
+        const uint32_t *words = reinterpret_cast<const uint32_t *>(src - s);
+        const unsigned short *halves = reinterpret_cast<const unsigned short *>(src);
+#pragma unroll
+        for (int i = 0; i < 5; ++i) {
+            const int o = lane + 32 * i, lo = 2 * o - s, hi = lo + 1;  // word o holds values lo and hi
+            if (lo >= 0 && hi < n) {
+                r.w[i] = __ldg(words + o);
+            } else {
+                const uint32_t a = lo >= 0 && lo < n ? __ldg(halves + lo) : 0u, b = hi < n ? __ldg(halves + hi) : 0u;
+                r.w[i] = a | b << 16;
+            }
+        }
+    }
+    return r;
+}
+template <typename T>
+__device__ __forceinline__ void seg_stage(uint32_t *sw, const Seg<T> &r, int lane) {
+#pragma unroll
+    for (int i = 0; i < (sizeof(T) == 4 ? 8 : 4); ++i) sw[lane + 32 * i] = r.w[i];
+    if (sizeof(T) == 2 && lane == 0) sw[128] = r.w[4];
+}
+// NW words of values from value `first` (even) on, of a staged row with shift s.
+template <typename T, int NW>
+__device__ __forceinline__ void seg_read(const uint32_t *sw, int s, int first, uint32_t (&out)[NW]) {
+    const uint32_t *p = sw + first * (int)sizeof(T) / 4;
+#pragma unroll
+    for (int i = 0; i < NW; i += 4) {
+        const uint4 q = *reinterpret_cast<const uint4 *>(p + i);
+        out[i] = q.x;
+        out[i + 1] = q.y;
+        out[i + 2] = q.z;
+        out[i + 3] = q.w;
+    }
+    if (sizeof(T) == 2 && s) {
+        const uint32_t end = p[NW];
+#pragma unroll
+        for (int i = 0; i < NW; ++i) out[i] = __funnelshift_r(out[i], i + 1 < NW ? out[i + 1] : end, 16);
+    }
+}
+// n (at most 256) values from sw, value 0 in the lower half of its first word, to dst.
+template <typename T>
+__device__ __forceinline__ void seg_store(T *dst, int n, const uint32_t *sw, int lane) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (lane + 32 * i < n) reinterpret_cast<uint32_t *>(dst)[lane + 32 * i] = sw[lane + 32 * i];
+    } else {
+        n = n < kMx4StageCols ? n : kMx4StageCols;
+        const int s = seg_shift(dst);
+        uint32_t *words = reinterpret_cast<uint32_t *>(dst - s);  // as in seg_load
+        unsigned short *halves = reinterpret_cast<unsigned short *>(dst);
+        if (s) {
+            const uint32_t first = sw[0];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int o = lane + 32 * i;
+                if (o > 0 && 2 * o < n) words[o] = __funnelshift_r(sw[o - 1], sw[o], 16);
+            }
+            if (lane == 0 && n > 0) halves[0] = (unsigned short)first;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int o = lane + 32 * i;
+                if (2 * o + 1 < n) words[o] = sw[o];
+            }
+        }
+        if (lane == 1 && n > 0 && (n - 1 + s) % 2 == 0) halves[n - 1] = (unsigned short)(s ? sw[(n - 1) / 2] >> 16 : sw[(n - 1) / 2]);
+    }
+}
+
+template <typename T, bool NV, bool SEGS>  // SEGS: rows that are not 16-byte aligned
 __global__ void __launch_bounds__(32 * kQWarps)
 mx4_quant_kernel(const T *__restrict__ x, long long ld, int rows, int cols, const int *n_rows, float ts,
                  uint8_t *__restrict__ codes, uint8_t *__restrict__ scales, int vec, int pairs, const int *status,
                  int trigger) {
+    __shared__ uint4 seg4[SEGS ? kQWarps * 2 * kSegWords<T> / 4 : 1];
+    uint32_t *seg = reinterpret_cast<uint32_t *>(seg4) + (SEGS ? (threadIdx.x >> 5) * 2 * kSegWords<T> : 0);
     if (trigger) griddep_launch_dependents();
     griddep_wait();
     const Mx4Ts tsc = mx4_ts(ts);
@@ -106,12 +204,43 @@ mx4_quant_kernel(const T *__restrict__ x, long long ld, int rows, int cols, cons
     const int chunks = mx4_stages(cols), pitch = mx4_code_pitch(cols);
     const int row_tiles = chunks * Mx4<NV>::kStageTiles;
     Walk w(chunks, blockIdx.x * kQWarps + (threadIdx.x >> 5), gridDim.x * kQWarps);
-    auto load = [&]() {
-        const int row = w.row0() + 32 * lower, col = w.chunk * kMx4StageCols + sub * 16;
-        return load_raw16<T>(x + (size_t)row * ld + col, w.pair < pairs && row < nr ? cols - col : 0, vec);
+    struct Segs {
+        Seg<T> h[2];
     };
-    auto store = [&](const Raw16<T> &r, int row0, int chunk) {
+    using Raw = std::conditional_t<SEGS, Segs, Raw16<T>>;
+    auto load = [&]() -> Raw {
+        if constexpr (SEGS) {
+            Raw r;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int row = w.row0() + 32 * h, col = w.chunk * kMx4StageCols;
+                r.h[h] = seg_load<T>(x + (size_t)row * ld + col, w.pair < pairs && row < nr ? cols - col : 0, lane);
+            }
+            return r;
+        } else {
+            const int row = w.row0() + 32 * lower, col = w.chunk * kMx4StageCols + sub * 16;
+            return load_raw16<T>(x + (size_t)row * ld + col, w.pair < pairs && row < nr ? cols - col : 0, vec);
+        }
+    };
+    auto store = [&](const Raw &raw, int row0, int chunk) {
         const int row = row0 + 32 * lower, col = chunk * kMx4StageCols + sub * 16;
+        Raw16<T> r;
+        if constexpr (SEGS) {
+            constexpr int kHalf = 2 * sizeof(T);  // words of eight values
+            __syncwarp();
+            seg_stage<T>(seg, raw.h[0], lane);
+            seg_stage<T>(seg + kSegWords<T>, raw.h[1], lane);
+            __syncwarp();
+            uint32_t t[2 * kHalf];
+            seg_read<T>(seg + lower * kSegWords<T>, seg_shift(x + (size_t)row * ld), sub * 16, t);
+#pragma unroll
+            for (int i = 0; i < kHalf; ++i) {
+                r.h[0].w[i] = t[i];
+                r.h[1].w[i] = t[kHalf + i];
+            }
+        } else {
+            r = raw;
+        }
         uint32_t m;
         if constexpr (sizeof(T) == 4) {
             m = umax(raw8_amax<T>(r.h[0]), raw8_amax<T>(r.h[1]));
@@ -149,7 +278,7 @@ mx4_quant_kernel(const T *__restrict__ x, long long ld, int rows, int cols, cons
                                                                      row_tiles)) = word;
     };
     // the next item's rows load while the current ones are converted
-    Raw16<T> a = load(), b;
+    Raw a = load(), b;
     while (w.pair < pairs) {
         int row0 = w.row0(), chunk = w.chunk;
         w.next();
@@ -164,10 +293,12 @@ mx4_quant_kernel(const T *__restrict__ x, long long ld, int rows, int cols, cons
     }
 }
 
-template <typename T, bool NV>
+template <typename T, bool NV, bool SEGS>
 __global__ void __launch_bounds__(32 * kQWarps)
 mx4_dequant_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict__ scales, int rows, int cols, float ts,
                    T *__restrict__ out, long long ld, int vec, int pairs) {
+    __shared__ uint4 seg4[SEGS ? kQWarps * 2 * kSegWords<T> / 4 : 1];
+    uint32_t *seg = reinterpret_cast<uint32_t *>(seg4) + (SEGS ? (threadIdx.x >> 5) * 2 * kSegWords<T> : 0);
     const int lane = threadIdx.x & 31, sub = lane & 15, lower = lane >> 4;
     const int chunks = mx4_stages(cols), pitch = mx4_code_pitch(cols);
     const int row_tiles = chunks * Mx4<NV>::kStageTiles;
@@ -183,7 +314,7 @@ mx4_dequant_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict_
     };
     auto store = [&](uint2 q, uint32_t sb, int row0, int chunk) {
         const int row = row0 + 32 * lower, col = chunk * kMx4StageCols + sub * 16, n = cols - col;
-        if (row >= rows || n <= 0) return;
+        if (!SEGS && (row >= rows || n <= 0)) return;
         const float s = mx4_scale_value<NV>(sb);
         float v[2][8];
 #pragma unroll
@@ -196,7 +327,18 @@ mx4_dequant_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict_
             }
         }
         T *dst = out + (size_t)row * ld + col;
-        if (vec == 2 && n >= 16) {
+        if constexpr (SEGS) {
+            uint32_t *mine = seg + lower * kSegWords<T> + sub * 4 * sizeof(T);
+            __syncwarp();
+            store8<T>(reinterpret_cast<T *>(mine), 8, true, v[0]);
+            store8<T>(reinterpret_cast<T *>(mine) + 8, 8, true, v[1]);
+            __syncwarp();
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int r = row0 + 32 * h, c = chunk * kMx4StageCols;
+                if (r < rows) seg_store<T>(out + (size_t)r * ld + c, cols - c, seg + h * kSegWords<T>, lane);
+            }
+        } else if (vec == 2 && n >= 16) {
             if constexpr (sizeof(T) == 4) {
                 st_global_v8(dst, reinterpret_cast<const uint32_t *>(v[0]));
                 st_global_v8(dst + 8, reinterpret_cast<const uint32_t *>(v[1]));
@@ -342,13 +484,14 @@ mx4_norm_warp_kernel(const T *__restrict__ x, long long ld, const float *__restr
         for (; row < nr; row += stride) one_row(std::false_type{});
 }
 
-// The same with one CTA of W warps per row, for wider rows and for few of them: each warp
-// holds HELD of the row's 256-column chunks (every W-th); chunks beyond those are read
-// again in each pass (from L1 or L2). Over many rows what bounds it is the quantiser's
-// arithmetic and the two barriers a row, which few resident CTAs hide: 8192 rows of 2048
-// bf16 columns take 21 us with the next row's values under way (33 without), 8192 of 4096
-// 44 with sixteen warps (58 with eight that hold up to four chunks); rows past 4096
-// columns stay with eight that hold four (4096 rows of 8192: 47 us, 53 with 32 warps).
+// The same with one CTA of W warps per row, for rows of at most 256 W columns: each warp
+// has one of the row's 256-column chunks.  The next row's values load while this one's sums
+// are joined; the parameters stay in registers.  PLAIN: a lane's eight columns all exist or
+// none does, and rows are 16-byte aligned; else rows come and go by words through shared
+// memory.  Over many rows what bounds it is the quantiser's arithmetic and the two barriers
+// a row, which few resident CTAs hide: 8192 rows of 1000, 2048, 4096 bf16 columns take 11,
+// 21 and 44 us with four, eight and sixteen warps (17 for the first with eight; 25, 33 and
+// 58 in the kernel for wider rows).
 template <int W>
 __device__ __forceinline__ float block_sum(float v, float *red) {
 #pragma unroll
@@ -361,13 +504,14 @@ __device__ __forceinline__ float block_sum(float v, float *red) {
     return s;
 }
 
-template <typename T, bool NV, int W, int HELD>
+template <typename T, bool NV, int W, bool PLAIN>
 __global__ void __launch_bounds__(32 * W)
 mx4_norm_cta_kernel(const T *__restrict__ x, long long ld, const float *__restrict__ gamma,
                     const float *__restrict__ beta, float eps, int rows, int cols, const int *n_rows, float ts,
                     T *__restrict__ y, long long ld_y, uint8_t *__restrict__ codes,
                     uint8_t *__restrict__ scales, int vec, int vec_y, int vec_g, const int *status, int trigger) {
     __shared__ float red[2][W];  // one per sum: a row's second barrier separates its first from the next row's
+    __shared__ uint4 seg4[PLAIN ? 1 : W * kSegWords<T> / 4];
     if (trigger) griddep_launch_dependents();
     griddep_wait();
     const Mx4Ts tsc = mx4_ts(ts);
@@ -378,62 +522,110 @@ mx4_norm_cta_kernel(const T *__restrict__ x, long long ld, const float *__restri
     const int chunks = mx4_stages(cols), pitch = mx4_code_pitch(cols);
     const int row_tiles = chunks * Mx4<NV>::kStageTiles;
     constexpr int kTileLanes = Mx4<NV>::kTileCols / 8;
-    if (HELD == 1 && cols % 8 == 0 && vec && vec_g == 2 && (!y || vec_y)) {
-        // A lane's eight columns all exist or none does: its parameters stay in registers, the
-        // next row's values load while this one's sums are joined.
-        const int col = warp * kMx4StageCols + lane * 8;
-        const bool here = col < cols;
-        float g[8] = {}, b[8] = {};
-        if (here) {
+    uint32_t *seg = reinterpret_cast<uint32_t *>(seg4) + (PLAIN ? 0 : warp * kSegWords<T>);
+    using Raw = std::conditional_t<PLAIN, Raw8<T>, Seg<T>>;
+    const int col0 = warp * kMx4StageCols, col = col0 + lane * 8, n = cols - col;
+    float g[8] = {}, b[8] = {};
+    if constexpr (PLAIN) {
+        if (n > 0) {
             ld_cached_v8(gamma + col, g);
             ld_cached_v8(beta + col, b);
         }
-        int row = blockIdx.x;
-        Raw8<T> raw = load_raw8<T>(x + (size_t)row * ld + col, here && row < nr ? 8 : 0, true);
-        for (; row < nr; row += gridDim.x) {
-            float f[8];
-            raw8_values<T>(raw, f);
-            const int next = row + gridDim.x;
-            if (next < nr) raw = load_raw8<T>(x + (size_t)next * ld + col, here ? 8 : 0, true);
-            uint64_t v[4];
-            uint64_t s2 = f2_make(0.f, 0.f), q2 = s2;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[i] = f2_make(f[2 * i], f[2 * i + 1]);
-                s2 = f2_add(s2, v[i]);
-            }
-            const float2 sf = f2_split(s2);
-            const float mean = block_sum<W>(sf.x + sf.y, red[0]) / (float)cols;
-            const uint64_t nmean2 = f2_make(-mean, -mean);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[i] = f2_add(v[i], nmean2);
-                q2 = f2_fma(v[i], v[i], q2);
-            }
-            const float2 qf = f2_split(q2);
-            const float rstd = rsqrtf(block_sum<W>(here ? qf.x + qf.y : 0.f, red[1]) / (float)cols + eps);
-            const uint64_t rstd2 = f2_make(rstd, rstd);
-            if (warp >= chunks) continue;
-            float u[8];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 w = f2_split(f2_fma(f2_mul(v[i], rstd2), f2_make(g[2 * i], g[2 * i + 1]), f2_make(b[2 * i], b[2 * i + 1])));
-                u[2 * i] = here ? w.x : 0.f;
-                u[2 * i + 1] = here ? w.y : 0.f;
-            }
-            float m = fmax3_abs_nan(u[0], u[1], u[2]);
-            m = fmax3_abs_nan(m, u[3], u[4]);
-            m = fmax3_abs_nan(m, u[5], fmax3_abs_nan(u[6], u[7], 0.f));
-            if (y && here) store8<T>(y + (size_t)row * ld_y + col, 8, true, u);
-            uint32_t word;
-            const uint32_t q = mx4_warp_quant<NV>(u, abs_bits(m), tsc, lane, word);
-            if (col / 2 < pitch) *reinterpret_cast<uint32_t *>(codes + (size_t)row * pitch + col / 2) = q;
-            if (lane % kTileLanes == 0)
-                *reinterpret_cast<uint32_t *>(scales + scale_word_offset(row, warp * Mx4<NV>::kStageTiles + lane / kTileLanes,
-                                                                         row_tiles)) = word;
-        }
-        return;
+    } else {
+        load8<float>(gamma + col, n, vec_g != 0, g);
+        load8<float>(beta + col, n, vec_g != 0, b);
     }
+    auto load = [&](int row) -> Raw {
+        const T *src = x + (size_t)row * ld + col0;
+        if constexpr (PLAIN) return load_raw8<T>(src + lane * 8, row < nr && n > 0 ? 8 : 0, true);
+        else return seg_load<T>(src, row < nr ? cols - col0 : 0, lane);
+    };
+    int row = blockIdx.x;
+    Raw raw = load(row);
+    for (; row < nr; row += gridDim.x) {
+        Raw8<T> r;
+        if constexpr (PLAIN) {
+            r = raw;
+        } else {
+            __syncwarp();
+            seg_stage<T>(seg, raw, lane);
+            __syncwarp();
+            seg_read<T>(seg, seg_shift(x + (size_t)row * ld), lane * 8, r.w);
+        }
+        raw = load(row + gridDim.x);
+        float f[8];
+        raw8_values<T>(r, f);
+        uint64_t v[4];
+        uint64_t s2 = f2_make(0.f, 0.f), q2 = s2;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] = f2_make(f[2 * i], f[2 * i + 1]);
+            s2 = f2_add(s2, v[i]);
+        }
+        const float2 sf = f2_split(s2);
+        const float mean = block_sum<W>(sf.x + sf.y, red[0]) / (float)cols;
+        const uint64_t nmean2 = f2_make(-mean, -mean);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[i] = f2_add(v[i], nmean2);
+            if constexpr (!PLAIN) {
+                const float2 d = f2_split(v[i]);
+                v[i] = f2_make(2 * i < n ? d.x : 0.f, 2 * i + 1 < n ? d.y : 0.f);
+            }
+            q2 = f2_fma(v[i], v[i], q2);
+        }
+        const float2 qf = f2_split(q2);
+        const float rstd = rsqrtf(block_sum<W>(n > 0 ? qf.x + qf.y : 0.f, red[1]) / (float)cols + eps);
+        const uint64_t rstd2 = f2_make(rstd, rstd);
+        if (warp >= chunks) continue;
+        float u[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 w = f2_split(f2_fma(f2_mul(v[i], rstd2), f2_make(g[2 * i], g[2 * i + 1]),
+                                             f2_make(b[2 * i], b[2 * i + 1])));
+            u[2 * i] = (PLAIN ? n > 0 : 2 * i < n) ? w.x : 0.f;
+            u[2 * i + 1] = (PLAIN ? n > 0 : 2 * i + 1 < n) ? w.y : 0.f;
+        }
+        float m = fmax3_abs_nan(u[0], u[1], u[2]);
+        m = fmax3_abs_nan(m, u[3], u[4]);
+        m = fmax3_abs_nan(m, u[5], fmax3_abs_nan(u[6], u[7], 0.f));
+        if constexpr (PLAIN) {
+            if (y && n > 0) store8<T>(y + (size_t)row * ld_y + col, 8, true, u);
+        } else if (y) {  // (the staged row has been read: two barriers ago)
+            store8<T>(reinterpret_cast<T *>(seg) + lane * 8, 8, true, u);
+            __syncwarp();
+            seg_store<T>(y + (size_t)row * ld_y + col0, cols - col0, seg, lane);
+        }
+        uint32_t word;
+        const uint32_t q = mx4_warp_quant<NV>(u, abs_bits(m), tsc, lane, word);
+        if (col / 2 < pitch) *reinterpret_cast<uint32_t *>(codes + (size_t)row * pitch + col / 2) = q;
+        if (lane % kTileLanes == 0)
+            *reinterpret_cast<uint32_t *>(scales + scale_word_offset(row, warp * Mx4<NV>::kStageTiles + lane / kTileLanes,
+                                                                     row_tiles)) = word;
+    }
+}
+
+// Wider rows: one CTA per row, each warp holds four of the row's chunks (every eighth);
+// chunks beyond those are read again in each pass (from L1 or L2).  4096 rows of 8192 bf16
+// columns take 47 us; one chunk per warp and 32 warps 53.
+template <typename T, bool NV>
+__global__ void __launch_bounds__(32 * kQWarps)
+mx4_norm_wide_kernel(const T *__restrict__ x, long long ld, const float *__restrict__ gamma,
+                     const float *__restrict__ beta, float eps, int rows, int cols, const int *n_rows, float ts,
+                     T *__restrict__ y, long long ld_y, uint8_t *__restrict__ codes,
+                     uint8_t *__restrict__ scales, int vec, int vec_y, int vec_g, const int *status, int trigger) {
+    constexpr int W = kQWarps, HELD = 4;
+    __shared__ float red[2][W];  // as above
+    if (trigger) griddep_launch_dependents();
+    griddep_wait();
+    const Mx4Ts tsc = mx4_ts(ts);
+    if (status && *reinterpret_cast<const volatile int *>(status) != 0) return;
+    int nr = n_rows ? *reinterpret_cast<const volatile int *>(n_rows) : rows;
+    nr = nr < rows ? nr : rows;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int chunks = mx4_stages(cols), pitch = mx4_code_pitch(cols);
+    const int row_tiles = chunks * Mx4<NV>::kStageTiles;
+    constexpr int kTileLanes = Mx4<NV>::kTileCols / 8;
     for (int row = blockIdx.x; row < nr; row += gridDim.x) {
         const T *src = x + (size_t)row * ld;
         Raw8<T> raw[HELD];
@@ -530,38 +722,54 @@ inline int vec_width(const void *p, long long ld, int elem) {
     return (reinterpret_cast<uintptr_t>(p) & 31) == 0 && (ld * elem) % 32 == 0 ? 2 : aligned16(p, ld, elem) ? 1 : 0;
 }
 
-template <typename T, bool NV>
-cudaError_t quant_typed(const Mx4QuantArgs &a, cudaStream_t s, bool pdl) {
+template <typename T, bool NV, bool SEGS>
+cudaError_t quant_launch(const Mx4QuantArgs &a, int vec, cudaStream_t s, bool pdl) {
     // (all row pairs of the last tile, whose scale bytes are written whole)
     const int pairs = (a.rows + 127) / 128 * 64;
     const long long items = (long long)pairs * mx4_stages(a.cols);
     static std::atomic<int> cached[64];
     int blocks = 0;
-    cudaError_t e = resident_grid(mx4_quant_kernel<T, NV>, cached, (items + kQWarps - 1) / kQWarps, blocks);
+    auto kernel = mx4_quant_kernel<T, NV, SEGS>;
+    cudaError_t e = resident_grid(kernel, cached, (items + kQWarps - 1) / kQWarps, blocks);
     if (e != cudaSuccess) return e;
-    const int vec = vec_width(a.x, a.ld, sizeof(T));
     if (pdl)
-        return launch_pdl(mx4_quant_kernel<T, NV>, dim3(blocks), dim3(32 * kQWarps), 0, s, static_cast<const T *>(a.x),
-                          a.ld, a.rows, a.cols, a.n_rows, a.tensor_scale, a.codes, a.scales, vec, pairs, a.status,
-                          a.trigger);
-    mx4_quant_kernel<T, NV><<<blocks, 32 * kQWarps, 0, s>>>(static_cast<const T *>(a.x), a.ld, a.rows, a.cols, a.n_rows,
-                                                            a.tensor_scale, a.codes, a.scales, vec, pairs, a.status,
-                                                            a.trigger);
+        return launch_pdl(kernel, dim3(blocks), dim3(32 * kQWarps), 0, s, static_cast<const T *>(a.x), a.ld, a.rows, a.cols,
+                          a.n_rows, a.tensor_scale, a.codes, a.scales, vec, pairs, a.status, a.trigger);
+    kernel<<<blocks, 32 * kQWarps, 0, s>>>(static_cast<const T *>(a.x), a.ld, a.rows, a.cols, a.n_rows, a.tensor_scale,
+                                           a.codes, a.scales, vec, pairs, a.status, a.trigger);
     return cudaGetLastError();
 }
-
 template <typename T, bool NV>
-cudaError_t dequant_typed(const uint8_t *codes, const uint8_t *scales, int rows, int cols, float ts, void *out,
-                          long long ld, cudaStream_t s) {
+cudaError_t quant_typed(const Mx4QuantArgs &a, cudaStream_t s, bool pdl) {
+    const int vec = vec_width(a.x, a.ld, sizeof(T));
+    return vec ? quant_launch<T, NV, false>(a, vec, s, pdl) : quant_launch<T, NV, true>(a, vec, s, pdl);
+}
+
+template <typename T, bool NV, bool SEGS>
+cudaError_t dequant_launch(const uint8_t *codes, const uint8_t *scales, int rows, int cols, float ts, T *out, long long ld,
+                           int vec, cudaStream_t s) {
     const int pairs = (rows + 127) / 128 * 64;
     const long long items = (long long)pairs * mx4_stages(cols);
     static std::atomic<int> cached[64];
     int blocks = 0;
-    cudaError_t e = resident_grid(mx4_dequant_kernel<T, NV>, cached, (items + kQWarps - 1) / kQWarps, blocks);
+    auto kernel = mx4_dequant_kernel<T, NV, SEGS>;
+    cudaError_t e = resident_grid(kernel, cached, (items + kQWarps - 1) / kQWarps, blocks);
     if (e != cudaSuccess) return e;
-    mx4_dequant_kernel<T, NV><<<blocks, 32 * kQWarps, 0, s>>>(codes, scales, rows, cols, ts, static_cast<T *>(out), ld,
-                                                              vec_width(out, ld, sizeof(T)), pairs);
+    kernel<<<blocks, 32 * kQWarps, 0, s>>>(codes, scales, rows, cols, ts, out, ld, vec, pairs);
     return cudaGetLastError();
+}
+template <typename T, bool NV>
+cudaError_t dequant_typed(const uint8_t *codes, const uint8_t *scales, int rows, int cols, float ts, void *out,
+                          long long ld, cudaStream_t s) {
+    const int vec = vec_width(out, ld, sizeof(T));
+    return vec ? dequant_launch<T, NV, false>(codes, scales, rows, cols, ts, static_cast<T *>(out), ld, vec, s)
+               : dequant_launch<T, NV, true>(codes, scales, rows, cols, ts, static_cast<T *>(out), ld, vec, s);
+}
+
+// Whether rows of x and of y are 16-byte aligned.
+template <typename T>
+bool norm_aligned(const Mx4NormArgs &a) {
+    return aligned16(a.q.x, a.q.ld, sizeof(T)) && (!a.y || aligned16(a.y, a.ld_y, sizeof(T)));
 }
 
 template <typename T, bool NV, typename K>
@@ -582,18 +790,28 @@ cudaError_t norm_launch(K kernel, std::atomic<int> (&cached)[64], int rows_per_c
     return cudaGetLastError();
 }
 
+template <typename T, bool NV, int W>
+cudaError_t norm_rows(const Mx4NormArgs &a, cudaStream_t s, bool pdl) {
+    static std::atomic<int> plain[64], other[64];
+    if (a.q.cols % 8 == 0 && norm_aligned<T>(a) && vec_width(a.gamma, 8, 4) == 2 && vec_width(a.beta, 8, 4) == 2)
+        return norm_launch<T, NV>(mx4_norm_cta_kernel<T, NV, W, true>, plain, 1, W, a, s, pdl);
+    return norm_launch<T, NV>(mx4_norm_cta_kernel<T, NV, W, false>, other, 1, W, a, s, pdl);
+}
+
 template <typename T, bool NV>
 cudaError_t norm_typed(const Mx4NormArgs &a, cudaStream_t s, bool pdl) {
     // A warp per row once the rows fill the machine's warps several times over; a CTA per
-    // row for few rows (5 rows of 1000: 4.4 us against 7.9) and for rows a warp cannot hold
-    // in half its registers; both sides of the widths at the kernel above.
-    static std::atomic<int> c1[64], c3[64], w8[64], w16[64], w8x4[64];
+    // row for few rows (5 rows of 1000: 4.4 us against 7.9), for rows a warp cannot hold
+    // in half its registers, and for rows without alignment (8192 x 767: 16.6 us against
+    // 21); both sides of the other widths at the kernel above.
+    static std::atomic<int> c1[64], c3[64], wide[64];
     if (a.q.cols <= 256) return norm_launch<T, NV>(mx4_norm_warp_kernel<T, NV, 1>, c1, kQWarps, kQWarps, a, s, pdl);
-    if (a.q.cols <= 768 && a.q.rows >= 512)
+    if (a.q.cols <= 768 && a.q.rows >= 512 && norm_aligned<T>(a))
         return norm_launch<T, NV>(mx4_norm_warp_kernel<T, NV, 3>, c3, kQWarps, kQWarps, a, s, pdl);
-    if (a.q.cols <= 2048) return norm_launch<T, NV>(mx4_norm_cta_kernel<T, NV, 8, 1>, w8, 1, 8, a, s, pdl);
-    if (a.q.cols <= 4096) return norm_launch<T, NV>(mx4_norm_cta_kernel<T, NV, 16, 1>, w16, 1, 16, a, s, pdl);
-    return norm_launch<T, NV>(mx4_norm_cta_kernel<T, NV, 8, 4>, w8x4, 1, 8, a, s, pdl);
+    if (a.q.cols <= 1024) return norm_rows<T, NV, 4>(a, s, pdl);
+    if (a.q.cols <= 2048) return norm_rows<T, NV, 8>(a, s, pdl);
+    if (a.q.cols <= 4096) return norm_rows<T, NV, 16>(a, s, pdl);
+    return norm_launch<T, NV>(mx4_norm_wide_kernel<T, NV>, wide, 1, kQWarps, a, s, pdl);
 }
 
 }  // namespace
