@@ -130,6 +130,12 @@ __device__ __forceinline__ uint16_t ld_shared_u16(uint32_t a) {
     return v;
 }
 
+// Four bytes to shared memory, without registers in between; and all of this thread's.
+__device__ __forceinline__ void copy4_async(uint32_t dst, const void *src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // tma_store_2d of the lane whose predicate holds, without a branch.
 __device__ __forceinline__ void tma_store_if(bool on, const void *tmap, uint32_t src, int x, int y) {
     asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %4, 0;\n\t"
@@ -403,6 +409,19 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
             }
             res_pending = true;
         };
+        // fp32: two tiles of 16 columns; a lane copies its column of the residual rows, which are in
+        // place before the chunk's sums are (loaded on use, a few rows at a time, they made
+        // 8192 x 2304 x 1024 take 49 us instead of 42)
+        const uint32_t col_at = stg + (lane >> 4) * kTile + (lane & 3) * 4;
+        const int col_q = (lane >> 2) & 3;
+        auto res32_issue = [&](const TileWalk &w, uint32_t tt, int i) {
+            const int col = w.n * TN + chunk_of(tt, i) * 32 + lane, r0 = w.m * P::UM + (int)rank * 128 + quad * 32;
+            if (col >= p.N) return;
+            const uint32_t *src = static_cast<const uint32_t *>(p.res) + (size_t)r0 * p.ld_res + col;
+            const int rows = n_rows - r0 < 32 ? n_rows - r0 : 32;
+#pragma unroll 8
+            for (int y = 0; y < rows; ++y) copy4_async(col_at + stg_off(y, col_q), src + (size_t)y * p.ld_res);
+        };
         auto bias_load = [&](const TileWalk &w, uint32_t tt, int i) {
             const int col = w.n * TN + chunk_of(tt, i) * 32 + lane;
             return (p.bias && col < p.N) ? __ldg(p.bias + col) : 0.f;
@@ -413,6 +432,7 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         if (w.u < units) {
             bnext = bias_load(w, 0, 0);
             if (RES && tma_res) res_issue(w, 0, 0);
+            if (f32 && res) res32_issue(w, 0, 0);
         }
         bool ok = true;
         for (; w.u < units && ok; w = wn, ++t) {
@@ -504,22 +524,14 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 } else {
                     const int rows = n_rows - row0 < 32 ? n_rows - row0 : 32;  // of this warp's 32 that exist
                     if constexpr (f32) {
-                        // through the warp's own 4 KB: two tiles of 16 columns, a column per lane to and
-                        // from global memory
-                        const uint32_t tile = stg;
-                        const uint32_t at = tile + (lane >> 4) * kTile + (lane & 3) * 4;
-                        const int q0 = (lane >> 2) & 3;
+                        // through the warp's own 4 KB; a column per lane to and from global memory
                         __syncwarp();
                         if (res) {
-                            if (lane < left) {
-                                const uint32_t *src = static_cast<const uint32_t *>(p.res) + (size_t)row0 * p.ld_res + col0 + lane;
-#pragma unroll 8
-                                for (int y = 0; y < rows; ++y) st_shared_u1(at + stg_off(y, q0), src[(size_t)y * p.ld_res]);
-                            }
+                            copy_async_wait();
                             __syncwarp();
 #pragma unroll
                             for (int q = 0; q < 8; ++q) {
-                                const uint4 x = ld_shared_u4(tile + (q >> 2) * kTile + stg_off(lane, q & 3));
+                                const uint4 x = ld_shared_u4(stg + (q >> 2) * kTile + stg_off(lane, q & 3));
                                 v[4 * q] += __uint_as_float(x.x);
                                 v[4 * q + 1] += __uint_as_float(x.y);
                                 v[4 * q + 2] += __uint_as_float(x.z);
@@ -528,13 +540,19 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                         }
 #pragma unroll
                         for (int q = 0; q < 8; ++q)
-                            st_shared_u4(tile + (q >> 2) * kTile + stg_off(lane, q & 3),
+                            st_shared_u4(stg + (q >> 2) * kTile + stg_off(lane, q & 3),
                                          make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]),
                                                     __float_as_uint(v[4 * q + 2]), __float_as_uint(v[4 * q + 3])));
                         __syncwarp();
                         if (lane < left) {
                             uint32_t *dst = static_cast<uint32_t *>(p.out) + (size_t)row0 * p.ld_out + col0 + lane;
-                            for (int y = 0; y < rows; ++y) dst[(size_t)y * p.ld_out] = ld_shared_u1(at + stg_off(y, q0));
+#pragma unroll 8
+                            for (int y = 0; y < rows; ++y) dst[(size_t)y * p.ld_out] = ld_shared_u1(col_at + stg_off(y, col_q));
+                        }
+                        if (res) {
+                            __syncwarp();
+                            if (i + 1 < PER) res32_issue(w, t, i + 1);
+                            else if (wn.u < units) res32_issue(wn, t + 1, 0);
                         }
                     } else {
                         // a 16-bit 32x32 tile
@@ -602,6 +620,7 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
         }
         // outstanding copies finish before the CTA's shared memory goes away
         if (lane == 0) bulk_wait0();
+        if (f32) copy_async_wait();
         if (res_pending && lane == 0) mbar_wait_drain(rbar, rph);
         __syncwarp();
     }
