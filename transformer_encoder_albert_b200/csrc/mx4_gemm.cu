@@ -7,27 +7,33 @@
 // Persistent, one CTA per SM, warp-specialized:
 //   warp 0      : TMA producer: per stage 256 columns of A and W (128-byte rows,
 //                 128-byte swizzle) and their scale tiles (512 bytes per 128 rows and
-//                 four blocks, plain);
+//                 four blocks, plain); the whole warp in step, one elected lane issues
+//                 (117 cycles a stage; one lane inside a branch needed 374);
 //   warp 1      : issues four products of K = 64 per stage;
-//   warp 2      : issues the copies of a stage's scale tiles to tensor memory, one
-//                 stage ahead of the products (6 or 12 copies per stage at about 26
-//                 cycles each would cost the products' warp more than half their time);
+//   warp 2      : issues the copies of the scale tiles to tensor memory, ahead of the
+//                 products (6 or 12 copies per stage at about 26 cycles each would cost
+//                 the products' warp more than half their time);
 //   warps 4..19 : epilogue, four warps per lane quadrant, each every fourth 32-column
 //                 chunk (a chunk is some 190 dependent instructions: with two warps per
 //                 quadrant it took 1330 cycles, and K = 768 only gives a tile 1536);
-//                 16-bit rows leave through swizzled staging tiles by TMA, their residual
+//                 16-bit rows leave through a swizzled staging tile by TMA, their residual
 //                 tiles arrive by TMA a chunk ahead; fp32 and rows that are not 16-byte
 //                 aligned go a column per lane.
 // Two tile shapes:
 //   * a CTA pair per 256x256 tile (cta_group::2): each CTA stages 128 rows of A and of
 //     W and the scales of its A rows and of all W rows.  Two 256-column accumulators
 //     would fill tensor memory; they overlap by 96 columns, which leaves 96 for the
-//     scales (two stages).  The epilogue's first chunks cover the overlap, so the next
-//     tile's products start once those are in registers.
+//     scales.  The epilogue's first chunks cover the overlap, so the next tile's
+//     products start once those are in registers.
 //   * one CTA per 128x128 tile, two separate accumulators, for work that would leave
 //     pairs idle.
-// Scale columns are written again only after the products that read them have
-// completed (their stage's empty barrier), two stages later.
+// Tensor memory holds four scale units (a stage of mxfp4, half a stage of nvfp4, 24
+// columns on pairs).  A unit's columns are written again only after the products that
+// read them have completed: their stage's empty barrier, or the commit in its middle.
+// (With two whole stages of nvfp4 the copies waited for products: 8192^3 250 us, 245 now.)
+// What bounds it: at K = 768 the epilogue (18797 x 2304: 24.2 us, 86.6 MB of results alone
+// are 13 at the copy rate); at 8192^3 the power cap -- the main loop takes 654 (mxfp4) and
+// 705 (nvfp4) cycles a stage where the nominal rate is 512, at 1.6 GHz; 194 and 206 us.
 // Every wait is bounded; see the bf16 GEMM.
 #include <type_traits>
 
@@ -112,9 +118,6 @@ __device__ __forceinline__ uint4 ld_shared_u4(uint32_t a) {
     uint4 v;
     asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
     return v;
-}
-__device__ __forceinline__ void st_shared_u1(uint32_t a, uint32_t v) {
-    asm volatile("st.shared.b32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
 __device__ __forceinline__ void st_shared_u16(uint32_t a, uint16_t v) {
     asm volatile("st.shared.u16 [%0], %1;" ::"r"(a), "h"(v) : "memory");
@@ -691,16 +694,16 @@ cudaError_t launch_tile(const Mx4GemmArgs &a, int num_sms, cudaStream_t s, bool 
 
 template <bool NV, Result OUT>
 cudaError_t launch_fmt(const Mx4GemmArgs &a, int num_sms, cudaStream_t s, bool pdl) {
-    // The cheaper of the two shapes by their waves: measured over 256..9000 rows, N 768..4096,
-    // K 768..4096 (stages 3, 8, 16), a launch takes about 4.4 us + waves (0.6 + 0.30 stages)
-    // on single 128x128 tiles and 5.6 us + waves (0.7 + 0.44 stages) on pairs' 256x256 tiles
-    // (3000x2304x768: 9.1 against 9.7; 4096x2304x768: 10.3 against 10.0; 2048x4096x4096:
-    // 25.7 against 20.8).
+    // The cheaper of the two shapes by their waves: measured in both formats over 64..9000 rows,
+    // N 768..4096, K 768..4096 (stages 3, 8, 16), a launch takes about 4.4 us + waves (0.36 +
+    // 0.33 stages) on single 128x128 tiles and 5.4 us + waves (1.05 + 0.35 stages) on pairs'
+    // 256x256 tiles (mxfp4: 3000x2304x4096 19.8 against 17.8; 4096x2304x768 9.2 against 10.0,
+    // where the rule is wrong by most, it takes the pairs; 1500x4096x4096 19.2 against 17.7).
     const int stages = mx4_stages(a.K);
     const long long single = (long long)((a.M + 127) / 128) * ((a.N + 127) / 128);
     const long long pair = (long long)((a.M + 255) / 256) * ((a.N + 255) / 256);
     const long long waves1 = (single + num_sms - 1) / num_sms, waves2 = (pair + num_sms / 2 - 1) / (num_sms / 2);
-    if (560 + waves2 * (70 + 44 * stages) < 440 + waves1 * (60 + 30 * stages))
+    if (540 + waves2 * (105 + 35 * stages) < 440 + waves1 * (36 + 33 * stages))
         return launch_tile<NV, true, OUT>(a, num_sms, s, pdl);
     return launch_tile<NV, false, OUT>(a, num_sms, s, pdl);
 }
