@@ -714,6 +714,21 @@ cudaError_t resident_grid(K kernel, std::atomic<int> (&cached)[64], long long ne
     return cudaSuccess;
 }
 
+// One call for both kinds of launch (pdl: as launch_pdl).
+template <typename... KArgs, typename... Args>
+cudaError_t launch(void (*kernel)(KArgs...), int blocks, int warps, cudaStream_t s, bool pdl, Args... args) {
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(32 * warps);
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = pdl ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
+}
+
 inline bool aligned16(const void *p, long long ld, int elem) {
     return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (ld * elem) % 16 == 0;
 }
@@ -732,12 +747,8 @@ cudaError_t quant_launch(const Mx4QuantArgs &a, int vec, cudaStream_t s, bool pd
     auto kernel = mx4_quant_kernel<T, NV, SEGS>;
     cudaError_t e = resident_grid(kernel, cached, (items + kQWarps - 1) / kQWarps, blocks);
     if (e != cudaSuccess) return e;
-    if (pdl)
-        return launch_pdl(kernel, dim3(blocks), dim3(32 * kQWarps), 0, s, static_cast<const T *>(a.x), a.ld, a.rows, a.cols,
-                          a.n_rows, a.tensor_scale, a.codes, a.scales, vec, pairs, a.status, a.trigger);
-    kernel<<<blocks, 32 * kQWarps, 0, s>>>(static_cast<const T *>(a.x), a.ld, a.rows, a.cols, a.n_rows, a.tensor_scale,
-                                           a.codes, a.scales, vec, pairs, a.status, a.trigger);
-    return cudaGetLastError();
+    return launch(kernel, blocks, kQWarps, s, pdl, static_cast<const T *>(a.x), a.ld, a.rows, a.cols, a.n_rows,
+                  a.tensor_scale, a.codes, a.scales, vec, pairs, a.status, a.trigger);
 }
 template <typename T, bool NV>
 cudaError_t quant_typed(const Mx4QuantArgs &a, cudaStream_t s, bool pdl) {
@@ -755,8 +766,7 @@ cudaError_t dequant_launch(const uint8_t *codes, const uint8_t *scales, int rows
     auto kernel = mx4_dequant_kernel<T, NV, SEGS>;
     cudaError_t e = resident_grid(kernel, cached, (items + kQWarps - 1) / kQWarps, blocks);
     if (e != cudaSuccess) return e;
-    kernel<<<blocks, 32 * kQWarps, 0, s>>>(codes, scales, rows, cols, ts, out, ld, vec, pairs);
-    return cudaGetLastError();
+    return launch(kernel, blocks, kQWarps, s, false, codes, scales, rows, cols, ts, out, ld, vec, pairs);
 }
 template <typename T, bool NV>
 cudaError_t dequant_typed(const uint8_t *codes, const uint8_t *scales, int rows, int cols, float ts, void *out,
@@ -780,14 +790,9 @@ cudaError_t norm_launch(K kernel, std::atomic<int> (&cached)[64], int rows_per_c
     if (e != cudaSuccess) return e;
     const int vec = aligned16(a.q.x, a.q.ld, sizeof(T)), vec_y = aligned16(a.y, a.ld_y, sizeof(T));
     const int vec_g = std::min(vec_width(a.gamma, 8, 4), vec_width(a.beta, 8, 4));
-    if (pdl)
-        return launch_pdl(kernel, dim3(blocks), dim3(32 * warps), 0, s, static_cast<const T *>(a.q.x), a.q.ld, a.gamma,
-                          a.beta, a.eps, a.q.rows, a.q.cols, a.q.n_rows, a.q.tensor_scale, static_cast<T *>(a.y),
-                          a.ld_y, a.q.codes, a.q.scales, vec, vec_y, vec_g, a.q.status, a.q.trigger);
-    kernel<<<blocks, 32 * warps, 0, s>>>(static_cast<const T *>(a.q.x), a.q.ld, a.gamma, a.beta, a.eps, a.q.rows,
-                                           a.q.cols, a.q.n_rows, a.q.tensor_scale, static_cast<T *>(a.y), a.ld_y,
-                                           a.q.codes, a.q.scales, vec, vec_y, vec_g, a.q.status, a.q.trigger);
-    return cudaGetLastError();
+    return launch(kernel, blocks, warps, s, pdl, static_cast<const T *>(a.q.x), a.q.ld, a.gamma, a.beta, a.eps, a.q.rows,
+                  a.q.cols, a.q.n_rows, a.q.tensor_scale, static_cast<T *>(a.y), a.ld_y, a.q.codes, a.q.scales, vec, vec_y,
+                  vec_g, a.q.status, a.q.trigger);
 }
 
 template <typename T, bool NV, int W>
