@@ -498,10 +498,16 @@ __device__ __forceinline__ float block_sum(float v, float *red) {
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
-    float s = 0.f;
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-    for (int i = 0; i < W; ++i) s += red[i];
-    return s;
+    for (int i = 0; i < W / 4; ++i) {
+        const float4 r = reinterpret_cast<const float4 *>(red)[i];
+        s.x += r.x;
+        s.y += r.y;
+        s.z += r.z;
+        s.w += r.w;
+    }
+    return (s.x + s.y) + (s.z + s.w);
 }
 
 template <typename T, bool NV, int W, bool PLAIN>
@@ -510,7 +516,7 @@ mx4_norm_cta_kernel(const T *__restrict__ x, long long ld, const float *__restri
                     const float *__restrict__ beta, float eps, int rows, int cols, const int *n_rows, float ts,
                     T *__restrict__ y, long long ld_y, uint8_t *__restrict__ codes,
                     uint8_t *__restrict__ scales, int vec, int vec_y, int vec_g, const int *status, int trigger) {
-    __shared__ float red[2][W];  // one per sum: a row's second barrier separates its first from the next row's
+    __shared__ __align__(16) float red[2][W];  // one per sum: a row's second barrier separates its first from the next row's
     __shared__ uint4 seg4[PLAIN ? 1 : W * kSegWords<T> / 4];
     if (trigger) griddep_launch_dependents();
     griddep_wait();
@@ -521,6 +527,7 @@ mx4_norm_cta_kernel(const T *__restrict__ x, long long ld, const float *__restri
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int chunks = mx4_stages(cols), pitch = mx4_code_pitch(cols);
     const int row_tiles = chunks * Mx4<NV>::kStageTiles;
+    const float inv_cols = 1.0f / (float)cols;  // (a division per sum cost a tenth of a row)
     constexpr int kTileLanes = Mx4<NV>::kTileCols / 8;
     uint32_t *seg = reinterpret_cast<uint32_t *>(seg4) + (PLAIN ? 0 : warp * kSegWords<T>);
     using Raw = std::conditional_t<PLAIN, Raw8<T>, Seg<T>>;
@@ -563,7 +570,7 @@ mx4_norm_cta_kernel(const T *__restrict__ x, long long ld, const float *__restri
             s2 = f2_add(s2, v[i]);
         }
         const float2 sf = f2_split(s2);
-        const float mean = block_sum<W>(sf.x + sf.y, red[0]) / (float)cols;
+        const float mean = block_sum<W>(sf.x + sf.y, red[0]) * inv_cols;
         const uint64_t nmean2 = f2_make(-mean, -mean);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -575,7 +582,7 @@ mx4_norm_cta_kernel(const T *__restrict__ x, long long ld, const float *__restri
             q2 = f2_fma(v[i], v[i], q2);
         }
         const float2 qf = f2_split(q2);
-        const float rstd = rsqrtf(block_sum<W>(n > 0 ? qf.x + qf.y : 0.f, red[1]) / (float)cols + eps);
+        const float rstd = rsqrtf(block_sum<W>(n > 0 ? qf.x + qf.y : 0.f, red[1]) * inv_cols + eps);
         const uint64_t rstd2 = f2_make(rstd, rstd);
         if (warp >= chunks) continue;
         float u[8];
@@ -615,7 +622,7 @@ mx4_norm_wide_kernel(const T *__restrict__ x, long long ld, const float *__restr
                      T *__restrict__ y, long long ld_y, uint8_t *__restrict__ codes,
                      uint8_t *__restrict__ scales, int vec, int vec_y, int vec_g, const int *status, int trigger) {
     constexpr int W = kQWarps, HELD = 4;
-    __shared__ float red[2][W];  // as above
+    __shared__ __align__(16) float red[2][W];  // as above
     if (trigger) griddep_launch_dependents();
     griddep_wait();
     const Mx4Ts tsc = mx4_ts(ts);
