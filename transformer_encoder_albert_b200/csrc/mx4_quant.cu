@@ -484,20 +484,18 @@ mx4_norm_warp_kernel(const T *__restrict__ x, long long ld, const float *__restr
         for (; row < nr; row += stride) one_row(std::false_type{});
 }
 
-// The same with one CTA of W warps per row, for rows of at most 256 W columns: each warp
-// has one of the row's 256-column chunks.  The next row's values load while this one's sums
-// are joined; the parameters stay in registers.  PLAIN: a lane's eight columns all exist or
-// none does, and rows are 16-byte aligned; else rows come and go by words through shared
-// memory.  Over many rows what bounds it is the quantiser's arithmetic and the two barriers
-// a row, which few resident CTAs hide: 8192 rows of 1000, 2048, 4096 bf16 columns take 11,
-// 21 and 44 us with four, eight and sixteen warps (17 for the first with eight; 25, 33 and
-// 58 in the kernel for wider rows).
+// The same with one CTA of W warps per row, for aligned rows of at most 512 W columns, a
+// multiple of 8: a lane has sixteen consecutive columns (per row and warp the sums, the
+// scales and the addresses cost about as much as eight columns' arithmetic), the parameters
+// stay in registers and the next row's values load while this one's sums are joined.  What
+// bounds it over many rows is instructions: FIGURES
 template <int W>
 __device__ __forceinline__ float block_sum(float v, float *red) {
 #pragma unroll
     for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
     __syncthreads();
+    if constexpr (W == 2) return red[0] + red[1];
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int i = 0; i < W / 4; ++i) {
@@ -510,14 +508,145 @@ __device__ __forceinline__ float block_sum(float v, float *red) {
     return (s.x + s.y) + (s.z + s.w);
 }
 
-template <typename T, bool NV, int W, bool PLAIN>
+template <typename T, bool NV, int W>
 __global__ void __launch_bounds__(32 * W)
 mx4_norm_cta_kernel(const T *__restrict__ x, long long ld, const float *__restrict__ gamma,
                     const float *__restrict__ beta, float eps, int rows, int cols, const int *n_rows, float ts,
                     T *__restrict__ y, long long ld_y, uint8_t *__restrict__ codes,
                     uint8_t *__restrict__ scales, int vec, int vec_y, int vec_g, const int *status, int trigger) {
     __shared__ __align__(16) float red[2][W];  // one per sum: a row's second barrier separates its first from the next row's
-    __shared__ uint4 seg4[PLAIN ? 1 : W * kSegWords<T> / 4];
+    if (trigger) griddep_launch_dependents();
+    griddep_wait();
+    const Mx4Ts tsc = mx4_ts(ts);
+    if (status && *reinterpret_cast<const volatile int *>(status) != 0) return;
+    int nr = n_rows ? *reinterpret_cast<const volatile int *>(n_rows) : rows;
+    nr = nr < rows ? nr : rows;
+    const int lane = threadIdx.x & 31;
+    const int chunks = mx4_stages(cols), pitch = mx4_code_pitch(cols);
+    const int row_tiles = chunks * Mx4<NV>::kStageTiles;
+    const float inv_cols = 1.0f / (float)cols;  // (a division per sum cost a twentieth)
+    const int col = threadIdx.x * 16, n = cols - col;  // n: <= 0, 8, or more than 8
+    constexpr int kLanes = NV ? 1 : 2, kTileLanes = 4 * kLanes;  // lanes of a block, of a scale tile
+    uint64_t g[8], b[8];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        float t[8] = {}, u[8] = {};
+        if (n > 8 * h) {
+            ld_cached_v8(gamma + col + 8 * h, t);
+            ld_cached_v8(beta + col + 8 * h, u);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            g[4 * h + i] = f2_make(t[2 * i], t[2 * i + 1]);
+            b[4 * h + i] = f2_make(u[2 * i], u[2 * i + 1]);
+        }
+    }
+    // (no path by values: it would hold up the one warp that has the end of the row, and with it the rest)
+    auto load = [&](int row) {
+        Raw16<T> r = {};
+        const T *src = x + (size_t)row * ld + col;
+        if (row >= nr || n <= 0) return r;
+        if (vec == 2 && n > 8) return load_raw16<T>(src, 16, 2);
+        r.h[0] = load_raw8<T>(src, 8, true);
+        if (n > 8) r.h[1] = load_raw8<T>(src + 8, 8, true);
+        return r;
+    };
+    int row = blockIdx.x;
+    Raw16<T> raw = load(row);
+    for (; row < nr; row += gridDim.x) {
+        uint64_t v[8];
+        uint64_t s2 = f2_make(0.f, 0.f);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float f[8];
+            raw8_values<T>(raw.h[h], f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[4 * h + i] = f2_make(f[2 * i], f[2 * i + 1]);
+                s2 = f2_add(s2, v[4 * h + i]);
+            }
+        }
+        raw = load(row + gridDim.x);
+        const float2 sf = f2_split(s2);
+        const float mean = block_sum<W>(sf.x + sf.y, red[0]) * inv_cols;
+        const uint64_t nmean2 = f2_make(-mean, -mean);
+        float sq = 0.f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint64_t q2 = f2_make(0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[4 * h + i] = f2_add(v[4 * h + i], nmean2);
+                q2 = f2_fma(v[4 * h + i], v[4 * h + i], q2);
+            }
+            const float2 qf = f2_split(q2);
+            sq += n > 8 * h ? qf.x + qf.y : 0.f;
+        }
+        const float rstd = rsqrtf(block_sum<W>(sq, red[1]) * inv_cols + eps);
+        const uint64_t rstd2 = f2_make(rstd, rstd);
+        if (col - lane * 16 >= chunks * kMx4StageCols) continue;  // (the whole warp)
+        float u[16];
+        float m = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float2 w = f2_split(f2_fma(f2_mul(v[i], rstd2), g[i], b[i]));
+            const bool here = n > 8 * (i >> 2);
+            u[2 * i] = here ? w.x : 0.f;
+            u[2 * i + 1] = here ? w.y : 0.f;
+            m = fmax3_abs_nan(m, u[2 * i], u[2 * i + 1]);
+        }
+        if (y && n > 0) {
+            T *dst = y + (size_t)row * ld_y + col;
+            if (vec_y == 2 && n > 8) {
+                if constexpr (sizeof(T) == 4) {
+                    st_global_v8(dst, reinterpret_cast<const uint32_t *>(u));
+                    st_global_v8(dst + 8, reinterpret_cast<const uint32_t *>(u + 8));
+                } else {
+                    uint32_t o[8];
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) o[i] = pack_x2<T>(u[2 * i], u[2 * i + 1]);
+                    st_global_v8(dst, o);
+                }
+            } else {
+                store8<T>(dst, 8, true, *reinterpret_cast<const float (*)[8]>(u));
+                if (n > 8) store8<T>(dst + 8, 8, true, *reinterpret_cast<const float (*)[8]>(u + 8));
+            }
+        }
+        uint32_t bits = abs_bits(m);
+        if constexpr (!NV) bits = umax(bits, __shfl_xor_sync(0xffffffffu, bits, 1));
+        const Mx4Scale s = mx4_block_scale<NV>(bits, tsc);
+        const uint64_t mul2 = f2_make(s.mul, s.mul);
+        uint32_t q[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float z[8];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = f2_split(f2_mul(f2_make(u[8 * h + 2 * i], u[8 * h + 2 * i + 1]), mul2));
+                z[2 * i] = f.x;
+                z[2 * i + 1] = f.y;
+            }
+            q[h] = s.zero ? 0u : cvt_e2m1x8(z);
+        }
+        uint32_t word = s.byte << (8 * ((lane / kLanes) & 3));
+        word |= __shfl_xor_sync(0xffffffffu, word, kLanes);
+        word |= __shfl_xor_sync(0xffffffffu, word, 2 * kLanes);
+        if (col / 2 < pitch) *reinterpret_cast<uint2 *>(codes + (size_t)row * pitch + col / 2) = make_uint2(q[0], q[1]);
+        if (lane % kTileLanes == 0 && col < chunks * kMx4StageCols)
+            *reinterpret_cast<uint32_t *>(scales + scale_word_offset(row, col / Mx4<NV>::kTileCols, row_tiles)) = word;
+    }
+}
+
+// Rows without that alignment, or of a width that is no multiple of 8: words through shared
+// memory, a 256-column chunk per warp, at most 256 W columns.
+template <typename T, bool NV, int W>
+__global__ void __launch_bounds__(32 * W)
+mx4_norm_words_kernel(const T *__restrict__ x, long long ld, const float *__restrict__ gamma,
+                    const float *__restrict__ beta, float eps, int rows, int cols, const int *n_rows, float ts,
+                    T *__restrict__ y, long long ld_y, uint8_t *__restrict__ codes,
+                    uint8_t *__restrict__ scales, int vec, int vec_y, int vec_g, const int *status, int trigger) {
+    __shared__ __align__(16) float red[2][W];  // one per sum: a row's second barrier separates its first from the next row's
+    __shared__ uint4 seg4[W * kSegWords<T> / 4];
     if (trigger) griddep_launch_dependents();
     griddep_wait();
     const Mx4Ts tsc = mx4_ts(ts);
@@ -529,36 +658,22 @@ mx4_norm_cta_kernel(const T *__restrict__ x, long long ld, const float *__restri
     const int row_tiles = chunks * Mx4<NV>::kStageTiles;
     const float inv_cols = 1.0f / (float)cols;  // (a division per sum cost a tenth of a row)
     constexpr int kTileLanes = Mx4<NV>::kTileCols / 8;
-    uint32_t *seg = reinterpret_cast<uint32_t *>(seg4) + (PLAIN ? 0 : warp * kSegWords<T>);
-    using Raw = std::conditional_t<PLAIN, Raw8<T>, Seg<T>>;
+    uint32_t *seg = reinterpret_cast<uint32_t *>(seg4) + warp * kSegWords<T>;
     const int col0 = warp * kMx4StageCols, col = col0 + lane * 8, n = cols - col;
     float g[8] = {}, b[8] = {};
-    if constexpr (PLAIN) {
-        if (n > 0) {
-            ld_cached_v8(gamma + col, g);
-            ld_cached_v8(beta + col, b);
-        }
-    } else {
-        load8<float>(gamma + col, n, vec_g != 0, g);
-        load8<float>(beta + col, n, vec_g != 0, b);
-    }
-    auto load = [&](int row) -> Raw {
-        const T *src = x + (size_t)row * ld + col0;
-        if constexpr (PLAIN) return load_raw8<T>(src + lane * 8, row < nr && n > 0 ? 8 : 0, true);
-        else return seg_load<T>(src, row < nr ? cols - col0 : 0, lane);
+    load8<float>(gamma + col, n, vec_g != 0, g);
+    load8<float>(beta + col, n, vec_g != 0, b);
+    auto load = [&](int row) {
+        return seg_load<T>(x + (size_t)row * ld + col0, row < nr ? cols - col0 : 0, lane);
     };
     int row = blockIdx.x;
-    Raw raw = load(row);
+    Seg<T> raw = load(row);
     for (; row < nr; row += gridDim.x) {
         Raw8<T> r;
-        if constexpr (PLAIN) {
-            r = raw;
-        } else {
-            __syncwarp();
-            seg_stage<T>(seg, raw, lane);
-            __syncwarp();
-            seg_read<T>(seg, seg_shift(x + (size_t)row * ld), lane * 8, r.w);
-        }
+        __syncwarp();
+        seg_stage<T>(seg, raw, lane);
+        __syncwarp();
+        seg_read<T>(seg, seg_shift(x + (size_t)row * ld), lane * 8, r.w);
         raw = load(row + gridDim.x);
         float f[8];
         raw8_values<T>(r, f);
@@ -575,14 +690,12 @@ mx4_norm_cta_kernel(const T *__restrict__ x, long long ld, const float *__restri
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             v[i] = f2_add(v[i], nmean2);
-            if constexpr (!PLAIN) {
-                const float2 d = f2_split(v[i]);
-                v[i] = f2_make(2 * i < n ? d.x : 0.f, 2 * i + 1 < n ? d.y : 0.f);
-            }
+            const float2 d = f2_split(v[i]);
+            v[i] = f2_make(2 * i < n ? d.x : 0.f, 2 * i + 1 < n ? d.y : 0.f);
             q2 = f2_fma(v[i], v[i], q2);
         }
         const float2 qf = f2_split(q2);
-        const float rstd = rsqrtf(block_sum<W>(n > 0 ? qf.x + qf.y : 0.f, red[1]) * inv_cols + eps);
+        const float rstd = rsqrtf(block_sum<W>(qf.x + qf.y, red[1]) * inv_cols + eps);
         const uint64_t rstd2 = f2_make(rstd, rstd);
         if (warp >= chunks) continue;
         float u[8];
@@ -590,15 +703,13 @@ mx4_norm_cta_kernel(const T *__restrict__ x, long long ld, const float *__restri
         for (int i = 0; i < 4; ++i) {
             const float2 w = f2_split(f2_fma(f2_mul(v[i], rstd2), f2_make(g[2 * i], g[2 * i + 1]),
                                              f2_make(b[2 * i], b[2 * i + 1])));
-            u[2 * i] = (PLAIN ? n > 0 : 2 * i < n) ? w.x : 0.f;
-            u[2 * i + 1] = (PLAIN ? n > 0 : 2 * i + 1 < n) ? w.y : 0.f;
+            u[2 * i] = 2 * i < n ? w.x : 0.f;
+            u[2 * i + 1] = 2 * i + 1 < n ? w.y : 0.f;
         }
         float m = fmax3_abs_nan(u[0], u[1], u[2]);
         m = fmax3_abs_nan(m, u[3], u[4]);
         m = fmax3_abs_nan(m, u[5], fmax3_abs_nan(u[6], u[7], 0.f));
-        if constexpr (PLAIN) {
-            if (y && n > 0) store8<T>(y + (size_t)row * ld_y + col, 8, true, u);
-        } else if (y) {  // (the staged row has been read: two barriers ago)
+        if (y) {  // (the staged row has been read: two barriers ago)
             store8<T>(reinterpret_cast<T *>(seg) + lane * 8, 8, true, u);
             __syncwarp();
             seg_store<T>(y + (size_t)row * ld_y + col0, cols - col0, seg, lane);
@@ -795,7 +906,7 @@ cudaError_t norm_launch(K kernel, std::atomic<int> (&cached)[64], int rows_per_c
     int blocks = 0;
     cudaError_t e = resident_grid(kernel, cached, (a.q.rows + rows_per_cta - 1) / rows_per_cta, blocks, warps);
     if (e != cudaSuccess) return e;
-    const int vec = aligned16(a.q.x, a.q.ld, sizeof(T)), vec_y = aligned16(a.y, a.ld_y, sizeof(T));
+    const int vec = vec_width(a.q.x, a.q.ld, sizeof(T)), vec_y = vec_width(a.y, a.ld_y, sizeof(T));
     const int vec_g = std::min(vec_width(a.gamma, 8, 4), vec_width(a.beta, 8, 4));
     return launch(kernel, blocks, warps, s, pdl, static_cast<const T *>(a.q.x), a.q.ld, a.gamma, a.beta, a.eps, a.q.rows,
                   a.q.cols, a.q.n_rows, a.q.tensor_scale, static_cast<T *>(a.y), a.ld_y, a.q.codes, a.q.scales, vec, vec_y,
@@ -804,10 +915,13 @@ cudaError_t norm_launch(K kernel, std::atomic<int> (&cached)[64], int rows_per_c
 
 template <typename T, bool NV, int W>
 cudaError_t norm_rows(const Mx4NormArgs &a, cudaStream_t s, bool pdl) {
-    static std::atomic<int> plain[64], other[64];
-    if (a.q.cols % 8 == 0 && norm_aligned<T>(a) && vec_width(a.gamma, 8, 4) == 2 && vec_width(a.beta, 8, 4) == 2)
-        return norm_launch<T, NV>(mx4_norm_cta_kernel<T, NV, W, true>, plain, 1, W, a, s, pdl);
-    return norm_launch<T, NV>(mx4_norm_cta_kernel<T, NV, W, false>, other, 1, W, a, s, pdl);
+    static std::atomic<int> cached[64];
+    return norm_launch<T, NV>(mx4_norm_cta_kernel<T, NV, W>, cached, 1, W, a, s, pdl);
+}
+template <typename T, bool NV, int W>
+cudaError_t norm_words(const Mx4NormArgs &a, cudaStream_t s, bool pdl) {
+    static std::atomic<int> cached[64];
+    return norm_launch<T, NV>(mx4_norm_words_kernel<T, NV, W>, cached, 1, W, a, s, pdl);
 }
 
 template <typename T, bool NV>
@@ -820,9 +934,16 @@ cudaError_t norm_typed(const Mx4NormArgs &a, cudaStream_t s, bool pdl) {
     if (a.q.cols <= 256) return norm_launch<T, NV>(mx4_norm_warp_kernel<T, NV, 1>, c1, kQWarps, kQWarps, a, s, pdl);
     if (a.q.cols <= 768 && a.q.rows >= 512 && norm_aligned<T>(a))
         return norm_launch<T, NV>(mx4_norm_warp_kernel<T, NV, 3>, c3, kQWarps, kQWarps, a, s, pdl);
-    if (a.q.cols <= 1024) return norm_rows<T, NV, 4>(a, s, pdl);
-    if (a.q.cols <= 2048) return norm_rows<T, NV, 8>(a, s, pdl);
-    if (a.q.cols <= 4096) return norm_rows<T, NV, 16>(a, s, pdl);
+    if (a.q.cols % 8 == 0 && norm_aligned<T>(a) && vec_width(a.gamma, 8, 4) == 2 && vec_width(a.beta, 8, 4) == 2) {
+        if (a.q.cols <= 1024) return norm_rows<T, NV, 2>(a, s, pdl);
+        if (a.q.cols <= 2048) return norm_rows<T, NV, 4>(a, s, pdl);
+        if (a.q.cols <= 4096) return norm_rows<T, NV, 8>(a, s, pdl);
+        if (a.q.cols <= 8192) return norm_rows<T, NV, 16>(a, s, pdl);
+    } else {
+        if (a.q.cols <= 1024) return norm_words<T, NV, 4>(a, s, pdl);
+        if (a.q.cols <= 2048) return norm_words<T, NV, 8>(a, s, pdl);
+        if (a.q.cols <= 4096) return norm_words<T, NV, 16>(a, s, pdl);
+    }
     return norm_launch<T, NV>(mx4_norm_wide_kernel<T, NV>, wide, 1, kQWarps, a, s, pdl);
 }
 
