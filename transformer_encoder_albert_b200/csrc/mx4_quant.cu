@@ -94,12 +94,13 @@ __device__ __forceinline__ Raw16<T> load_raw16(const T *p, int n, int vec) {
 // Rows that are aligned to their type only (an odd row stride): a warp moves 256 columns of
 // one row in consecutive 4-byte words, aligned down for 16-bit types, and hands them over
 // through shared memory -- one value per access cost a lane 16 loads or stores 32 bytes
-// apart (8192 x 1001 bf16: quantised in 11.9 us, 8.7 now; read back in 54, 7.1 now).
+// apart (8192 x 1001 bf16: quantised in 11.9 us, 9.3 now; read back in 54, 7.1 now).
 template <typename T>
 constexpr int kSegWords = sizeof(T) == 4 ? 256 : 132;  // (16-bit: 129, up to a multiple of 16 bytes)
 template <typename T>
-struct Seg {
-    uint32_t w[sizeof(T) == 4 ? 8 : 5];
+struct Seg {  // as loaded: nothing waits for the values before they are staged
+    uint32_t w[sizeof(T) == 4 ? 8 : 4];
+    unsigned short edge;  // (16-bit) lane 0: the first value if its word starts before the row; lane 1: a last one alone in its word
 };
 // 1 if a 16-bit row starts in the upper half of a 4-byte word.
 template <typename T>
@@ -109,34 +110,39 @@ __device__ __forceinline__ int seg_shift(const T *p) {
 // The first n (at most 256) values at src; the others are 0.
 template <typename T>
 __device__ __forceinline__ Seg<T> seg_load(const T *src, int n, int lane) {
-    Seg<T> r;
+    Seg<T> r = {};
     if constexpr (sizeof(T) == 4) {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            r.w[i] = lane + 32 * i < n ? __ldg(reinterpret_cast<const uint32_t *>(src) + lane + 32 * i) : 0u;
+            if (lane + 32 * i < n) r.w[i] = __ldg(reinterpret_cast<const uint32_t *>(src) + lane + 32 * i);
     } else {
         n = n < kMx4StageCols ? n : kMx4StageCols;
         const int s = seg_shift(src);
-        const uint32_t *words = reinterpret_cast<const uint32_t *>(src - s);
+        const uint32_t *words = reinterpret_cast<const uint32_t *>(src - s);  // word o: values 2 o - s, 2 o - s + 1
         const unsigned short *halves = reinterpret_cast<const unsigned short *>(src);
 #pragma unroll
-        for (int i = 0; i < 5; ++i) {
-            const int o = lane + 32 * i, lo = 2 * o - s, hi = lo + 1;  // word o holds values lo and hi
-            if (lo >= 0 && hi < n) {
-                r.w[i] = __ldg(words + o);
-            } else {
-                const uint32_t a = lo >= 0 && lo < n ? __ldg(halves + lo) : 0u, b = hi < n ? __ldg(halves + hi) : 0u;
-                r.w[i] = a | b << 16;
-            }
+        for (int i = 0; i < 4; ++i) {
+            const int o = lane + 32 * i;
+            if (2 * o >= s && 2 * o - s + 1 < n) r.w[i] = __ldg(words + o);
         }
+        const int alone = lane == 0 ? (s ? 0 : -1) : lane == 1 && (n - 1 + s) % 2 == 0 ? n - 1 : -1;
+        if (alone >= 0 && alone < n) r.edge = __ldg(halves + alone);
     }
     return r;
 }
+// To shared memory, word by word (s, n: as loaded).
 template <typename T>
-__device__ __forceinline__ void seg_stage(uint32_t *sw, const Seg<T> &r, int lane) {
+__device__ __forceinline__ void seg_stage(uint32_t *sw, const Seg<T> &r, int s, int n, int lane) {
 #pragma unroll
     for (int i = 0; i < (sizeof(T) == 4 ? 8 : 4); ++i) sw[lane + 32 * i] = r.w[i];
-    if (sizeof(T) == 2 && lane == 0) sw[128] = r.w[4];
+    if constexpr (sizeof(T) == 2) {
+        n = n < kMx4StageCols ? n : kMx4StageCols;
+        if (lane == 0) sw[128] = 0;
+        __syncwarp();
+        unsigned short *halves = reinterpret_cast<unsigned short *>(sw);
+        if (lane == 0 && s && n > 0) halves[1] = r.edge;
+        if (lane == 1 && n > 0 && (n - 1 + s) % 2 == 0) halves[n - 1 + s] = r.edge;
+    }
 }
 // NW words of values from value `first` (even) on, of a staged row with shift s.
 template <typename T, int NW>
@@ -228,8 +234,12 @@ mx4_quant_kernel(const T *__restrict__ x, long long ld, int rows, int cols, cons
         if constexpr (SEGS) {
             constexpr int kHalf = 2 * sizeof(T);  // words of eight values
             __syncwarp();
-            seg_stage<T>(seg, raw.h[0], lane);
-            seg_stage<T>(seg + kSegWords<T>, raw.h[1], lane);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int y = row0 + 32 * h;
+                seg_stage<T>(seg + h * kSegWords<T>, raw.h[h], seg_shift(x + (size_t)y * ld),
+                             y < nr ? cols - chunk * kMx4StageCols : 0, lane);
+            }
             __syncwarp();
             uint32_t t[2 * kHalf];
             seg_read<T>(seg + lower * kSegWords<T>, seg_shift(x + (size_t)row * ld), sub * 16, t);
@@ -484,11 +494,14 @@ mx4_norm_warp_kernel(const T *__restrict__ x, long long ld, const float *__restr
         for (; row < nr; row += stride) one_row(std::false_type{});
 }
 
-// The same with one CTA of W warps per row, for aligned rows of at most 512 W columns, a
-// multiple of 8: a lane has sixteen consecutive columns (per row and warp the sums, the
-// scales and the addresses cost about as much as eight columns' arithmetic), the parameters
-// stay in registers and the next row's values load while this one's sums are joined.  What
-// bounds it over many rows is instructions: FIGURES
+// The same with one CTA of W warps per row, for rows of at most 512 W columns: a lane has
+// sixteen consecutive columns (per row and warp the sums, the scales and the addresses cost
+// about as much as eight columns' arithmetic), the parameters stay in registers and the
+// next row's values load while this one's sums are joined.  WORDS: rows that are not
+// 16-byte aligned, or of a width that is no multiple of 8, come and go by words.  What
+// bounds it over many rows is instructions: 8192 rows of 1000, 2048, 4096 bf16 columns take
+// 9.2, 16.7 and 33.5 us (eight columns a lane: 10.7, 20.9, 43; in the kernel for wider rows
+// 25, 33, 58), of 1001 by words 16.4 (by values, in that kernel, 30).
 template <int W>
 __device__ __forceinline__ float block_sum(float v, float *red) {
 #pragma unroll
@@ -508,13 +521,15 @@ __device__ __forceinline__ float block_sum(float v, float *red) {
     return (s.x + s.y) + (s.z + s.w);
 }
 
-template <typename T, bool NV, int W>
+template <typename T, bool NV, int W, bool WORDS>
 __global__ void __launch_bounds__(32 * W)
 mx4_norm_cta_kernel(const T *__restrict__ x, long long ld, const float *__restrict__ gamma,
                     const float *__restrict__ beta, float eps, int rows, int cols, const int *n_rows, float ts,
                     T *__restrict__ y, long long ld_y, uint8_t *__restrict__ codes,
                     uint8_t *__restrict__ scales, int vec, int vec_y, int vec_g, const int *status, int trigger) {
     __shared__ __align__(16) float red[2][W];  // one per sum: a row's second barrier separates its first from the next row's
+    __shared__ uint4 seg4[WORDS ? W * 2 * kSegWords<T> / 4 : 1];
+    uint32_t *seg = reinterpret_cast<uint32_t *>(seg4) + (WORDS ? (threadIdx.x >> 5) * 2 * kSegWords<T> : 0);
     if (trigger) griddep_launch_dependents();
     griddep_wait();
     const Mx4Ts tsc = mx4_ts(ts);
@@ -525,13 +540,17 @@ mx4_norm_cta_kernel(const T *__restrict__ x, long long ld, const float *__restri
     const int chunks = mx4_stages(cols), pitch = mx4_code_pitch(cols);
     const int row_tiles = chunks * Mx4<NV>::kStageTiles;
     const float inv_cols = 1.0f / (float)cols;  // (a division per sum cost a twentieth)
-    const int col = threadIdx.x * 16, n = cols - col;  // n: <= 0, 8, or more than 8
+    const int col = threadIdx.x * 16, n = cols - col;  // aligned rows: n is 0 or less, 8, or more
+    const int col0 = (threadIdx.x >> 5) * 512;
     constexpr int kLanes = NV ? 1 : 2, kTileLanes = 4 * kLanes;  // lanes of a block, of a scale tile
     uint64_t g[8], b[8];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
         float t[8] = {}, u[8] = {};
-        if (n > 8 * h) {
+        if constexpr (WORDS) {
+            load8<float>(gamma + col + 8 * h, n - 8 * h, vec_g != 0, t);
+            load8<float>(beta + col + 8 * h, n - 8 * h, vec_g != 0, u);
+        } else if (n > 8 * h) {
             ld_cached_v8(gamma + col + 8 * h, t);
             ld_cached_v8(beta + col + 8 * h, u);
         }
@@ -541,25 +560,53 @@ mx4_norm_cta_kernel(const T *__restrict__ x, long long ld, const float *__restri
             b[4 * h + i] = f2_make(u[2 * i], u[2 * i + 1]);
         }
     }
-    // (no path by values: it would hold up the one warp that has the end of the row, and with it the rest)
-    auto load = [&](int row) {
-        Raw16<T> r = {};
-        const T *src = x + (size_t)row * ld + col;
-        if (row >= nr || n <= 0) return r;
-        if (vec == 2 && n > 8) return load_raw16<T>(src, 16, 2);
-        r.h[0] = load_raw8<T>(src, 8, true);
-        if (n > 8) r.h[1] = load_raw8<T>(src + 8, 8, true);
-        return r;
+    struct Segs {
+        Seg<T> h[2];
+    };
+    using Raw = std::conditional_t<WORDS, Segs, Raw16<T>>;
+    auto load = [&](int row) -> Raw {
+        Raw r = {};
+        if constexpr (WORDS) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                r.h[h] = seg_load<T>(x + (size_t)row * ld + col0 + 256 * h, row < nr ? cols - col0 - 256 * h : 0, lane);
+            return r;
+        } else {  // (no path by values: it would hold up the one warp that has the row's end, and with it the rest)
+            const T *src = x + (size_t)row * ld + col;
+            if (row >= nr || n <= 0) return r;
+            if (vec == 2 && n > 8) return load_raw16<T>(src, 16, 2);
+            r.h[0] = load_raw8<T>(src, 8, true);
+            if (n > 8) r.h[1] = load_raw8<T>(src + 8, 8, true);
+            return r;
+        }
     };
     int row = blockIdx.x;
-    Raw16<T> raw = load(row);
+    Raw raw = load(row);
     for (; row < nr; row += gridDim.x) {
+        Raw16<T> own;
+        if constexpr (WORDS) {
+            constexpr int kHalf = 2 * sizeof(T);  // words of eight values
+            uint32_t w[2 * kHalf];
+            __syncwarp();
+            const int shift = seg_shift(x + (size_t)row * ld);
+            seg_stage<T>(seg, raw.h[0], shift, cols - col0, lane);
+            seg_stage<T>(seg + kSegWords<T>, raw.h[1], shift, cols - col0 - 256, lane);
+            __syncwarp();
+            seg_read<T>(seg + (lane >> 4) * kSegWords<T>, shift, (lane & 15) * 16, w);
+#pragma unroll
+            for (int i = 0; i < kHalf; ++i) {
+                own.h[0].w[i] = w[i];
+                own.h[1].w[i] = w[kHalf + i];
+            }
+        } else {
+            own = raw;
+        }
         uint64_t v[8];
         uint64_t s2 = f2_make(0.f, 0.f);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             float f[8];
-            raw8_values<T>(raw.h[h], f);
+            raw8_values<T>(own.h[h], f);
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 v[4 * h + i] = f2_make(f[2 * i], f[2 * i + 1]);
@@ -577,25 +624,36 @@ mx4_norm_cta_kernel(const T *__restrict__ x, long long ld, const float *__restri
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 v[4 * h + i] = f2_add(v[4 * h + i], nmean2);
+                if constexpr (WORDS) {
+                    const float2 d = f2_split(v[4 * h + i]);
+                    v[4 * h + i] = f2_make(8 * h + 2 * i < n ? d.x : 0.f, 8 * h + 2 * i + 1 < n ? d.y : 0.f);
+                }
                 q2 = f2_fma(v[4 * h + i], v[4 * h + i], q2);
             }
             const float2 qf = f2_split(q2);
-            sq += n > 8 * h ? qf.x + qf.y : 0.f;
+            sq += WORDS || n > 8 * h ? qf.x + qf.y : 0.f;
         }
         const float rstd = rsqrtf(block_sum<W>(sq, red[1]) * inv_cols + eps);
         const uint64_t rstd2 = f2_make(rstd, rstd);
-        if (col - lane * 16 >= chunks * kMx4StageCols) continue;  // (the whole warp)
+        if (col0 >= cols) continue;  // (the whole warp)
         float u[16];
         float m = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float2 w = f2_split(f2_fma(f2_mul(v[i], rstd2), g[i], b[i]));
-            const bool here = n > 8 * (i >> 2);
-            u[2 * i] = here ? w.x : 0.f;
-            u[2 * i + 1] = here ? w.y : 0.f;
+            u[2 * i] = n > (WORDS ? 2 * i : 8 * (i >> 2)) ? w.x : 0.f;
+            u[2 * i + 1] = n > (WORDS ? 2 * i + 1 : 8 * (i >> 2)) ? w.y : 0.f;
             m = fmax3_abs_nan(m, u[2 * i], u[2 * i + 1]);
         }
-        if (y && n > 0) {
+        if (WORDS && y) {  // (the staged row has been read: two barriers ago)
+            T *mine = reinterpret_cast<T *>(seg + (lane >> 4) * kSegWords<T>) + (lane & 15) * 16;
+            store8<T>(mine, 8, true, *reinterpret_cast<const float (*)[8]>(u));
+            store8<T>(mine + 8, 8, true, *reinterpret_cast<const float (*)[8]>(u + 8));
+            __syncwarp();
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                seg_store<T>(y + (size_t)row * ld_y + col0 + 256 * h, cols - col0 - 256 * h, seg + h * kSegWords<T>, lane);
+        } else if (y && n > 0) {
             T *dst = y + (size_t)row * ld_y + col;
             if (vec_y == 2 && n > 8) {
                 if constexpr (sizeof(T) == 4) {
@@ -637,95 +695,9 @@ mx4_norm_cta_kernel(const T *__restrict__ x, long long ld, const float *__restri
     }
 }
 
-// Rows without that alignment, or of a width that is no multiple of 8: words through shared
-// memory, a 256-column chunk per warp, at most 256 W columns.
-template <typename T, bool NV, int W>
-__global__ void __launch_bounds__(32 * W)
-mx4_norm_words_kernel(const T *__restrict__ x, long long ld, const float *__restrict__ gamma,
-                    const float *__restrict__ beta, float eps, int rows, int cols, const int *n_rows, float ts,
-                    T *__restrict__ y, long long ld_y, uint8_t *__restrict__ codes,
-                    uint8_t *__restrict__ scales, int vec, int vec_y, int vec_g, const int *status, int trigger) {
-    __shared__ __align__(16) float red[2][W];  // one per sum: a row's second barrier separates its first from the next row's
-    __shared__ uint4 seg4[W * kSegWords<T> / 4];
-    if (trigger) griddep_launch_dependents();
-    griddep_wait();
-    const Mx4Ts tsc = mx4_ts(ts);
-    if (status && *reinterpret_cast<const volatile int *>(status) != 0) return;
-    int nr = n_rows ? *reinterpret_cast<const volatile int *>(n_rows) : rows;
-    nr = nr < rows ? nr : rows;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int chunks = mx4_stages(cols), pitch = mx4_code_pitch(cols);
-    const int row_tiles = chunks * Mx4<NV>::kStageTiles;
-    const float inv_cols = 1.0f / (float)cols;  // (a division per sum cost a tenth of a row)
-    constexpr int kTileLanes = Mx4<NV>::kTileCols / 8;
-    uint32_t *seg = reinterpret_cast<uint32_t *>(seg4) + warp * kSegWords<T>;
-    const int col0 = warp * kMx4StageCols, col = col0 + lane * 8, n = cols - col;
-    float g[8] = {}, b[8] = {};
-    load8<float>(gamma + col, n, vec_g != 0, g);
-    load8<float>(beta + col, n, vec_g != 0, b);
-    auto load = [&](int row) {
-        return seg_load<T>(x + (size_t)row * ld + col0, row < nr ? cols - col0 : 0, lane);
-    };
-    int row = blockIdx.x;
-    Seg<T> raw = load(row);
-    for (; row < nr; row += gridDim.x) {
-        Raw8<T> r;
-        __syncwarp();
-        seg_stage<T>(seg, raw, lane);
-        __syncwarp();
-        seg_read<T>(seg, seg_shift(x + (size_t)row * ld), lane * 8, r.w);
-        raw = load(row + gridDim.x);
-        float f[8];
-        raw8_values<T>(r, f);
-        uint64_t v[4];
-        uint64_t s2 = f2_make(0.f, 0.f), q2 = s2;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[i] = f2_make(f[2 * i], f[2 * i + 1]);
-            s2 = f2_add(s2, v[i]);
-        }
-        const float2 sf = f2_split(s2);
-        const float mean = block_sum<W>(sf.x + sf.y, red[0]) * inv_cols;
-        const uint64_t nmean2 = f2_make(-mean, -mean);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[i] = f2_add(v[i], nmean2);
-            const float2 d = f2_split(v[i]);
-            v[i] = f2_make(2 * i < n ? d.x : 0.f, 2 * i + 1 < n ? d.y : 0.f);
-            q2 = f2_fma(v[i], v[i], q2);
-        }
-        const float2 qf = f2_split(q2);
-        const float rstd = rsqrtf(block_sum<W>(qf.x + qf.y, red[1]) * inv_cols + eps);
-        const uint64_t rstd2 = f2_make(rstd, rstd);
-        if (warp >= chunks) continue;
-        float u[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 w = f2_split(f2_fma(f2_mul(v[i], rstd2), f2_make(g[2 * i], g[2 * i + 1]),
-                                             f2_make(b[2 * i], b[2 * i + 1])));
-            u[2 * i] = 2 * i < n ? w.x : 0.f;
-            u[2 * i + 1] = 2 * i + 1 < n ? w.y : 0.f;
-        }
-        float m = fmax3_abs_nan(u[0], u[1], u[2]);
-        m = fmax3_abs_nan(m, u[3], u[4]);
-        m = fmax3_abs_nan(m, u[5], fmax3_abs_nan(u[6], u[7], 0.f));
-        if (y) {  // (the staged row has been read: two barriers ago)
-            store8<T>(reinterpret_cast<T *>(seg) + lane * 8, 8, true, u);
-            __syncwarp();
-            seg_store<T>(y + (size_t)row * ld_y + col0, cols - col0, seg, lane);
-        }
-        uint32_t word;
-        const uint32_t q = mx4_warp_quant<NV>(u, abs_bits(m), tsc, lane, word);
-        if (col / 2 < pitch) *reinterpret_cast<uint32_t *>(codes + (size_t)row * pitch + col / 2) = q;
-        if (lane % kTileLanes == 0)
-            *reinterpret_cast<uint32_t *>(scales + scale_word_offset(row, warp * Mx4<NV>::kStageTiles + lane / kTileLanes,
-                                                                     row_tiles)) = word;
-    }
-}
-
 // Wider rows: one CTA per row, each warp holds four of the row's chunks (every eighth);
-// chunks beyond those are read again in each pass (from L1 or L2).  4096 rows of 8192 bf16
-// columns take 47 us; one chunk per warp and 32 warps 53.
+// chunks beyond those are read again in each pass (from L1 or L2).  2000 rows of 8200 bf16
+// columns take 27 us.
 template <typename T, bool NV>
 __global__ void __launch_bounds__(32 * kQWarps)
 mx4_norm_wide_kernel(const T *__restrict__ x, long long ld, const float *__restrict__ gamma,
@@ -913,37 +885,31 @@ cudaError_t norm_launch(K kernel, std::atomic<int> (&cached)[64], int rows_per_c
                   vec_g, a.q.status, a.q.trigger);
 }
 
-template <typename T, bool NV, int W>
+template <typename T, bool NV, int W, bool WORDS>
 cudaError_t norm_rows(const Mx4NormArgs &a, cudaStream_t s, bool pdl) {
     static std::atomic<int> cached[64];
-    return norm_launch<T, NV>(mx4_norm_cta_kernel<T, NV, W>, cached, 1, W, a, s, pdl);
+    return norm_launch<T, NV>(mx4_norm_cta_kernel<T, NV, W, WORDS>, cached, 1, W, a, s, pdl);
 }
 template <typename T, bool NV, int W>
-cudaError_t norm_words(const Mx4NormArgs &a, cudaStream_t s, bool pdl) {
-    static std::atomic<int> cached[64];
-    return norm_launch<T, NV>(mx4_norm_words_kernel<T, NV, W>, cached, 1, W, a, s, pdl);
+cudaError_t norm_width(const Mx4NormArgs &a, cudaStream_t s, bool pdl) {
+    const bool words = a.q.cols % 8 || !norm_aligned<T>(a) || vec_width(a.gamma, 8, 4) != 2 || vec_width(a.beta, 8, 4) != 2;
+    return words ? norm_rows<T, NV, W, true>(a, s, pdl) : norm_rows<T, NV, W, false>(a, s, pdl);
 }
 
 template <typename T, bool NV>
 cudaError_t norm_typed(const Mx4NormArgs &a, cudaStream_t s, bool pdl) {
     // A warp per row once the rows fill the machine's warps several times over; a CTA per
     // row for few rows (5 rows of 1000: 4.4 us against 7.9), for rows a warp cannot hold
-    // in half its registers, and for rows without alignment (8192 x 767: 16.6 us against
+    // in half its registers, and for rows without alignment (8192 x 767: 15.9 us against
     // 21); both sides of the other widths at the kernel above.
     static std::atomic<int> c1[64], c3[64], wide[64];
     if (a.q.cols <= 256) return norm_launch<T, NV>(mx4_norm_warp_kernel<T, NV, 1>, c1, kQWarps, kQWarps, a, s, pdl);
     if (a.q.cols <= 768 && a.q.rows >= 512 && norm_aligned<T>(a))
         return norm_launch<T, NV>(mx4_norm_warp_kernel<T, NV, 3>, c3, kQWarps, kQWarps, a, s, pdl);
-    if (a.q.cols % 8 == 0 && norm_aligned<T>(a) && vec_width(a.gamma, 8, 4) == 2 && vec_width(a.beta, 8, 4) == 2) {
-        if (a.q.cols <= 1024) return norm_rows<T, NV, 2>(a, s, pdl);
-        if (a.q.cols <= 2048) return norm_rows<T, NV, 4>(a, s, pdl);
-        if (a.q.cols <= 4096) return norm_rows<T, NV, 8>(a, s, pdl);
-        if (a.q.cols <= 8192) return norm_rows<T, NV, 16>(a, s, pdl);
-    } else {
-        if (a.q.cols <= 1024) return norm_words<T, NV, 4>(a, s, pdl);
-        if (a.q.cols <= 2048) return norm_words<T, NV, 8>(a, s, pdl);
-        if (a.q.cols <= 4096) return norm_words<T, NV, 16>(a, s, pdl);
-    }
+    if (a.q.cols <= 1024) return norm_width<T, NV, 2>(a, s, pdl);
+    if (a.q.cols <= 2048) return norm_width<T, NV, 4>(a, s, pdl);
+    if (a.q.cols <= 4096) return norm_width<T, NV, 8>(a, s, pdl);
+    if (a.q.cols <= 8192) return norm_width<T, NV, 16>(a, s, pdl);
     return norm_launch<T, NV>(mx4_norm_wide_kernel<T, NV>, wide, 1, kQWarps, a, s, pdl);
 }
 
