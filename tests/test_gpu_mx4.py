@@ -183,7 +183,8 @@ def test_rows_at_any_offset_of_a_wider_buffer(cols, width, offset, dtype):
 @pytest.mark.parametrize("dtype", list(DTYPES))
 @pytest.mark.parametrize("rows,cols,pad", [(1, 768, 0), (1, 1, 0), (7, 40, 5), (133, 768, 0), (20, 1001, 0), (6, 2304, 8),
                                             (3, 9000, 0), (700, 768, 0), (700, 520, 8), (2500, 2048, 0), (40, 1000, 0),
-                                            (40, 1000, 8), (700, 2600, 0), (320, 8000, 0), (9, 4001, 0)])
+                                            (40, 1000, 8), (700, 2600, 0), (320, 8000, 0), (9, 4001, 0), (600, 1477, 0),
+                                            (5, 5001, 1)])
 def test_layer_norm_rows_and_their_4_bit_form(rows, cols, pad, dtype, fmt):
     rng = np.random.default_rng(rows + cols)
     x, t = _rows(rng, rows, cols + pad, dtype, 3.0)
