@@ -381,9 +381,29 @@ mx4_dequant_kernel(const uint8_t *__restrict__ codes, const uint8_t *__restrict_
 }
 
 // LayerNorm, one warp per row of at most 256 NCH columns: the row stays in registers
-// (one read), both sums by shuffles, the next row's loads in flight meanwhile.  fp32
-// statistics in two passes (mean, then the squares of the differences); the 4-bit
-// form is taken of the fp32 result, y is its rounding to x's type.
+// (one read), the sums by shuffles, the next row's loads in flight meanwhile.  fp32
+// statistics in two passes; the 4-bit form is taken of the fp32 result, y is its rounding to
+// x's type.  The first pass's mean m0 carries the rounding of its sum, which outweighs the
+// row's own spread where that is small beside the mean (rows of one value: y was off by up
+// to 1).  So the second pass sums the differences d = x - m0 beside their squares:
+//   e = sum(d) / n, variance = sum(d^2) / n - e^2, y = (d - e) rstd gamma + beta,
+// which holds for any m0 near the mean.  It costs an addition per pair and its shuffles
+// (12301 x 768 bf16 in mxfp4: 9.1 us, 8.6 without).
+// The warp's sum of a in lanes 0..15, of b in lanes 16..31: six shuffles for two sums' ten.
+__device__ __forceinline__ float warp_sums(float a, float b, int lane) {
+    const bool upper = lane & 16;
+    float s = (upper ? b : a) + __shfl_xor_sync(0xffffffffu, upper ? a : b, 16);
+#pragma unroll
+    for (int o = 8; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s;
+}
+// From the means of d^2 and of d: rstd, and -e rstd.  (A variance below 0 is rounding; NaN stays.)
+__device__ __forceinline__ float2 norm_factors(float mean_sq, float e, float eps) {
+    const float var = fmaf(-e, e, mean_sq);
+    const float rstd = rsqrtf((var < 0.f ? 0.f : var) + eps);
+    return make_float2(rstd, -e * rstd);
+}
+
 template <typename T, bool NV, int NCH>
 __global__ void __launch_bounds__(32 * kQWarps)
 mx4_norm_warp_kernel(const T *__restrict__ x, long long ld, const float *__restrict__ gamma,
@@ -430,7 +450,7 @@ mx4_norm_warp_kernel(const T *__restrict__ x, long long ld, const float *__restr
         for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         const float mean = sum / (float)cols;
         const uint64_t nmean2 = f2_make(-mean, -mean);
-        uint64_t q2 = f2_make(0.f, 0.f);
+        uint64_t q2 = f2_make(0.f, 0.f), e2 = q2;
 #pragma unroll
         for (int c = 0; c < NCH; ++c) {
             const int n = cols - c * kMx4StageCols - lane * 8;
@@ -442,14 +462,14 @@ mx4_norm_warp_kernel(const T *__restrict__ x, long long ld, const float *__restr
                     v[c][i] = f2_make(2 * i < n ? d.x : 0.f, 2 * i + 1 < n ? d.y : 0.f);
                 }
                 q2 = f2_fma(v[c][i], v[c][i], q2);
+                e2 = f2_add(e2, v[c][i]);
             }
         }
-        const float2 qf = f2_split(q2);
-        float sq = qf.x + qf.y;
-#pragma unroll
-        for (int o = 16; o; o >>= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
-        const float rstd = rsqrtf(sq / (float)cols + eps);
-        const uint64_t rstd2 = f2_make(rstd, rstd);
+        const float2 qf = f2_split(q2), ef = f2_split(e2);
+        float sq = qf.x + qf.y, sd = ef.x + ef.y;
+        const float s = warp_sums(sq, sd, lane), t = __shfl_xor_sync(0xffffffffu, s, 16);
+        const float2 k = norm_factors((lane & 16 ? t : s) / (float)cols, (lane & 16 ? s : t) / (float)cols, eps);
+        const uint64_t rstd2 = f2_make(k.x, k.x), off2 = f2_make(k.y, k.y);
 #pragma unroll
         for (int c = 0; c < NCH; ++c) {
             if (!WHOLE && c >= chunks) break;
@@ -464,7 +484,7 @@ mx4_norm_warp_kernel(const T *__restrict__ x, long long ld, const float *__restr
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float2 f = f2_split(f2_fma(f2_mul(v[c][i], rstd2), f2_make(g[2 * i], g[2 * i + 1]), f2_make(b[2 * i], b[2 * i + 1])));
+                const float2 f = f2_split(f2_fma(f2_fma(v[c][i], rstd2, off2), f2_make(g[2 * i], g[2 * i + 1]), f2_make(b[2 * i], b[2 * i + 1])));
                 u[2 * i] = f.x;
                 u[2 * i + 1] = f.y;
             }
@@ -500,8 +520,8 @@ mx4_norm_warp_kernel(const T *__restrict__ x, long long ld, const float *__restr
 // next row's values load while this one's sums are joined.  WORDS: rows that are not
 // 16-byte aligned, or of a width that is no multiple of 8, come and go by words.  What
 // bounds it over many rows is instructions: 8192 rows of 1000, 2048, 4096 bf16 columns take
-// 9.2, 16.7 and 33.5 us (eight columns a lane: 10.7, 20.9, 43; in the kernel for wider rows
-// 25, 33, 58), of 1001 by words 16.4 (by values, in that kernel, 30).
+// 9.1, 15.8 and 34.5 us (eight columns a lane: 10.7, 20.9, 43; in the kernel for wider rows
+// 25, 33, 58), of 1001 by words 16.8 (by values, in that kernel, 30).
 template <int W>
 __device__ __forceinline__ float block_sum(float v, float *red) {
 #pragma unroll
@@ -520,6 +540,23 @@ __device__ __forceinline__ float block_sum(float v, float *red) {
     }
     return (s.x + s.y) + (s.z + s.w);
 }
+// Two sums at once.
+template <int W>
+__device__ __forceinline__ float2 block_sums(float a, float b, float *red) {
+    const float v = warp_sums(a, b, threadIdx.x & 31);
+    if ((threadIdx.x & 15) == 0) red[threadIdx.x >> 4] = v;
+    __syncthreads();
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i) {
+        const float4 r = reinterpret_cast<const float4 *>(red)[i];
+        s.x += r.x;
+        s.y += r.y;
+        s.z += r.z;
+        s.w += r.w;
+    }
+    return make_float2(s.x + s.z, s.y + s.w);
+}
 
 template <typename T, bool NV, int W, bool WORDS>
 __global__ void __launch_bounds__(32 * W)
@@ -527,7 +564,9 @@ mx4_norm_cta_kernel(const T *__restrict__ x, long long ld, const float *__restri
                     const float *__restrict__ beta, float eps, int rows, int cols, const int *n_rows, float ts,
                     T *__restrict__ y, long long ld_y, uint8_t *__restrict__ codes,
                     uint8_t *__restrict__ scales, int vec, int vec_y, int vec_g, const int *status, int trigger) {
-    __shared__ __align__(16) float red[2][W];  // one per sum: a row's second barrier separates its first from the next row's
+    // one for each barrier of a row: its second one separates its first from the next row's
+    __shared__ __align__(16) float red[W];
+    __shared__ __align__(16) float red2[2 * W];
     __shared__ uint4 seg4[WORDS ? W * 2 * kSegWords<T> / 4 : 1];
     uint32_t *seg = reinterpret_cast<uint32_t *>(seg4) + (WORDS ? (threadIdx.x >> 5) * 2 * kSegWords<T> : 0);
     if (trigger) griddep_launch_dependents();
@@ -539,7 +578,9 @@ mx4_norm_cta_kernel(const T *__restrict__ x, long long ld, const float *__restri
     const int lane = threadIdx.x & 31;
     const int chunks = mx4_stages(cols), pitch = mx4_code_pitch(cols);
     const int row_tiles = chunks * Mx4<NV>::kStageTiles;
-    const float inv_cols = 1.0f / (float)cols;  // (a division per sum cost a twentieth)
+    // (a division per sum cost a twentieth; the mean's rounding is made good below, the
+    // variance's is half a unit of rstd)
+    const float inv_cols = 1.0f / (float)cols;
     const int col = threadIdx.x * 16, n = cols - col;  // aligned rows: n is 0 or less, 8, or more
     const int col0 = (threadIdx.x >> 5) * 512;
     constexpr int kLanes = NV ? 1 : 2, kTileLanes = 4 * kLanes;  // lanes of a block, of a scale tile
@@ -615,12 +656,12 @@ mx4_norm_cta_kernel(const T *__restrict__ x, long long ld, const float *__restri
         }
         raw = load(row + gridDim.x);
         const float2 sf = f2_split(s2);
-        const float mean = block_sum<W>(sf.x + sf.y, red[0]) * inv_cols;
+        const float mean = block_sum<W>(sf.x + sf.y, red) * inv_cols;
         const uint64_t nmean2 = f2_make(-mean, -mean);
-        float sq = 0.f;
+        float sq = 0.f, sd = 0.f;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            uint64_t q2 = f2_make(0.f, 0.f);
+            uint64_t q2 = f2_make(0.f, 0.f), e2 = q2;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 v[4 * h + i] = f2_add(v[4 * h + i], nmean2);
@@ -629,18 +670,21 @@ mx4_norm_cta_kernel(const T *__restrict__ x, long long ld, const float *__restri
                     v[4 * h + i] = f2_make(8 * h + 2 * i < n ? d.x : 0.f, 8 * h + 2 * i + 1 < n ? d.y : 0.f);
                 }
                 q2 = f2_fma(v[4 * h + i], v[4 * h + i], q2);
+                e2 = f2_add(e2, v[4 * h + i]);
             }
-            const float2 qf = f2_split(q2);
+            const float2 qf = f2_split(q2), ef = f2_split(e2);
             sq += WORDS || n > 8 * h ? qf.x + qf.y : 0.f;
+            sd += WORDS || n > 8 * h ? ef.x + ef.y : 0.f;
         }
-        const float rstd = rsqrtf(block_sum<W>(sq, red[1]) * inv_cols + eps);
-        const uint64_t rstd2 = f2_make(rstd, rstd);
+        const float2 sums = block_sums<W>(sq, sd, red2);
+        const float2 k = norm_factors(sums.x * inv_cols, sums.y * inv_cols, eps);
+        const uint64_t rstd2 = f2_make(k.x, k.x), off2 = f2_make(k.y, k.y);
         if (col0 >= cols) continue;  // (the whole warp)
         float u[16];
         float m = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const float2 w = f2_split(f2_fma(f2_mul(v[i], rstd2), g[i], b[i]));
+            const float2 w = f2_split(f2_fma(f2_fma(v[i], rstd2, off2), g[i], b[i]));
             u[2 * i] = n > (WORDS ? 2 * i : 8 * (i >> 2)) ? w.x : 0.f;
             u[2 * i + 1] = n > (WORDS ? 2 * i + 1 : 8 * (i >> 2)) ? w.y : 0.f;
             m = fmax3_abs_nan(m, u[2 * i], u[2 * i + 1]);
@@ -697,15 +741,16 @@ mx4_norm_cta_kernel(const T *__restrict__ x, long long ld, const float *__restri
 
 // Wider rows: one CTA per row, each warp holds four of the row's chunks (every eighth);
 // chunks beyond those are read again in each pass (from L1 or L2).  2000 rows of 8200 bf16
-// columns take 27 us.
+// columns take 24 us in mxfp4, 29 in nvfp4.
 template <typename T, bool NV>
-__global__ void __launch_bounds__(32 * kQWarps)
+__global__ void __launch_bounds__(32 * kQWarps, sizeof(T) == 4 ? 2 : NV ? 3 : 4)  // (nvfp4: two CTAs per SM took 36 us)
 mx4_norm_wide_kernel(const T *__restrict__ x, long long ld, const float *__restrict__ gamma,
                      const float *__restrict__ beta, float eps, int rows, int cols, const int *n_rows, float ts,
                      T *__restrict__ y, long long ld_y, uint8_t *__restrict__ codes,
                      uint8_t *__restrict__ scales, int vec, int vec_y, int vec_g, const int *status, int trigger) {
     constexpr int W = kQWarps, HELD = 4;
-    __shared__ __align__(16) float red[2][W];  // as above
+    __shared__ __align__(16) float red[W];  // as above
+    __shared__ __align__(16) float red2[2 * W];
     if (trigger) griddep_launch_dependents();
     griddep_wait();
     const Mx4Ts tsc = mx4_ts(ts);
@@ -745,16 +790,18 @@ mx4_norm_wide_kernel(const T *__restrict__ x, long long ld, const float *__restr
 #pragma unroll
             for (int i = 0; i < 8; ++i) sum += v[i];
         });
-        const float mean = block_sum<W>(sum, red[0]) / (float)cols;
-        float sq = 0.f;
+        const float mean = block_sum<W>(sum, red) / (float)cols;
+        float sq = 0.f, sd = 0.f;
         each([&](int, int, int n, const float (&v)[8]) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const float d = i < n ? v[i] - mean : 0.f;
                 sq = fmaf(d, d, sq);
+                sd += d;
             }
         });
-        const float rstd = rsqrtf(block_sum<W>(sq, red[1]) / (float)cols + eps);
+        const float2 sums = block_sums<W>(sq, sd, red2);
+        const float2 k = norm_factors(sums.x / (float)cols, sums.y / (float)cols, eps);
         each([&](int c, int col, int n, float (&v)[8]) {
             float g[8], b[8];
             load8<float>(gamma + col, n, vec_g != 0, g);
@@ -762,7 +809,7 @@ mx4_norm_wide_kernel(const T *__restrict__ x, long long ld, const float *__restr
             uint32_t m = 0;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                v[i] = i < n ? fmaf((v[i] - mean) * rstd, g[i], b[i]) : 0.f;
+                v[i] = i < n ? fmaf(fmaf(v[i] - mean, k.x, k.y), g[i], b[i]) : 0.f;
                 m = umax(m, abs_bits(v[i]));
             }
             if (y) store8<T>(y + (size_t)row * ld_y + col, n, vec_y != 0, v);
