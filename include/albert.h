@@ -381,7 +381,7 @@ int albert_mx4_layer_norm(const void *x, int x_type, long long ld_x, const float
 /* A linear layer on 4-bit operands:
  *   z = A W^T + bias (tcgen05, fp32 accumulation over the scaled products)
  *   z = 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)))   if gelu
- *   z = z + residual                                     if residual
+ *   z = z + residual                                     if residual (only with out)
  * then out = z rounded once to out_type, or the 4-bit form of z (q_codes,
  * q_scales).  A [rows, k] is either 4-bit (a_codes, a_scales) or x of x_type,
  * which is quantized as albert_mx4_quantize does (same result as calling it).
@@ -389,7 +389,8 @@ int albert_mx4_layer_norm(const void *x, int x_type, long long ld_x, const float
  * out may be the same rows.  Each row's result depends on that row alone.  At most
  * 32 rows run in one kernel that quantizes x itself (no workspace); more take a
  * quantization pass into the workspace, then the product.
- * Further ALBERT_ERR_CONFIG: x_scale * w_scale outside [2^-100, 2^100]. */
+ * Further ALBERT_ERR_CONFIG: x_scale * w_scale outside [2^-100, 2^100]; a residual with a
+ * 4-bit result. */
 typedef struct {
     const void *x;             /* rows to quantize, or NULL                      */
     const void *a_codes;       /* 4-bit rows (x == NULL)                         */
@@ -397,7 +398,7 @@ typedef struct {
     const void *w_codes;
     const void *w_scales;
     const float *bias;         /* [n] or NULL                                    */
-    const void *residual;      /* [rows, n] of out_type, or NULL                 */
+    const void *residual;      /* [rows, n] of out_type, or NULL (and if out is) */
     void *out;                 /* [rows, n], or NULL for a 4-bit result          */
     void *q_codes;             /* 4-bit result [rows, n] (out == NULL)           */
     void *q_scales;

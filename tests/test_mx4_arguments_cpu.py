@@ -1,0 +1,32 @@
+"""Arguments of the 4-bit operators without a GPU: calls that the host must refuse, and what the
+Python wrappers do with the tensors they are given."""
+import ctypes as C
+
+import pytest
+
+import transformer_encoder_albert_b200 as tea
+from transformer_encoder_albert_b200 import build as tea_build
+
+P = 1 << 20  # a non-NULL, aligned pointer value that the host checks never dereference
+CONFIG = 2
+
+
+@pytest.fixture(scope="module")
+def lib():
+    tea_build.build()
+    return tea.lib()
+
+
+def _linear(lib, **kw):
+    a = tea.albert_mx4_linear_args()
+    base = dict(a_codes=P, a_scales=P, w_codes=P, w_scales=P, out=P, ld_out=48, x_scale=1.0, w_scale=1.0, q_scale=1.0,
+                rows=4, n=48, k=64, fmt=3)
+    for k, v in {**base, **kw}.items():
+        setattr(a, k, v)
+    return lib.albert_mx4_linear(C.byref(a), None)
+
+
+@pytest.mark.parametrize("rows", [4, 300])
+def test_a_residual_with_a_4_bit_result_is_refused(lib, rows):
+    for fmt in (tea.ALBERT_MXFP4, tea.ALBERT_NVFP4):
+        assert _linear(lib, rows=rows, fmt=fmt, out=None, q_codes=P, q_scales=P, residual=P, ld_residual=48) == CONFIG

@@ -45,7 +45,7 @@ struct Mx4GemmArgs {
     float alpha;            // product of the two tensor scales
     const float *bias;      // [N] or nullptr
     int gelu;
-    const void *res;        // [M, N] of out_type, or nullptr
+    const void *res;        // [M, N] of out_type, or nullptr (as with a 4-bit result)
     long long ld_res;
     void *out;              // nullptr: 4-bit result
     int out_type;

@@ -147,6 +147,7 @@ int albert_mx4_linear(const albert_mx4_linear_args *p, void *stream) {
         (p->out ? !aligned(p->out, elem_size(p->out_type)) : !aligned(p->q_codes, 16) || !aligned(p->q_scales, 16)))
         return ALBERT_ERR_CONFIG;
     if (p->gelu != 0 && p->gelu != 1) return ALBERT_ERR_CONFIG;
+    if (p->residual && !p->out) return ALBERT_ERR_CONFIG;
     // the product of the tensor scales multiplies the fp32 sum: far from fp32's limits
     if (p->fmt == ALBERT_NVFP4 && !(p->x_scale * p->w_scale >= kMinScale && p->x_scale * p->w_scale <= kMaxScale))
         return ALBERT_ERR_CONFIG;
