@@ -380,7 +380,7 @@ int albert_mx4_layer_norm(const void *x, int x_type, long long ld_x, const float
 
 /* A linear layer on 4-bit operands:
  *   z = A W^T + bias (tcgen05, fp32 accumulation over the scaled products)
- *   z = 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)))   if gelu
+ *   z = 0.5 z (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)))   if gelu (-0 for z < -7.61: above -10^-18)
  *   z = z + residual                                     if residual (only with out)
  * then out = z rounded once to out_type, or the 4-bit form of z (q_codes,
  * q_scales).  A [rows, k] is either 4-bit (a_codes, a_scales) or x of x_type,

@@ -225,8 +225,12 @@ __device__ __forceinline__ float fmax3_abs_nan(float a, float b, float c) {
 // GELU_tanh of a pair: x / (1 + e), e = exp(-2u), u = sqrt(2/pi) (x + 0.044715 x^3).  The
 // two quotients share one reciprocal, 1 / ((1 + e0)(1 + e1)): three special-function
 // operations for two values instead of four (they set the pace: 16 lanes per clock and
-// SM).  The exponent stops at 63, so that the product stays finite; the value there is
-// x 2^-63.  Relative error a few 2^-23 plus 2^-23 |2u| from the exponential's argument.
+// SM).  The exponent stops at 63, so that the product stays finite.  Past it (x below -7.61)
+// the factor is 0, which is off by at most 7.7 x 2^-63 < 10^-18 and gives -0 however far x
+// is, and NaN for -infinity, as the tanh form does.  Above, the relative error is a few 2^-23
+// plus 2^-23 |2u| from the exponential's argument.  (18797 x 768 -> 2048 in mxfp4 with a bf16
+// result: 30.4 us; 28.7 without the two selections, 31.3 with a reciprocal each and no limit,
+// 31.8 where a warp first looks whether it has such a value.)
 __device__ __forceinline__ uint64_t gelu_f2(uint64_t x) {
     const float k0 = -2.0f * 0.7978845608028654f * 1.4426950408889634f, k1 = k0 * 0.044715f;
     const float2 t = f2_split(f2_mul(x, f2_fma(f2_mul(x, x), f2_make(k1, k1), f2_make(k0, k0))));
@@ -234,7 +238,8 @@ __device__ __forceinline__ uint64_t gelu_f2(uint64_t x) {
     const float2 df = f2_split(d);
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(df.x * df.y));
-    return f2_mul(x, f2_mul(f2_make(df.y, df.x), f2_make(r, r)));  // (1 / d first: x d could overflow)
+    const float2 f = f2_split(f2_mul(f2_make(df.y, df.x), f2_make(r, r)));  // (1 / d first: x d could overflow)
+    return f2_mul(x, f2_make(t.x > 63.0f ? 0.f : f.x, t.y > 63.0f ? 0.f : f.y));
 }
 
 __device__ __forceinline__ uint32_t abs_bits(float x) { return __float_as_uint(x) & 0x7fffffffu; }
