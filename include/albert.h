@@ -340,7 +340,8 @@ size_t albert_length_regulate_scratch_bytes(int n_tok);
  *   scales  albert_mx4_scales_bytes: tiles of 128 rows x 4 blocks of a row, 512
  *           bytes each, [ceil(rows / 128)][tiles per row]: the scale of row r,
  *           block b is byte (r % 32) * 16 + (r % 128) / 32 * 4 + b % 4 of tile
- *           [r / 128][b / 4].  Tiles per row cover cols rounded up to 256.
+ *           [r / 128][b / 4].  Tiles per row cover cols rounded up to 256.  The
+ *           entries below write whole tiles: bytes past cols and past rows are 0.
  * and a format with, for ALBERT_NVFP4, a tensor scale ts (a host float, finite,
  * 2^-100 <= ts <= 2^100; ignored for ALBERT_MXFP4).  For a block with largest
  * magnitude amax:

@@ -58,3 +58,57 @@ def test_far_values_do_not_set_a_blocks_scale(rows, fmt):
     assert np.all(np.abs(got - ref) <= np.abs(ref) * (0.25 + 2.0 ** -16))
     _, byte = mq.unpack(q.codes.cpu().numpy(), q.scales.cpu().numpy(), rows, n, fmt)
     assert np.all(byte[:, -1] == 0)
+
+
+# -------------------------------------------------------- what a call writes --
+
+def _tensor(rows, cols, fmt):
+    """A 4-bit matrix over buffers filled with 0xAA, and the bytes behind each."""
+    c, s = tea.mx4_shapes(rows, cols, fmt)
+    n, m = c[0] * c[1], s[0] * s[1] * s[2]
+    cb, sb = (torch.full((k + 512,), 0xAA, dtype=torch.uint8, device="cuda") for k in (n, m))
+    return tea.Mx4Tensor(cb[:n].view(c), sb[:m].view(s), rows, cols, fmt, TS[fmt]), cb[n:], sb[m:]
+
+
+def _check_past_rows(q, behind_codes, behind_scales):
+    t = q.scales.cpu().numpy()
+    r, b = np.arange(q.rows, t.shape[0] * 128)[:, None], np.arange(t.shape[1] * 4)[None]
+    assert np.all(t[r // 128, b // 4, (r % 32) * 16 + (r % 128) // 32 * 4 + b % 4] == 0)
+    r, b = np.arange(q.rows)[:, None], np.arange(q.codes.shape[1] * 2 // mq.BLOCK[q.fmt], t.shape[1] * 4)[None]
+    assert np.all(t[r // 128, b // 4, (r % 32) * 16 + (r % 128) // 32 * 4 + b % 4] == 0)
+    assert torch.all(behind_codes == 0xAA) and torch.all(behind_scales == 0xAA)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("rows,cols", [(1, 1), (1, 200), (7, 768), (600, 700), (128, 256), (700, 768), (1, 1000), (129, 1001),
+                                       (9, 2000), (5, 4096), (3, 8001), (1, 8200), (140, 9000)])
+def test_layer_norm_writes_whole_scale_tiles(rows, cols, fmt):
+    q, cb, sb = _tensor(rows, cols, fmt)
+    x, g, b = torch.randn(rows, cols, device="cuda"), torch.ones(cols, device="cuda"), torch.zeros(cols, device="cuda")
+    rc = tea.lib().albert_mx4_layer_norm(x.data_ptr(), tea.ALBERT_FP32, cols, g.data_ptr(), b.data_ptr(), 1e-5, rows, cols,
+                                         tea.MX4_FORMATS[fmt], TS[fmt], None, 0, q.codes.data_ptr(), q.scales.data_ptr(),
+                                         torch.cuda.current_stream().cuda_stream)
+    assert rc == 0
+    _check_past_rows(q, cb, sb)
+    ref = tea.mx4_layer_norm(x, g, b, 1e-5, fmt, TS[fmt], return_rows=False)[1]
+    assert torch.equal(q.codes, ref.codes) and torch.equal(q.scales, ref.scales)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("rows,n,k", [(1, 32, 32), (1, 2048, 768), (5, 100, 96), (16, 300, 4200), (31, 33, 256), (32, 640, 768),
+                                      (33, 256, 300), (130, 320, 768), (129, 1000, 64), (300, 2048, 256), (2600, 2020, 288),
+                                      (10000, 1030, 96)])
+def test_a_4_bit_result_writes_whole_scale_tiles(rows, n, k, fmt):
+    import ctypes as C
+    q, cb, sb = _tensor(rows, n, fmt)
+    w = tea.mx4_quantize(torch.randn(n, k, device="cuda") * 0.05, fmt, 1e-4)
+    x = tea.mx4_quantize(torch.randn(rows, k, device="cuda"), fmt, TS[fmt])
+    a = tea.albert_mx4_linear_args()
+    for f, v in dict(a_codes=x.codes.data_ptr(), a_scales=x.scales.data_ptr(), w_codes=w.codes.data_ptr(),
+                     w_scales=w.scales.data_ptr(), q_codes=q.codes.data_ptr(), q_scales=q.scales.data_ptr(), x_scale=TS[fmt],
+                     w_scale=1e-4, q_scale=TS[fmt], rows=rows, n=n, k=k, fmt=tea.MX4_FORMATS[fmt]).items():
+        setattr(a, f, v)
+    assert tea.lib().albert_mx4_linear(C.byref(a), torch.cuda.current_stream().cuda_stream) == 0
+    _check_past_rows(q, cb, sb)
+    ref = tea.mx4_linear_quant(x, w, out_scale=TS[fmt])
+    assert torch.equal(q.codes, ref.codes) and torch.equal(q.scales, ref.scales)

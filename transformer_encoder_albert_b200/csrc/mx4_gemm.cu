@@ -515,12 +515,14 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                             q[(b * kB + j) / 8] = s.zero ? 0u : cvt_e2m1x8(y);
                         }
                     }
-                    if (row_ok) {
-                        if (col0 / 2 < pitch)
+                    // (rows past the last: scale 0 to the end of their tile, as the quantiser leaves them)
+                    if (row < (n_rows + 127) / 128 * 128) {
+                        if (row_ok && col0 / 2 < pitch)
                             *reinterpret_cast<uint4 *>(p.q + (size_t)row * pitch + col0 / 2) = make_uint4(q[0], q[1], q[2], q[3]);
                         const int blk = col0 / kB;
                         uint8_t *sp = p.q_scales + ((size_t)(row >> 7) * tiles + (blk >> 2)) * kMx4TileBytes + (row & 31) * 16 +
                                       ((row >> 5) & 3) * 4 + (blk & 3);
+                        if (!row_ok) bytes = 0;
                         if (NV) *reinterpret_cast<uint16_t *>(sp) = (uint16_t)bytes;
                         else *sp = (uint8_t)bytes;
                     }

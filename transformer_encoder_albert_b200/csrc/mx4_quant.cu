@@ -26,6 +26,26 @@ __device__ __forceinline__ size_t scale_word_offset(int row, int tile, int row_t
     return ((size_t)(row >> 7) * row_tiles + tile) * kMx4TileBytes + (row & 31) * 16 + ((row >> 5) & 3) * 4;
 }
 
+// The scale bytes of the rows between the last and the end of its tile are 0, as the quantiser
+// leaves them: equal calls leave equal tiles.  By all threads of the grid; a thread takes the
+// four rows that share 16 bytes of a tile.
+__device__ __forceinline__ void zero_past_rows(uint8_t *scales, int rows, int row_tiles) {
+    const int in_tile = rows & 127;
+    if (rows <= 0 || in_tile == 0) return;
+    uint8_t *last = scales + (size_t)(rows >> 7) * row_tiles * kMx4TileBytes;
+    for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < row_tiles * 32; i += gridDim.x * blockDim.x) {
+        const int r = i & 31;
+        uint32_t *word = reinterpret_cast<uint32_t *>(last + (size_t)i * 16);
+        if (r >= in_tile) {
+            *reinterpret_cast<uint4 *>(word) = make_uint4(0, 0, 0, 0);
+        } else {
+#pragma unroll
+            for (int q = 1; q < 4; ++q)
+                if (r + 32 * q >= in_tile) word[q] = 0;
+        }
+    }
+}
+
 // A warp's walk over (row pair, chunk) items with a grid stride, chunks innermost:
 // one division at the start, none per item.  Pair g is the rows 128 (g / 64) +
 // 64 (g / 32 % 2) + g % 32 and the row 32 below.
@@ -507,6 +527,7 @@ mx4_norm_warp_kernel(const T *__restrict__ x, long long ld, const float *__restr
         }
     };
     if (row < nr) load(row);
+    zero_past_rows(scales, nr, row_tiles);
     const bool whole = cols == NCH * kMx4StageCols && vec && vec_g == 2 && (!y || vec_y);
     if (whole)
         for (; row < nr; row += stride) one_row(std::true_type{});
@@ -623,6 +644,7 @@ mx4_norm_cta_kernel(const T *__restrict__ x, long long ld, const float *__restri
     };
     int row = blockIdx.x;
     Raw raw = load(row);
+    zero_past_rows(scales, nr, row_tiles);
     for (; row < nr; row += gridDim.x) {
         Raw16<T> own;
         if constexpr (WORDS) {
@@ -761,6 +783,7 @@ mx4_norm_wide_kernel(const T *__restrict__ x, long long ld, const float *__restr
     const int chunks = mx4_stages(cols), pitch = mx4_code_pitch(cols);
     const int row_tiles = chunks * Mx4<NV>::kStageTiles;
     constexpr int kTileLanes = Mx4<NV>::kTileCols / 8;
+    zero_past_rows(scales, nr, row_tiles);
     for (int row = blockIdx.x; row < nr; row += gridDim.x) {
         const T *src = x + (size_t)row * ld;
         Raw8<T> raw[HELD];
@@ -923,7 +946,11 @@ template <typename T, bool NV, typename K>
 cudaError_t norm_launch(K kernel, std::atomic<int> (&cached)[64], int rows_per_cta, int warps, const Mx4NormArgs &a, cudaStream_t s,
                         bool pdl) {
     int blocks = 0;
-    cudaError_t e = resident_grid(kernel, cached, (a.q.rows + rows_per_cta - 1) / rows_per_cta, blocks, warps);
+    // (few rows: CTAs without one too, so that a thread zeroes 16 bytes of the last tiles at the
+    // most; one row of 8192 in nvfp4 took 4.8 us with its own CTA writing all 64 KB)
+    const int row_tiles = mx4_stages(a.q.cols) * Mx4<NV>::kStageTiles;
+    const int need = std::max((a.q.rows + rows_per_cta - 1) / rows_per_cta, (row_tiles + warps - 1) / warps);
+    cudaError_t e = resident_grid(kernel, cached, need, blocks, warps);
     if (e != cudaSuccess) return e;
     const int vec = vec_width(a.q.x, a.q.ld, sizeof(T)), vec_y = vec_width(a.y, a.ld_y, sizeof(T));
     const int vec_g = std::min(vec_width(a.gamma, 8, 4), vec_width(a.beta, 8, 4));

@@ -325,6 +325,15 @@ mx4_tokens_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
         const float bias = p.bias && feat < p.N ? __ldg(p.bias + feat) : 0.f;
         const uint32_t own = smem_u32(sum);
         const Mx4Ts q_ts = mx4_ts(p.q_ts);
+        if (!p.out) {  // scale bytes of the rows past the last token, to the end of their tile
+            constexpr int kTiles = 128 / Mx4<NV>::kTileCols;
+            for (int i = threadIdx.x - 64 + (int)rank * 32 * kWorkers; i < 128 * kTiles; i += 32 * kWorkers * nclu) {
+                const int r = i & 127;
+                if (r >= p.M)
+                    *reinterpret_cast<uint32_t *>(p.q_scales + (size_t)(tile * kTiles + (i >> 7)) * kMx4TileBytes + (r & 31) * 16 +
+                                                  (r >> 5) * 4) = 0;
+            }
+        }
         // this CTA's tokens: rank, rank + nclu, ..., the groups of four warps in turn
         for (int t = (int)rank + (wk >> 2) * nclu; t < p.M; t += kWorkers / 4 * nclu) {
             float acc = 0.f;
