@@ -387,11 +387,12 @@ int albert_mx4_layer_norm(const void *x, int x_type, long long ld_x, const float
  * q_scales).  A [rows, k] is either 4-bit (a_codes, a_scales) or x of x_type,
  * which is quantized as albert_mx4_quantize does (same result as calling it).
  * W [n, k] is 4-bit, as albert_mx4_quantize leaves a weight matrix.  residual and
- * out may be the same rows.  Each row's result depends on that row alone.  At most
+ * out may be the same rows, and more than 32 rows of x and out may overlap; a result
+ * overlaps no other operand.  Each row's result depends on that row alone.  At most
  * 32 rows run in one kernel that quantizes x itself (no workspace); more take a
  * quantization pass into the workspace, then the product.
  * Further ALBERT_ERR_CONFIG: x_scale * w_scale outside [2^-100, 2^100]; a residual with a
- * 4-bit result. */
+ * 4-bit result; rows of x and out that overlap, of at most 32. */
 typedef struct {
     const void *x;             /* rows to quantize, or NULL                      */
     const void *a_codes;       /* 4-bit rows (x == NULL)                         */

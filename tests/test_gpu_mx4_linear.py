@@ -112,3 +112,18 @@ def test_a_4_bit_result_writes_whole_scale_tiles(rows, n, k, fmt):
     _check_past_rows(q, cb, sb)
     ref = tea.mx4_linear_quant(x, w, out_scale=TS[fmt])
     assert torch.equal(q.codes, ref.codes) and torch.equal(q.scales, ref.scales)
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("rows", [1, 5, 32, 33, 300, 5000])
+def test_a_result_over_its_own_input(rows, fmt):
+    """x and out are the same rows, share columns of one buffer, or lie beside one another in it."""
+    buf = torch.randn(rows, 1600, device="cuda", dtype=torch.bfloat16)
+    w = tea.mx4_quantize(torch.randn(768, 768, device="cuda") * 0.05, fmt, 1e-4)
+    ref = tea.mx4_linear(buf[:, :768].clone(), w, x_scale=TS[fmt])
+    for at in (0, 64, 767, 800):
+        b = buf.clone()
+        out = tea.mx4_linear(b[:, :768], w, out=b[:, at:at + 768], x_scale=TS[fmt])
+        assert torch.equal(out, ref)
+        b[:, at:at + 768] = buf[:, at:at + 768]
+        assert torch.equal(b, buf)

@@ -30,3 +30,20 @@ def _linear(lib, **kw):
 def test_a_residual_with_a_4_bit_result_is_refused(lib, rows):
     for fmt in (tea.ALBERT_MXFP4, tea.ALBERT_NVFP4):
         assert _linear(lib, rows=rows, fmt=fmt, out=None, q_codes=P, q_scales=P, residual=P, ld_residual=48) == CONFIG
+
+
+def test_few_rows_of_x_and_out_that_overlap_are_refused(lib):
+    """The few-row kernel reads x while other parts of it write: any shared byte is refused; rows
+    that lie between one another, or more than 32 rows, are not."""
+    def f(x, out, **kw):
+        return _linear(lib, **{**dict(x=x, ld_x=64, out=out, ld_out=48, workspace=8 * P, k=64, n=48), **kw})
+
+    for kw in (dict(), dict(x_type=tea.ALBERT_FP32, out_type=tea.ALBERT_FP32), dict(rows=32)):
+        assert f(P, P, **kw) == CONFIG
+    assert f(P, P + 126) == CONFIG and f(P, P + 3 * 128 + 126) == CONFIG and f(P + 3 * 96 + 94, P) == CONFIG
+    ok = [f(P, P + 4 * 128), f(P + 3 * 96 + 96, P),                         # one behind the other
+          f(P, P + 128, ld_x=200, ld_out=200), f(P + 96, P, ld_x=200, ld_out=200),  # columns of one buffer
+          f(P, P, rows=33), f(None, P)]                                     # quantized first; 4-bit rows
+    assert CONFIG not in ok, ok
+    assert f(P, P + 126, ld_x=200, ld_out=200) == CONFIG                   # its columns, one too many
+    assert f(P, P + 128, ld_x=200, ld_out=112) == CONFIG                   # (strides apart: some pair of rows meets)

@@ -694,6 +694,10 @@ def mx4_layer_norm(x, gamma, beta, eps: float = 1e-12, fmt: str = "mxfp4", tenso
 
 def _mx4_linear(x, w: Mx4Tensor, bias, residual, gelu, x_scale, stream, out, dtype, q_scale):
     a = albert_mx4_linear_args()
+    # (few rows are read by one part of the kernel while another writes its results: rows of
+    # the result's own buffer are quantized first)
+    if out is not None and type(x) is not Mx4Tensor and out.untyped_storage().data_ptr() == x.untyped_storage().data_ptr():
+        x = mx4_quantize(x, w.fmt, x_scale, None, stream)
     if type(x) is Mx4Tensor:
         rows, k, dev = x.rows, x.cols, x._dev
         if x.fmt != w.fmt:
@@ -750,7 +754,8 @@ def mx4_linear(x, w: Mx4Tensor, bias=None, residual=None, gelu: bool = False, dt
 
     x: rows (bf16, fp16 or fp32), quantized in the call with tensor scale x_scale as
     mx4_quantize does, or a 4-bit matrix of w's format.  w: [n, k] 4-bit weights.
-    bias [n] fp32; residual [rows, n] of the result's dtype (default bfloat16)."""
+    bias [n] fp32; residual [rows, n] of the result's dtype (default bfloat16).  `out` may
+    overlap x, and be residual itself."""
     if out is None and dtype is None:
         torch = _torch or _mx4_torch()
         dtype = torch.bfloat16

@@ -65,6 +65,16 @@ int check_rows(const void *x, int x_type, long long ld, int rows, int cols, int 
     return ALBERT_OK;
 }
 
+// Whether any of the rows at a (wa bytes each, la apart) shares a byte with any of those at b.
+bool rows_overlap(const void *a, long long la, long long wa, const void *b, long long lb, long long wb, int rows) {
+    const uintptr_t pa = reinterpret_cast<uintptr_t>(a), pb = reinterpret_cast<uintptr_t>(b);
+    if (pa + (rows - 1) * la + wa <= pb || pb + (rows - 1) * lb + wb <= pa) return false;
+    for (int i = 0; i < rows; ++i)
+        for (int j = 0; j < rows; ++j)
+            if (pa + i * la < pb + j * lb + wb && pb + j * lb < pa + i * la + wa) return true;
+    return false;
+}
+
 }  // namespace
 
 extern "C" {
@@ -148,6 +158,11 @@ int albert_mx4_linear(const albert_mx4_linear_args *p, void *stream) {
         return ALBERT_ERR_CONFIG;
     if (p->gelu != 0 && p->gelu != 1) return ALBERT_ERR_CONFIG;
     if (p->residual && !p->out) return ALBERT_ERR_CONFIG;
+    // (a CTA of the few-row kernel may write its columns while another still reads x)
+    if (p->rows <= kMx4MaxTokens && p->x && p->out) {
+        const long long ex = elem_size(p->x_type), eo = elem_size(p->out_type);
+        if (rows_overlap(p->x, p->ld_x * ex, p->k * ex, p->out, p->ld_out * eo, p->n * eo, p->rows)) return ALBERT_ERR_CONFIG;
+    }
     // the product of the tensor scales multiplies the fp32 sum: far from fp32's limits
     if (p->fmt == ALBERT_NVFP4 && !(p->x_scale * p->w_scale >= kMinScale && p->x_scale * p->w_scale <= kMaxScale))
         return ALBERT_ERR_CONFIG;
