@@ -127,3 +127,43 @@ def test_a_result_over_its_own_input(rows, fmt):
         assert torch.equal(out, ref)
         b[:, at:at + 768] = buf[:, at:at + 768]
         assert torch.equal(b, buf)
+
+
+# ------------------------------------------------------------------- streams --
+
+def test_inputs_of_a_call_on_another_stream_keep_their_memory(monkeypatch):
+    """Every tensor of a call on another stream is recorded on it, so that the allocator does not
+    hand its memory out before the call has run where the caller drops it at once; the results
+    are those of the call alone."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    rows, n, k = 300, 512, 256
+    x = torch.randn(rows, k, device="cuda", generator=g).to(torch.bfloat16)
+    gamma, beta = (torch.randn(k, device="cuda", generator=g) for _ in range(2))
+    bias = torch.randn(n, device="cuda", generator=g)
+    res = torch.randn(rows, n, device="cuda", generator=g).to(torch.bfloat16)
+    w = tea.mx4_quantize(torch.randn(n, k, device="cuda", generator=g) * 0.05, "mxfp4")
+    u = tea.mx4_quantize(x, "mxfp4")
+    v = tea.Mx4Tensor(u.codes.clone(), u.scales.clone(), rows, k, "mxfp4")
+    out = torch.empty(rows, n, device="cuda", dtype=torch.bfloat16)
+    given = tea.mx4_empty(rows, k)
+    calls = [((x, given), lambda s: tea.mx4_quantize(x, "mxfp4", out=given, stream=s).codes),
+             ((u,), lambda s: tea.mx4_dequantize(u, stream=s)),
+             ((v, out), lambda s: tea.mx4_dequantize(v, out=out[:, :k], stream=s)),
+             ((x, gamma, beta), lambda s: tea.mx4_layer_norm(x, gamma, beta, 1e-5, stream=s)[0]),
+             ((x, w, bias, res, out), lambda s: tea.mx4_linear(x, w, bias, res, out=out, stream=s)),
+             ((x, w), lambda s: tea.mx4_linear(x[:4], w, stream=s)),
+             ((v, w, bias), lambda s: tea.mx4_linear_quant(v, w, bias, stream=s).codes)]
+    side, seen = torch.cuda.Stream(), set()
+    keep = torch.Tensor.record_stream
+    monkeypatch.setattr(torch.Tensor, "record_stream",
+                        lambda t, s: (seen.add((t.untyped_storage().data_ptr(), s.cuda_stream)), keep(t, s))[1])
+    for used, call in calls:
+        ref = call(None).clone()
+        assert not seen
+        torch.cuda.synchronize()
+        got = call(side)
+        torch.cuda.synchronize()
+        assert torch.equal(got, ref)
+        parts = [p for t in used for p in ((t.codes, t.scales) if type(t) is tea.Mx4Tensor else (t,))]
+        assert {(p.untyped_storage().data_ptr(), side.cuda_stream) for p in parts} == seen
+        seen.clear()

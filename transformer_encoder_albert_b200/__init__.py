@@ -621,22 +621,31 @@ def _mx4_away(dev: int, stream) -> bool:
     return stream is not None or _device_now() != dev
 
 
-def _mx4_on(dev: int, stream):
+def _mx4_on(dev: int, stream, *used):
+    """The device, or the stream; `used`, the call's tensors, may have been allocated on another
+    stream and be dropped before the call has run: their memory stays until it has."""
     torch = _torch or _mx4_torch()
     if stream is None:
         return torch.cuda.device(dev)
     if stream.device.index != dev:
         raise ValueError(f"stream of {stream.device} for tensors on cuda:{dev}")
+    for t in used:
+        if type(t) is Mx4Tensor:
+            for part in (t._codes, t._scales) if t._buf is None else (t._buf,):
+                part.record_stream(stream)
+        elif t is not None:
+            t.record_stream(stream)
     return torch.cuda.stream(stream)
 
 
 def mx4_quantize(x, fmt: str = "mxfp4", tensor_scale: float = 1.0, out: Mx4Tensor | None = None, stream=None) -> Mx4Tensor:
     """Rows of x [rows, cols] (bf16, fp16 or fp32, any row stride) in 4-bit form
-    (albert_mx4_quantize).  Asynchronous; outputs are allocated on the stream used."""
+    (albert_mx4_quantize).  Asynchronous on the current stream, or `stream`: outputs are
+    allocated on it, and the inputs' memory is kept until it has used them."""
     rows, cols, ld, dev = _mx4_rows(x, "x")
     typ = _mx4_type(x.dtype, "x")
     if _mx4_away(dev, stream):
-        with _mx4_on(dev, stream):
+        with _mx4_on(dev, stream, x, out):
             return mx4_quantize(x, fmt, tensor_scale, out)
     if out is None:
         out = mx4_empty(rows, cols, fmt, tensor_scale, x.device)
@@ -656,7 +665,7 @@ def mx4_dequantize(t: Mx4Tensor, dtype=None, out=None, stream=None):
     torch = _torch or _mx4_torch()
     dev = t._dev
     if _mx4_away(dev, stream):
-        with _mx4_on(dev, stream):
+        with _mx4_on(dev, stream, t, out):
             return mx4_dequantize(t, dtype, out)
     rows, cols = t.rows, t.cols
     if out is None:
@@ -680,7 +689,7 @@ def mx4_layer_norm(x, gamma, beta, eps: float = 1e-12, fmt: str = "mxfp4", tenso
     rows, cols, ld, dev = _mx4_rows(x, "x")
     typ = _mx4_type(x.dtype, "x")
     if _mx4_away(dev, stream):
-        with _mx4_on(dev, stream):
+        with _mx4_on(dev, stream, x, gamma, beta):
             return mx4_layer_norm(x, gamma, beta, eps, fmt, tensor_scale, return_rows)
     g, b = _mx4_vector(gamma, cols, "gamma", dev), _mx4_vector(beta, cols, "beta", dev)
     y = _empty((rows, cols), (cols, 1), dtype=x.dtype, device=x.device) if return_rows else None
@@ -712,7 +721,7 @@ def _mx4_linear(x, w: Mx4Tensor, bias, residual, gelu, x_scale, stream, out, dty
                          f"w must be [n >= 1, {k}] on the same device")
     if stream is not None or dev < 0 or _device_now() != dev:
         _mx4_away(dev, stream)
-        with _mx4_on(dev, stream):
+        with _mx4_on(dev, stream, x, w, bias, residual, out):
             return _mx4_linear(x, w, bias, residual, gelu, x_scale, None, out, dtype, q_scale)
     a.w_codes, a.w_scales, a.w_scale = w._cptr, w._sptr, w.tensor_scale
     a.rows, a.n, a.k = rows, n, k
