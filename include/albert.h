@@ -419,8 +419,14 @@ size_t albert_mx4_linear_workspace_bytes(int rows, int k, int fmt);
 
 /* The kernels of albert_mx4_linear bound every wait (2 s); a wait that runs out
  * is recorded in a status word of the current device that all these calls share.
- * This call synchronizes `stream`, returns the word and clears it. */
+ * This call synchronizes `stream`, returns the word and clears it.  (Results of a
+ * call whose wait ran out are undefined.) */
 int albert_mx4_get_status(void *stream);
+
+/* Failure injection for tests of the path above: albert_mx4_linear with a wait limit of
+ * wait_ns (>= 1, else ALBERT_ERR_CONFIG) and the product's loads withheld, so that its
+ * waits run out and the kernel ends with the status recorded. */
+int albert_test_mx4_linear_stall(const albert_mx4_linear_args *args, long long wait_ns, void *stream);
 
 /* ---- single-kernel entry points (parity tests of one kernel) ----
  * These run one kernel of the path in isolation, synchronously, and return its

@@ -167,3 +167,36 @@ def test_inputs_of_a_call_on_another_stream_keep_their_memory(monkeypatch):
         parts = [p for t in used for p in ((t.codes, t.scales) if type(t) is tea.Mx4Tensor else (t,))]
         assert {(p.untyped_storage().data_ptr(), side.cuda_stream) for p in parts} == seen
         seen.clear()
+
+
+# ------------------------------------------------------------- expired waits --
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("rows,n,k", [(5, 300, 768), (5, 256, 200), (20, 2304, 4200), (32, 40000, 512), (64, 300, 768),
+                                      (300, 640, 4200), (5000, 2304, 256)])
+@pytest.mark.parametrize("four_bit", [False, True])
+def test_expired_waits_are_reported_and_later_calls_are_right(rows, n, k, fmt, four_bit):
+    """Withheld loads with a limit of 2 ms: in a cluster and alone, one tile and several per CTA,
+    CTA pairs.  The call returns, the status says so once, the next call is as before."""
+    import ctypes as C
+    x = tea.mx4_quantize(torch.randn(rows, k, device="cuda"), fmt, TS[fmt])
+    w = tea.mx4_quantize(torch.randn(n, k, device="cuda") * 0.05, fmt, 1e-4)
+    good = tea.mx4_linear_quant(x, w, out_scale=TS[fmt]).codes if four_bit else tea.mx4_linear(x, w)
+    assert tea.mx4_status() == 0
+    a = tea.albert_mx4_linear_args()
+    for f, v in dict(a_codes=x.codes.data_ptr(), a_scales=x.scales.data_ptr(), w_codes=w.codes.data_ptr(),
+                     w_scales=w.scales.data_ptr(), x_scale=TS[fmt], w_scale=1e-4, q_scale=TS[fmt], rows=rows, n=n, k=k,
+                     fmt=tea.MX4_FORMATS[fmt]).items():
+        setattr(a, f, v)
+    out, q = torch.empty(rows, n, device="cuda", dtype=torch.bfloat16), tea.mx4_empty(rows, n, fmt, TS[fmt])
+    if four_bit:
+        a.q_codes, a.q_scales = q.codes.data_ptr(), q.scales.data_ptr()
+    else:
+        a.out, a.ld_out = out.data_ptr(), n
+    stream = torch.cuda.current_stream().cuda_stream
+    assert tea.lib().albert_test_mx4_linear_stall(C.byref(a), 0, stream) == 2
+    assert tea.lib().albert_test_mx4_linear_stall(C.byref(a), 2_000_000, stream) == 0
+    assert tea.mx4_status() == 8  # ALBERT_ERR_TIMEOUT
+    assert tea.mx4_status() == 0
+    again = tea.mx4_linear_quant(x, w, out_scale=TS[fmt]).codes if four_bit else tea.mx4_linear(x, w)
+    assert torch.equal(again, good) and tea.mx4_status() == 0

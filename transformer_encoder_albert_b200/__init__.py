@@ -45,6 +45,7 @@ EXPORTS = (
     "albert_test_quant_e4m3", "albert_forward_embedded", "albert_test_attention_groups",
     "albert_mx4_codes_bytes", "albert_mx4_scales_bytes", "albert_mx4_quantize", "albert_mx4_dequantize",
     "albert_mx4_layer_norm", "albert_mx4_linear", "albert_mx4_linear_workspace_bytes", "albert_mx4_get_status",
+    "albert_test_mx4_linear_stall",
 )
 
 
@@ -129,6 +130,7 @@ def lib() -> C.CDLL:
         L.albert_mx4_linear_workspace_bytes.argtypes = [i, i, i]
         L.albert_mx4_linear_workspace_bytes.restype = C.c_size_t
         L.albert_mx4_get_status.argtypes = [vp]
+        L.albert_test_mx4_linear_stall.argtypes = [C.POINTER(albert_mx4_linear_args), ll, vp]
         _lib = L
     return _lib
 

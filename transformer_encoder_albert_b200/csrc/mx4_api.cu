@@ -75,6 +75,89 @@ bool rows_overlap(const void *a, long long la, long long wa, const void *b, long
     return false;
 }
 
+// The linear layer; wait_ns, withhold: as in GemmArgs.
+int linear(const albert_mx4_linear_args *p, void *stream, unsigned long long wait_ns, int withhold) {
+    if (!p) return ALBERT_ERR_NULL;
+    if (!rows_ok(p->rows) || !cols_ok(p->n) || !cols_ok(p->k)) return ALBERT_ERR_SHAPE;
+    if (p->rows == 0) return ALBERT_OK;
+    if (!p->w_codes || !p->w_scales) return ALBERT_ERR_NULL;
+    if (!p->x && (!p->a_codes || !p->a_scales)) return ALBERT_ERR_NULL;
+    if (!p->out && (!p->q_codes || !p->q_scales)) return ALBERT_ERR_NULL;
+    const size_t ws = p->x ? albert_mx4_linear_workspace_bytes(p->rows, p->k, p->fmt) : 0;
+    if (ws && !p->workspace) return ALBERT_ERR_NULL;
+    if (p->x && p->ld_x < p->k) return ALBERT_ERR_SHAPE;
+    if (p->out && p->ld_out < p->n) return ALBERT_ERR_SHAPE;
+    if (p->residual && p->ld_residual < p->n) return ALBERT_ERR_SHAPE;
+    if (!is_format(p->fmt) || (p->x && !is_type(p->x_type)) || ((p->out || p->residual) && !is_type(p->out_type)))
+        return ALBERT_ERR_CONFIG;
+    if (!scale_ok(p->fmt, p->x_scale) || !scale_ok(p->fmt, p->w_scale) || (!p->out && !scale_ok(p->fmt, p->q_scale)))
+        return ALBERT_ERR_CONFIG;
+    if (!aligned(p->w_codes, 16) || !aligned(p->w_scales, 16) || !aligned(p->bias, 4) ||
+        (p->x ? !aligned(p->x, elem_size(p->x_type)) : !aligned(p->a_codes, 16) || !aligned(p->a_scales, 16)) ||
+        (ws && !aligned(p->workspace, 16)) || (p->residual && !aligned(p->residual, elem_size(p->out_type))) ||
+        (p->out ? !aligned(p->out, elem_size(p->out_type)) : !aligned(p->q_codes, 16) || !aligned(p->q_scales, 16)))
+        return ALBERT_ERR_CONFIG;
+    if (p->gelu != 0 && p->gelu != 1) return ALBERT_ERR_CONFIG;
+    if (p->residual && !p->out) return ALBERT_ERR_CONFIG;
+    // (a CTA of the few-row kernel may write its columns while another still reads x)
+    if (p->rows <= kMx4MaxTokens && p->x && p->out) {
+        const long long ex = elem_size(p->x_type), eo = elem_size(p->out_type);
+        if (rows_overlap(p->x, p->ld_x * ex, p->k * ex, p->out, p->ld_out * eo, p->n * eo, p->rows)) return ALBERT_ERR_CONFIG;
+    }
+    // the product of the tensor scales multiplies the fp32 sum: far from fp32's limits
+    if (p->fmt == ALBERT_NVFP4 && !(p->x_scale * p->w_scale >= kMinScale && p->x_scale * p->w_scale <= kMaxScale))
+        return ALBERT_ERR_CONFIG;
+
+    const bool nv = p->fmt == ALBERT_NVFP4;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int sms = 0;
+    int *status = nullptr;
+    cudaError_t e = device_info(sms, status);
+    if (e != cudaSuccess) return ALBERT_ERR_CUDA;
+    Mx4TokArgs g{};
+    g.w = static_cast<const uint8_t *>(p->w_codes);
+    g.w_scales = static_cast<const uint8_t *>(p->w_scales);
+    g.M = p->rows; g.N = p->n; g.K = p->k;
+    g.nv = nv;
+    g.alpha = nv ? p->x_scale * p->w_scale : 1.0f;
+    g.bias = p->bias;
+    g.gelu = p->gelu;
+    g.res = p->residual; g.ld_res = p->ld_residual;
+    g.out = p->out; g.out_type = p->out_type; g.ld_out = p->ld_out;
+    if (!p->out) {
+        g.q = static_cast<uint8_t *>(p->q_codes);
+        g.q_scales = static_cast<uint8_t *>(p->q_scales);
+        g.q_ts = nv ? p->q_scale : 1.0f;
+    }
+    g.status = status;
+    g.wait_ns = wait_ns;
+    g.withhold_loads = withhold;
+    g.a = static_cast<const uint8_t *>(p->a_codes);
+    g.a_scales = static_cast<const uint8_t *>(p->a_scales);
+    if (p->rows <= kMx4MaxTokens) {
+        g.x = p->x;
+        g.x_type = p->x_type;
+        g.ld_x = p->ld_x;
+        g.x_ts = nv ? p->x_scale : 1.0f;
+        g.vec_x = aligned(p->x, 16) && p->ld_x * elem_size(p->x_type) % 16 == 0;
+        return status_of(launch_mx4_tokens(g, sms, s));
+    }
+    if (p->x) {
+        Mx4QuantArgs q{};
+        q.x = p->x; q.type = p->x_type; q.ld = p->ld_x; q.rows = p->rows; q.cols = p->k;
+        q.nv = nv;
+        q.tensor_scale = nv ? p->x_scale : 1.0f;
+        q.codes = static_cast<uint8_t *>(p->workspace);
+        q.scales = q.codes + up16(codes_bytes(p->rows, p->k));
+        // (its grid is resident at once, so the product's CTAs only take SMs it has left)
+        q.trigger = 1;
+        if ((e = launch_mx4_quant(q, s, false)) != cudaSuccess) return ALBERT_ERR_CUDA;
+        g.a = q.codes;
+        g.a_scales = q.scales;
+    }
+    return status_of(launch_mx4_gemm(g, sms, s, p->x != nullptr));
+}
+
 }  // namespace
 
 extern "C" {
@@ -135,84 +218,10 @@ size_t albert_mx4_linear_workspace_bytes(int rows, int k, int fmt) {
     return up16(codes_bytes(rows, k)) + scales_bytes(rows, k, fmt == ALBERT_NVFP4);
 }
 
-int albert_mx4_linear(const albert_mx4_linear_args *p, void *stream) {
-    if (!p) return ALBERT_ERR_NULL;
-    if (!rows_ok(p->rows) || !cols_ok(p->n) || !cols_ok(p->k)) return ALBERT_ERR_SHAPE;
-    if (p->rows == 0) return ALBERT_OK;
-    if (!p->w_codes || !p->w_scales) return ALBERT_ERR_NULL;
-    if (!p->x && (!p->a_codes || !p->a_scales)) return ALBERT_ERR_NULL;
-    if (!p->out && (!p->q_codes || !p->q_scales)) return ALBERT_ERR_NULL;
-    const size_t ws = p->x ? albert_mx4_linear_workspace_bytes(p->rows, p->k, p->fmt) : 0;
-    if (ws && !p->workspace) return ALBERT_ERR_NULL;
-    if (p->x && p->ld_x < p->k) return ALBERT_ERR_SHAPE;
-    if (p->out && p->ld_out < p->n) return ALBERT_ERR_SHAPE;
-    if (p->residual && p->ld_residual < p->n) return ALBERT_ERR_SHAPE;
-    if (!is_format(p->fmt) || (p->x && !is_type(p->x_type)) || ((p->out || p->residual) && !is_type(p->out_type)))
-        return ALBERT_ERR_CONFIG;
-    if (!scale_ok(p->fmt, p->x_scale) || !scale_ok(p->fmt, p->w_scale) || (!p->out && !scale_ok(p->fmt, p->q_scale)))
-        return ALBERT_ERR_CONFIG;
-    if (!aligned(p->w_codes, 16) || !aligned(p->w_scales, 16) || !aligned(p->bias, 4) ||
-        (p->x ? !aligned(p->x, elem_size(p->x_type)) : !aligned(p->a_codes, 16) || !aligned(p->a_scales, 16)) ||
-        (ws && !aligned(p->workspace, 16)) || (p->residual && !aligned(p->residual, elem_size(p->out_type))) ||
-        (p->out ? !aligned(p->out, elem_size(p->out_type)) : !aligned(p->q_codes, 16) || !aligned(p->q_scales, 16)))
-        return ALBERT_ERR_CONFIG;
-    if (p->gelu != 0 && p->gelu != 1) return ALBERT_ERR_CONFIG;
-    if (p->residual && !p->out) return ALBERT_ERR_CONFIG;
-    // (a CTA of the few-row kernel may write its columns while another still reads x)
-    if (p->rows <= kMx4MaxTokens && p->x && p->out) {
-        const long long ex = elem_size(p->x_type), eo = elem_size(p->out_type);
-        if (rows_overlap(p->x, p->ld_x * ex, p->k * ex, p->out, p->ld_out * eo, p->n * eo, p->rows)) return ALBERT_ERR_CONFIG;
-    }
-    // the product of the tensor scales multiplies the fp32 sum: far from fp32's limits
-    if (p->fmt == ALBERT_NVFP4 && !(p->x_scale * p->w_scale >= kMinScale && p->x_scale * p->w_scale <= kMaxScale))
-        return ALBERT_ERR_CONFIG;
+int albert_mx4_linear(const albert_mx4_linear_args *p, void *stream) { return linear(p, stream, 0, 0); }
 
-    const bool nv = p->fmt == ALBERT_NVFP4;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    int sms = 0;
-    int *status = nullptr;
-    cudaError_t e = device_info(sms, status);
-    if (e != cudaSuccess) return ALBERT_ERR_CUDA;
-    Mx4TokArgs g{};
-    g.w = static_cast<const uint8_t *>(p->w_codes);
-    g.w_scales = static_cast<const uint8_t *>(p->w_scales);
-    g.M = p->rows; g.N = p->n; g.K = p->k;
-    g.nv = nv;
-    g.alpha = nv ? p->x_scale * p->w_scale : 1.0f;
-    g.bias = p->bias;
-    g.gelu = p->gelu;
-    g.res = p->residual; g.ld_res = p->ld_residual;
-    g.out = p->out; g.out_type = p->out_type; g.ld_out = p->ld_out;
-    if (!p->out) {
-        g.q = static_cast<uint8_t *>(p->q_codes);
-        g.q_scales = static_cast<uint8_t *>(p->q_scales);
-        g.q_ts = nv ? p->q_scale : 1.0f;
-    }
-    g.status = status;
-    g.a = static_cast<const uint8_t *>(p->a_codes);
-    g.a_scales = static_cast<const uint8_t *>(p->a_scales);
-    if (p->rows <= kMx4MaxTokens) {
-        g.x = p->x;
-        g.x_type = p->x_type;
-        g.ld_x = p->ld_x;
-        g.x_ts = nv ? p->x_scale : 1.0f;
-        g.vec_x = aligned(p->x, 16) && p->ld_x * elem_size(p->x_type) % 16 == 0;
-        return status_of(launch_mx4_tokens(g, sms, s));
-    }
-    if (p->x) {
-        Mx4QuantArgs q{};
-        q.x = p->x; q.type = p->x_type; q.ld = p->ld_x; q.rows = p->rows; q.cols = p->k;
-        q.nv = nv;
-        q.tensor_scale = nv ? p->x_scale : 1.0f;
-        q.codes = static_cast<uint8_t *>(p->workspace);
-        q.scales = q.codes + up16(codes_bytes(p->rows, p->k));
-        // (its grid is resident at once, so the product's CTAs only take SMs it has left)
-        q.trigger = 1;
-        if ((e = launch_mx4_quant(q, s, false)) != cudaSuccess) return ALBERT_ERR_CUDA;
-        g.a = q.codes;
-        g.a_scales = q.scales;
-    }
-    return status_of(launch_mx4_gemm(g, sms, s, p->x != nullptr));
+int albert_test_mx4_linear_stall(const albert_mx4_linear_args *p, long long wait_ns, void *stream) {
+    return wait_ns < 1 ? ALBERT_ERR_CONFIG : linear(p, stream, (unsigned long long)wait_ns, 1);
 }
 
 int albert_mx4_get_status(void *stream) {

@@ -207,9 +207,8 @@ mx4_tokens_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
             const uint64_t once = policy_evict_first();
             int stage = 0, issued = 0;
             uint32_t phase = 0;
-            bool ok = true;
-            for (int kb = kb0; kb < kb1; ++kb) {
-                if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1, abort_flag)) { ok = false; break; }
+            for (int kb = p.withhold_loads ? kb1 : kb0; kb < kb1; ++kb) {
+                if (!mbar_wait(smem_u32(&empty[stage]), phase ^ 1, abort_flag)) break;
                 const uint32_t fb = smem_u32(&full[stage]);
                 mbar_arrive_expect_tx(fb, P::RING);
                 if (stream_w)
@@ -220,11 +219,12 @@ mx4_tokens_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
                 ++issued;
                 if (++stage == ring) { stage = 0; phase ^= 1; }
             }
-            if (!ok)
-                for (int i = 0; i < ring && i < issued; ++i) {
-                    if (--stage < 0) { stage = ring - 1; phase ^= 1; }
-                    mbar_wait_drain(smem_u32(&full[stage]), phase);
-                }
+            // (the last of each slot: a wait that ran out in another warp leaves nobody else to see
+            // them land, and the CTA's memory must outlast them)
+            for (int i = 0; i < ring && i < issued; ++i) {
+                if (--stage < 0) { stage = ring - 1; phase ^= 1; }
+                mbar_wait_drain(smem_u32(&full[stage]), phase);
+            }
         }
         __syncwarp();
     } else if (warp == 1 || warp == 2 + kWorkers) {
@@ -261,8 +261,7 @@ mx4_tokens_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
             }
             if (++stage == (uint32_t)ring) { stage = 0; phase ^= 1; }
         }
-        // (after a wait that ran out, copies of scales may still be in flight: the CTA's memory
-        // must outlast them)
+        // (after a wait that ran out too: what was issued before it must complete)
         umma_commit_elected<false>(leader, smem_u32(done), 0);
     } else {
         // ------------------------------------------------------------ tokens --
@@ -304,8 +303,10 @@ mx4_tokens_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
         }
     }
     // ------------------------------------------------------------- epilogue --
-    // every product has completed, or a wait has run out somewhere in this CTA
+    // Every product has completed, or a wait has run out somewhere in this CTA; then what is in
+    // flight still ends before tensor memory is read or freed and the CTA's memory goes away.
     const bool got = mbar_wait(smem_u32(done), 0, abort_flag);
+    if (!got) mbar_wait_drain(smem_u32(done), 0);
     const bool ok = __syncthreads_and(got && *abort_flag == 0) != 0;
     tc_fence_after();
     if (warp >= 2 && warp < 6) {
