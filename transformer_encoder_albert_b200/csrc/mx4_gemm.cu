@@ -278,7 +278,9 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
                 if (++stage == NST) { stage = 0; phase ^= 1; }
             }
         }
-        if (!ok && rank == 0) {
+        // The last loads of each slot (rank 1's land on rank 0's barriers too): where a wait has run
+        // out in another warp nobody else sees them land, and the CTAs' memory must outlast them.
+        if (rank == 0) {
             for (int i = 0; i < NST && i < issued; ++i) {
                 if (--stage < 0) { stage = NST - 1; phase ^= 1; }
                 mbar_wait_drain(smem_u32(&c.full[stage]), phase);
