@@ -419,8 +419,9 @@ size_t albert_mx4_linear_workspace_bytes(int rows, int k, int fmt);
 
 /* The kernels of albert_mx4_linear bound every wait (2 s); a wait that runs out
  * is recorded in a status word of the current device that all these calls share.
- * This call synchronizes `stream`, returns the word and clears it.  (Results of a
- * call whose wait ran out are undefined.) */
+ * This call synchronizes `stream`, then takes the word and leaves 0, in one step: of
+ * several callers one gets a recorded status.  (Results of a call whose wait ran out
+ * are undefined.) */
 int albert_mx4_get_status(void *stream);
 
 /* Failure injection for tests of the path above: albert_mx4_linear with a wait limit of

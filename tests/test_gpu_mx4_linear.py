@@ -200,3 +200,58 @@ def test_expired_waits_are_reported_and_later_calls_are_right(rows, n, k, fmt, f
     assert tea.mx4_status() == 0
     again = tea.mx4_linear_quant(x, w, out_scale=TS[fmt]).codes if four_bit else tea.mx4_linear(x, w)
     assert torch.equal(again, good) and tea.mx4_status() == 0
+
+
+def test_one_of_several_callers_takes_a_recorded_status():
+    import ctypes as C
+    import threading
+    x, w = (tea.mx4_quantize(torch.randn(n, 256, device="cuda"), "mxfp4") for n in (3, 128))
+    out = torch.empty(3, 128, device="cuda", dtype=torch.bfloat16)
+    a = tea.albert_mx4_linear_args()
+    for f, v in dict(a_codes=x.codes.data_ptr(), a_scales=x.scales.data_ptr(), w_codes=w.codes.data_ptr(),
+                     w_scales=w.scales.data_ptr(), out=out.data_ptr(), ld_out=128, rows=3, n=128, k=256,
+                     fmt=tea.ALBERT_MXFP4).items():
+        setattr(a, f, v)
+    assert tea.mx4_status() == 0
+    streams = [torch.cuda.Stream() for _ in range(8)]
+    for rep in range(5):
+        assert tea.lib().albert_test_mx4_linear_stall(C.byref(a), 1_000_000, torch.cuda.current_stream().cuda_stream) == 0
+        torch.cuda.synchronize()
+        got, start = [], threading.Barrier(8)
+
+        def ask(s):
+            start.wait()
+            got.append(tea.mx4_status(s))
+
+        threads = [threading.Thread(target=ask, args=(s,)) for s in streams]
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+        assert sorted(got) == [0] * 7 + [8]
+
+
+def test_the_first_calls_of_a_process_may_be_captured():
+    """Nothing that the entries look up or set up on their first call keeps it out of a graph."""
+    import subprocess
+    import sys
+    code = """
+import torch, transformer_encoder_albert_b200 as tea
+x, wv = (torch.randn(*s, device="cuda", dtype=torch.bfloat16) for s in ((300, 768), (512, 768)))
+g, b = torch.ones(768, device="cuda"), torch.zeros(768, device="cuda")
+torch.cuda.synchronize()
+def go():
+    w = tea.mx4_quantize(wv, "nvfp4", 0.001)
+    y, y4 = tea.mx4_layer_norm(x, g, b, 1e-5, "nvfp4", 0.01)
+    h = tea.mx4_linear_quant(y4, w, gelu=True, out_scale=0.01)
+    return y, tea.mx4_dequantize(h), tea.mx4_linear(x, w, x_scale=0.01), tea.mx4_linear(x[:3], w, x_scale=0.01)
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    out = go()
+graph.replay()
+torch.cuda.synchronize()
+assert all(torch.equal(o, r) for o, r in zip(out, go())) and tea.mx4_status() == 0
+print("captured")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]

@@ -47,3 +47,23 @@ def test_few_rows_of_x_and_out_that_overlap_are_refused(lib):
     assert CONFIG not in ok, ok
     assert f(P, P + 126, ld_x=200, ld_out=200) == CONFIG                   # its columns, one too many
     assert f(P, P + 128, ld_x=200, ld_out=112) == CONFIG                   # (strides apart: some pair of rows meets)
+
+
+def test_status_is_asked_on_the_streams_device(monkeypatch):
+    import contextlib
+    import types
+
+    import torch
+    log = []
+
+    @contextlib.contextmanager
+    def device(d):
+        log.append(("on", str(d)))
+        yield
+        log.append(("off", str(d)))
+
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(tea, "lib", lambda: types.SimpleNamespace(albert_mx4_get_status=lambda s: log.append(("ask", s)) or 8))
+    stream = types.SimpleNamespace(device=torch.device("cuda", 3), cuda_stream=77)
+    assert tea.mx4_status(stream) == 8
+    assert log == [("on", "cuda:3"), ("ask", 77), ("off", "cuda:3")]

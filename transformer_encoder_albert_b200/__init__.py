@@ -780,6 +780,11 @@ def mx4_linear_quant(x, w: Mx4Tensor, bias=None, gelu: bool = False, x_scale: fl
 
 
 def mx4_status(stream=None) -> int:
-    """Synchronize the stream; status of the 4-bit linear layers run on this device
-    since the last call (ALBERT_OK, or ALBERT_ERR_TIMEOUT after an expired wait)."""
-    return lib().albert_mx4_get_status(_stream_ptr(stream))
+    """Synchronize the stream (default: the current one); status of the 4-bit linear layers
+    run on its device since the last call (ALBERT_OK, or ALBERT_ERR_TIMEOUT after an expired
+    wait)."""
+    if stream is None:
+        return lib().albert_mx4_get_status(_stream_ptr(None))
+    torch = _torch or _mx4_torch()
+    with torch.cuda.device(stream.device):
+        return lib().albert_mx4_get_status(_stream_ptr(stream))

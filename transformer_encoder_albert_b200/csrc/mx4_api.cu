@@ -2,6 +2,7 @@
 // checks of their arguments and their launches.
 #include <atomic>
 #include <cmath>
+#include <mutex>
 
 #include "albert.h"
 #include "mx4.cuh"
@@ -11,8 +12,10 @@ using namespace albert;
 
 namespace {
 
-// Status word of the linear layers' bounded waits, one per device.
-__device__ int g_mx4_status;
+// Status word of the linear layers' bounded waits, one per device, and where a query puts
+// what it has taken from it: in one step, so that no status recorded meanwhile is lost.
+__device__ int g_mx4_status, g_mx4_taken;
+__global__ void take_status() { g_mx4_taken = atomicExch(&g_mx4_status, 0); }
 
 constexpr int kMaxCols = 1 << 24, kMaxRows = 1 << 30;
 constexpr float kMinScale = 7.888609052210118e-31f, kMaxScale = 1.2676506002282294e30f;  // 2^-100, 2^100
@@ -225,11 +228,14 @@ int albert_test_mx4_linear_stall(const albert_mx4_linear_args *p, long long wait
 }
 
 int albert_mx4_get_status(void *stream) {
+    static std::mutex one;  // (queries of one device share the word they are taken to)
     int st = 0;
-    const int zero = 0;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (cudaMemcpyFromSymbolAsync(&st, g_mx4_status, sizeof(int), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
-        cudaMemcpyToSymbolAsync(g_mx4_status, &zero, sizeof(int), 0, cudaMemcpyHostToDevice, s) != cudaSuccess ||
+    if (cudaStreamSynchronize(s) != cudaSuccess) return ALBERT_ERR_CUDA;
+    const std::lock_guard<std::mutex> hold(one);
+    take_status<<<1, 1, 0, s>>>();
+    if (cudaGetLastError() != cudaSuccess ||
+        cudaMemcpyFromSymbolAsync(&st, g_mx4_taken, sizeof(int), 0, cudaMemcpyDeviceToHost, s) != cudaSuccess ||
         cudaStreamSynchronize(s) != cudaSuccess)
         return ALBERT_ERR_CUDA;
     return st;
