@@ -225,3 +225,18 @@ def test_bad_ids_leave_the_output_untouched(w_bf16):
     assert enc.status() == 4
     assert torch.all(out == 7.0)
     enc.close()
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_a_4_bit_handle_takes_less_memory_than_a_bf16_one(w_bf16, fmt):
+    """32768 rows: the FFN activation takes a quarter (4096 -> about 1100 bytes a row), the layer
+    matrices likewise, and nothing stays in bf16 that no forward reads."""
+    taken = {}
+    for dtype in ("bf16", fmt):
+        torch.cuda.synchronize()
+        before = torch.cuda.mem_get_info()[0]
+        enc = tea.Encoder(w_bf16, A, dtype=dtype, max_tokens=32768)
+        torch.cuda.synchronize()
+        taken[dtype] = before - torch.cuda.mem_get_info()[0]
+        enc.close()
+    assert taken[fmt] <= taken["bf16"] - 32768 * 2400

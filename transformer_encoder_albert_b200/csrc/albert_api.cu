@@ -9,6 +9,7 @@
 //   -> GEMM 768->512 scattered to [B, T, 512] -> zero padding rows.
 // The shared layer's weights exist once in device memory and every execution
 // reads the same copy, which stays resident in L2 across executions.
+#include <algorithm>
 #include <cmath>
 #include <cstdio>
 #include <cstdlib>
@@ -682,17 +683,21 @@ int create_impl(albert_handle *h, const albert_weights *w) {
     const size_t n_w1 = (size_t)kFfn * kHidden, n_w2 = (size_t)kHidden * kFfn, n_out = O * kHidden;
     auto al = [](size_t b) { return (b + 255) / 256 * 256; };
     const size_t group_bytes = al(n_qkv * eb) + al(n_wo * eb) + al(n_w1 * eb) + al(n_w2 * eb);
-    const size_t off_groups = al(n_win * eb), off_out = off_groups + G * group_bytes;
+    // (ALBERT_MXFP4 / ALBERT_NVFP4: the layer matrices in a block of their own, which goes once
+    // their 4-bit copies are made)
+    const size_t off_groups = al(n_win * eb), off_out = off_groups + (f4 ? 0 : G * group_bytes);
     h->wblock_bytes = off_out + al(n_out * eb);
     if ((rc = dev_alloc(h, &h->wblock, h->wblock_bytes))) return rc;
     uint8_t *wb = static_cast<uint8_t *>(h->wblock);
     h->w_in = wb;
     h->w_out = wb + off_out;
+    void *layer_block = wb + off_groups;
+    if (f4 && (rc = dev_alloc(h, &layer_block, G * group_bytes))) return rc;
     if ((rc = copy_matrix(h, h->w_in, w->w_in, n_win, s))) return rc;
     if (O && (rc = copy_matrix(h, h->w_out, w->w_out, n_out, s))) return rc;
     for (size_t g = 0; g < G; ++g) {
         auto &gp = h->grp[g];
-        uint8_t *gb = wb + off_groups + g * group_bytes;
+        uint8_t *gb = static_cast<uint8_t *>(layer_block) + g * group_bytes;
         gp.wqkv = gb;
         gp.wo = gb + al(n_qkv * eb);
         gp.w1 = static_cast<uint8_t *>(gp.wo) + al(n_wo * eb);
@@ -711,7 +716,7 @@ int create_impl(albert_handle *h, const albert_weights *w) {
     if ((rc = dev_alloc(h, &h->QKV, R * kQKV * eb))) return rc;
     if ((rc = dev_alloc(h, &h->C, R * kHidden * eb))) return rc;
     if ((rc = dev_alloc(h, &h->X1, R * kHidden * eb))) return rc;
-    if ((rc = dev_alloc(h, &h->H, R * kFfn * eb))) return rc;
+    if (!f4 && (rc = dev_alloc(h, &h->H, R * kFfn * eb))) return rc;  // (4 bits: mH)
     if ((rc = dev_alloc(h, &h->Z, R * kHidden * eb))) return rc;
     if (f4) {
         const bool nv = c.dtype == ALBERT_NVFP4;
@@ -758,7 +763,11 @@ int create_impl(albert_handle *h, const albert_weights *w) {
                 q.scales = m.m->scales;
                 TRY(launch_mx4_quant(q, s, false));
             }
+            gp.wqkv = gp.wo = gp.w1 = gp.w2 = nullptr;
         }
+        TRY(cudaStreamSynchronize(s));
+        h->allocs.erase(std::find(h->allocs.begin(), h->allocs.end(), layer_block));
+        TRY(cudaFree(layer_block));
     }
     if (bf && !f4) {
         const size_t nst = R * gemm::LN_PARTS;
@@ -834,6 +843,7 @@ int create_impl(albert_handle *h, const albert_weights *w) {
     if (c.out_layout == 1 && (rc = dev_alloc(h, &h->tout, (size_t)c.max_tokens * out_width(h) * eb))) return rc;
     // Deterministic contents for rows a forward never writes.
     for (void *p : {h->E, h->X, h->QKV, h->C, h->X1, h->H, h->Z}) {
+        if (!p) continue;
         size_t bytes = (p == h->E ? kEmb : p == h->QKV ? kQKV : p == h->H ? kFfn : kHidden) * R * eb;
         TRY(cudaMemsetAsync(p, 0, bytes, s));
     }
@@ -843,19 +853,19 @@ int create_impl(albert_handle *h, const albert_weights *w) {
     if (bf) {
         if (make_tmap_bf16(&h->tm_E, h->E, R, kEmb, gemm::BM) || make_tmap_bf16(&h->tm_X, h->X, R, kHidden, gemm::BM) ||
             make_tmap_bf16(&h->tm_C, h->C, R, kHidden, gemm::BM) || make_tmap_bf16(&h->tm_X1, h->X1, R, kHidden, gemm::BM) ||
-            make_tmap_bf16(&h->tm_H, h->H, R, kFfn, gemm::BM) || make_tmap_bf16(&h->tm_Z, h->Z, R, kHidden, gemm::BM) ||
+            (!f4 && make_tmap_bf16(&h->tm_H, h->H, R, kFfn, gemm::BM)) || make_tmap_bf16(&h->tm_Z, h->Z, R, kHidden, gemm::BM) ||
             make_tmap_bf16(&h->tm_QKV, h->QKV, R, kQKV, 128) || make_tmap_bf16(&h->tm_QKV64, h->QKV, R, kQKV, 64) ||
             make_tmap_bf16(&h->tm_win, h->w_in, kHidden, kEmb, gemm::B_BOX) ||
             (O && make_tmap_bf16(&h->tm_wout, h->w_out, O, kHidden, gemm::B_BOX)) ||
             make_tmap_bf16_tile32(&h->t32_X, h->X, R, kHidden) || make_tmap_bf16_tile32(&h->t32_QKV, h->QKV, R, kQKV) ||
-            make_tmap_bf16_tile32(&h->t32_X1, h->X1, R, kHidden) || make_tmap_bf16_tile32(&h->t32_H, h->H, R, kFfn) ||
+            make_tmap_bf16_tile32(&h->t32_X1, h->X1, R, kHidden) || (!f4 && make_tmap_bf16_tile32(&h->t32_H, h->H, R, kFfn)) ||
             make_tmap_bf16_tile32(&h->t32_Z, h->Z, R, kHidden))
             return ALBERT_ERR_CUDA;
         for (auto &gp : h->grp)
-            if (make_tmap_bf16(&gp.tm_wqkv, gp.wqkv, kQKV, kHidden, gemm::B_BOX) ||
+            if (!f4 && (make_tmap_bf16(&gp.tm_wqkv, gp.wqkv, kQKV, kHidden, gemm::B_BOX) ||
                 make_tmap_bf16(&gp.tm_wo, gp.wo, kHidden, kHidden, gemm::B_BOX) ||
                 make_tmap_bf16(&gp.tm_w1, gp.w1, kFfn, kHidden, gemm::B_BOX) ||
-                make_tmap_bf16(&gp.tm_w2, gp.w2, kHidden, kFfn, gemm::B_BOX))
+                make_tmap_bf16(&gp.tm_w2, gp.w2, kHidden, kFfn, gemm::B_BOX)))
                 return ALBERT_ERR_CUDA;
         if (f8) {
             if (make_tmap_e4m3(&h->tq_A768, h->qA, R, kHidden, gemm::BM) ||
