@@ -240,3 +240,51 @@ def test_a_4_bit_handle_takes_less_memory_than_a_bf16_one(w_bf16, fmt):
         taken[dtype] = before - torch.cuda.mem_get_info()[0]
         enc.close()
     assert taken[fmt] <= taken["bf16"] - 32768 * 2400
+
+
+def _rows_of_one_layer(w, fmt, x, act):
+    """A layer without attention (w["wo"] = 0) out of the operators of their own, from its bf16
+    input rows: what the handle's kernels must give bit for bit."""
+    cu = lambda k: torch.tensor(np.asarray(w[k], np.float32)).cuda()  # noqa: E731
+
+    def mat(k):
+        m = np.asarray(w[k], np.float32)
+        ts = float(np.float32(np.abs(m).max()) / np.float32(6 * 448)) if fmt == "nvfp4" else 1.0
+        return tea.mx4_quantize(torch.tensor(m).cuda(), fmt, ts if ts >= 1e-30 else 1.0)
+
+    a = act if fmt == "nvfp4" else 1.0
+    z = tea.mx4_linear(x, mat("wo"), cu("bo"), residual=x, x_scale=a)
+    x1, x4 = tea.mx4_layer_norm(z, cu("ln1_g"), cu("ln1_b"), A["ln_eps"], fmt, a)
+    h = tea.mx4_linear_quant(x4, mat("w1"), cu("b1"), gelu=True, out_scale=a)
+    z = tea.mx4_linear(h, mat("w2"), cu("b2"), residual=x1)
+    return tea.mx4_layer_norm(z, cu("ln2_g"), cu("ln2_b"), A["ln_eps"], fmt, a)[0]
+
+
+def _without_attention(w, seed):
+    rng = np.random.default_rng(seed)
+    w = dict(w)
+    w["wo"] = np.zeros_like(w["wo"])
+    for k in ("bo", "b1", "b2", "ln1_b", "ln2_b"):
+        w[k] = rng.normal(0, 0.3, w[k].shape).astype(np.float32)
+    for k in ("ln1_g", "ln2_g"):
+        w[k] = (1 + rng.normal(0, 0.2, w[k].shape)).astype(np.float32)
+    return w
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("lengths", [(128, 128, 128, 128, 128), (64,), (1, 100, 37, 512, 260)])
+def test_a_layer_is_its_operators_bit_for_bit(w_bf16, fmt, lengths):
+    """The handle's LayerNorms, products, GELU and residuals against the operators' own entries on
+    the same rows: equal, so that no scale, code or bias is anywhere else than there."""
+    rng = np.random.default_rng(len(lengths))
+    w = _without_attention(w_bf16, 3)
+    rows = sum(lengths)
+    E = torch.tensor(rng.normal(0, 1, (rows, 128)).astype(np.float32)).cuda()
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lengths)]).astype(np.int32)).cuda()
+    got = {}
+    for n_exec in (0, 1):
+        enc = tea.Encoder(w, A, dtype=fmt, max_tokens=rows, n_exec=n_exec, out_dim=0)
+        got[n_exec] = enc.forward_embedded(E, cu, max(lengths))
+        assert enc.status() == 0
+        enc.close()
+    assert torch.equal(got[1], _rows_of_one_layer(w, fmt, got[0], ACT))
