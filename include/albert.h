@@ -68,8 +68,9 @@ extern "C" {
 /* Microscaled 4-bit formats (albert_mx4_quantize); as the precision of a handle:
    the four layer GEMMs on 4-bit operands (weights quantized at creation, the
    activations in each forward), LayerNorms in fp32 from bf16 rows, everything
-   else as ALBERT_BF16.  ALBERT_NVFP4's activations have the tensor scale 1/32
-   (magnitudes up to 84). */
+   else as ALBERT_BF16.  ALBERT_NVFP4's activations have the tensor scale 1/32:
+   magnitudes above 6 * 448 / 32 = 84 saturate.  Where a model's go further (the FFN's
+   inner activation may), albert_set_activation_scale gives another. */
 #define ALBERT_MXFP4 3 /* E2M1 values, blocks of 32, power-of-two scales (E8M0)  */
 #define ALBERT_NVFP4 4 /* E2M1 values, blocks of 16, E4M3 scales times one fp32
                           factor per tensor                                      */
@@ -233,6 +234,12 @@ void albert_destroy(albert_handle *h);
  * ns < 0 returns ALBERT_ERR_CONFIG.  A limit shorter than a kernel's normal
  * waits makes healthy forwards fail with ALBERT_ERR_TIMEOUT. */
 int albert_set_wait_limit(albert_handle *h, long long ns);
+
+/* Tensor scale of the activations of an ALBERT_NVFP4 handle on later forwards (a captured
+ * forward keeps the one it was captured with): magnitudes up to 2688 * scale are represented,
+ * larger ones saturate.  2^-20 <= scale <= 2^20; 1/32 after creation.  ALBERT_ERR_CONFIG
+ * outside, and for handles of another dtype. */
+int albert_set_activation_scale(albert_handle *h, float scale);
 
 /* Failure injection for tests of the path above: on later forwards, the
  * launches of the kernel classes set in class_mask (bit i = class i of

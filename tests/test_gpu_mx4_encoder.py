@@ -243,8 +243,8 @@ def test_a_4_bit_handle_takes_less_memory_than_a_bf16_one(w_bf16, fmt):
 
 
 def _rows_of_one_layer(w, fmt, x, act):
-    """A layer without attention (w["wo"] = 0) out of the operators of their own, from its bf16
-    input rows: what the handle's kernels must give bit for bit."""
+    """A layer without attention (w["wo"] = 0) out of the operators by themselves, from its
+    bf16 input rows: what the handle's kernels must give bit for bit; and its inner activation."""
     cu = lambda k: torch.tensor(np.asarray(w[k], np.float32)).cuda()  # noqa: E731
 
     def mat(k):
@@ -257,7 +257,7 @@ def _rows_of_one_layer(w, fmt, x, act):
     x1, x4 = tea.mx4_layer_norm(z, cu("ln1_g"), cu("ln1_b"), A["ln_eps"], fmt, a)
     h = tea.mx4_linear_quant(x4, mat("w1"), cu("b1"), gelu=True, out_scale=a)
     z = tea.mx4_linear(h, mat("w2"), cu("b2"), residual=x1)
-    return tea.mx4_layer_norm(z, cu("ln2_g"), cu("ln2_b"), A["ln_eps"], fmt, a)[0]
+    return tea.mx4_layer_norm(z, cu("ln2_g"), cu("ln2_b"), A["ln_eps"], fmt, a)[0], h
 
 
 def _without_attention(w, seed):
@@ -287,4 +287,33 @@ def test_a_layer_is_its_operators_bit_for_bit(w_bf16, fmt, lengths):
         got[n_exec] = enc.forward_embedded(E, cu, max(lengths))
         assert enc.status() == 0
         enc.close()
-    assert torch.equal(got[1], _rows_of_one_layer(w, fmt, got[0], ACT))
+    assert torch.equal(got[1], _rows_of_one_layer(w, fmt, got[0], ACT)[0])
+
+
+def test_the_activation_scale_of_an_nvfp4_encoder(w_bf16):
+    """An FFN activation of about 300 (within the eighth and the sixteenth of E2M1's and the scale's
+    half steps): cut off at 84 with the scale 1/32, kept with 1/4.  With each scale the layer is its
+    operators with that scale."""
+    w = _without_attention(w_bf16, 4)
+    w["b1"] = w["b1"] + np.where(np.arange(w["b1"].size) % 7 == 0, 300, 0).astype(np.float32)
+    E = torch.tensor(np.random.default_rng(6).normal(0, 1, (200, 128)).astype(np.float32)).cuda()
+    cu = torch.tensor([0, 200], dtype=torch.int32, device="cuda")
+    enc = tea.Encoder(w, A, dtype="nvfp4", max_tokens=200, n_exec=0, out_dim=0)
+    x = enc.forward_embedded(E, cu, 200)
+    enc.close()
+    enc = tea.Encoder(w, A, dtype="nvfp4", max_tokens=200, n_exec=1, out_dim=0)
+    for scale in (ACT, 0.25, ACT):
+        enc.set_activation_scale(scale)
+        y = enc.forward_embedded(E, cu, 200)
+        out, h = _rows_of_one_layer(w, "nvfp4", x, scale)
+        assert enc.status() == 0 and torch.equal(y, out)
+        top = float(tea.mx4_dequantize(h, dtype=torch.float32).abs().max())
+        assert top == 84 if scale == ACT else 250 < top < 350
+    for bad in (0.0, -1.0, float("nan"), float("inf"), 2.0 ** -21, 2.0 ** 21):
+        with pytest.raises(tea.AlbertError):
+            enc.set_activation_scale(bad)
+    enc.close()
+    enc = tea.Encoder(w, A, dtype="mxfp4", max_tokens=64)
+    with pytest.raises(tea.AlbertError):
+        enc.set_activation_scale(0.25)
+    enc.close()

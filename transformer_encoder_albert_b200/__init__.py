@@ -45,7 +45,7 @@ EXPORTS = (
     "albert_test_quant_e4m3", "albert_forward_embedded", "albert_test_attention_groups",
     "albert_mx4_codes_bytes", "albert_mx4_scales_bytes", "albert_mx4_quantize", "albert_mx4_dequantize",
     "albert_mx4_layer_norm", "albert_mx4_linear", "albert_mx4_linear_workspace_bytes", "albert_mx4_get_status",
-    "albert_test_mx4_linear_stall",
+    "albert_test_mx4_linear_stall", "albert_set_activation_scale",
 )
 
 
@@ -113,6 +113,7 @@ def lib() -> C.CDLL:
         L.albert_length_regulate_scratch_bytes.restype = C.c_size_t
         L.albert_set_wait_limit.argtypes = [vp, C.c_longlong]
         L.albert_test_stall.argtypes = [vp, i]
+        L.albert_set_activation_scale.argtypes = [vp, C.c_float]
         L.albert_set_small_batch_kernel.argtypes = [vp, i]
         L.albert_last_forward_launches.argtypes = [vp]
         L.albert_test_quant_e4m3.argtypes = [vp, i, i, vp, vp, vp]
@@ -306,6 +307,11 @@ class Encoder:
     def set_wait_limit(self, ns: int) -> None:
         """Limit (ns) of the kernels' bounded waits on later forwards; 0 = default (2 s)."""
         _check(lib().albert_set_wait_limit(self.h, int(ns)), "albert_set_wait_limit")
+
+    def set_activation_scale(self, scale: float) -> None:
+        """Tensor scale of the activations of an "nvfp4" encoder on later forwards (1/32 at
+        first): magnitudes above 2688 * scale saturate."""
+        _check(lib().albert_set_activation_scale(self.h, float(scale)), "albert_set_activation_scale")
 
     def test_stall(self, classes=()) -> None:
         """Failure injection: the GEMM launches of these kernel classes withhold

@@ -38,9 +38,10 @@ const char *kProfNames[kProfClasses] = {
 
 constexpr int kEventPool = 16384;
 
-// ALBERT_NVFP4: tensor scale of every activation.  A block's E4M3 scale then reaches
-// magnitudes up to 6 * 448 / 32 = 84 and keeps its four bits down to a largest
-// magnitude of 6 * 2^-6 / 32 = 0.003; LayerNorm outputs stay below sqrt(768) = 28.
+// ALBERT_NVFP4: tensor scale of every activation unless albert_set_activation_scale gives
+// another.  A block's E4M3 scale then reaches magnitudes up to 6 * 448 / 32 = 84 and keeps its
+// four bits down to a largest magnitude of 6 * 2^-6 / 32 = 0.003; LayerNorm outputs stay below
+// sqrt(768) = 28 times the largest gamma, the FFN's inner activation has no such bound.
 constexpr float kMx4ActScale = 0.03125f;
 
 }  // namespace
@@ -113,6 +114,7 @@ struct albert_handle {
     // ALBERT_MXFP4 / ALBERT_NVFP4: the 4-bit layer input or attention output [rows, 768] and
     // the 4-bit FFN activation [rows, 2048]
     uint8_t *mA = nullptr, *mA_scales = nullptr, *mH = nullptr, *mH_scales = nullptr;
+    float act_scale = kMx4ActScale;
 
     // host-buffer staging
     int64_t *st_ids = nullptr;
@@ -333,7 +335,7 @@ GemmF32Args f32_args(albert_handle *h, const void *A, const void *W, const float
 int run_layers_mx4(albert_handle *h, Launch &L, int nseq, int max_len, long long row_bound) {
     const albert_config &c = h->cfg;
     const bool nv = c.dtype == ALBERT_NVFP4;
-    const float ats = nv ? kMx4ActScale : 1.0f;
+    const float ats = nv ? h->act_scale : 1.0f;
     const int M = row_bound < h->rows_cap ? (int)row_bound : h->rows_cap;
     auto rows = [&](const void *x) {
         Mx4QuantArgs q{};
@@ -1164,6 +1166,14 @@ int albert_set_wait_limit(albert_handle *h, long long ns) {
     if (!h) return ALBERT_ERR_NULL;
     if (ns < 0) return ALBERT_ERR_CONFIG;
     h->wait_ns = (unsigned long long)ns;
+    return ALBERT_OK;
+}
+
+int albert_set_activation_scale(albert_handle *h, float scale) {
+    if (!h) return ALBERT_ERR_NULL;
+    // (1/2^20 .. 2^20: its product with a matrix's tensor scale stays far from fp32's limits)
+    if (h->cfg.dtype != ALBERT_NVFP4 || !(scale >= 9.5367431640625e-07f && scale <= 1048576.0f)) return ALBERT_ERR_CONFIG;
+    h->act_scale = scale;
     return ALBERT_OK;
 }
 
