@@ -60,6 +60,55 @@ def test_far_values_do_not_set_a_blocks_scale(rows, fmt):
     assert np.all(byte[:, -1] == 0)
 
 
+# ----------------------------------------------------------------- residuals --
+
+RES = [(5, 200, 100), (24, 1000, 768), (40, 1001, 300), (300, 512, 256), (2600, 2020, 288)]
+
+
+def _residual_case(rng, rows, n, k, dtype, fmt):
+    """x, w and the residual with the 64-bit result, and how far fp32 sums and the rounding to
+    dtype may be from it: every one of K + 3 additions off by 2^-23 of a partial sum, the residual's
+    by 2^-23 of the result, half a step of dtype (and of fp16's smallest subnormal)."""
+    x = torch.tensor(rng.normal(0, 1, (rows, k)).astype(np.float32)).to(torch.bfloat16)
+    wv = rng.normal(0, 0.05, (n, k)).astype(np.float32)
+    res = torch.tensor(rng.normal(0, 1, (rows, n)).astype(np.float32)).to(DTYPES[dtype])
+    wts = 1e-4 if fmt == "nvfp4" else 1.0
+    a, w = mq.rounded(x.float().numpy(), fmt, TS[fmt]), mq.rounded(wv, fmt, wts)
+    ref = a @ w.T + res.double().numpy()
+    tol = (k + 3) * 2.0 ** -23 * (np.abs(a) @ np.abs(w).T) + 2.0 ** -23 * np.abs(ref)
+    half = torch.finfo(DTYPES[dtype]).eps / 2
+    tol = tol + half * (np.abs(ref) + tol) + (2.0 ** -25 if dtype == "fp16" else 0)
+    return x.cuda(), tea.mx4_quantize(torch.tensor(wv).cuda(), fmt, wts), res.cuda(), ref, tol
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("rows,n,k", RES)
+def test_residuals_of_every_type_in_place_and_at_any_offset(rows, n, k, dtype, fmt):
+    rng = np.random.default_rng(rows + n + k)
+    x, w, res, ref, tol = _residual_case(rng, rows, n, k, dtype, fmt)
+    want = tea.mx4_linear(x, w, residual=res, dtype=DTYPES[dtype], x_scale=TS[fmt])
+    err = np.abs(_np(want) - ref)
+    assert np.all(err <= tol), float((err - tol).max())
+    same = res.clone()
+    tea.mx4_linear(x, w, residual=same, out=same, x_scale=TS[fmt])
+    assert torch.equal(same, want)
+    # rows 16-byte aligned or not, the residual's and the result's apart; nothing beside them
+    for off_r, pad_r, off_o, pad_o in ((8, 16 - n % 8, 0, 24 - n % 8), (1, 3, 8, 16 - n % 8), (8, 8 - n % 8, 3, 5), (1, 1, 1, 2)):
+        rb = torch.full((rows * (n + pad_r) + 16,), float("nan"), device="cuda", dtype=DTYPES[dtype])
+        rv = rb[off_r:off_r + rows * (n + pad_r)].view(rows, n + pad_r)[:, :n]
+        rv.copy_(res)
+        ob = torch.full((rows * (n + pad_o) + 16,), 7.0, device="cuda", dtype=DTYPES[dtype])
+        ov = ob[off_o:off_o + rows * (n + pad_o)].view(rows, n + pad_o)[:, :n]
+        tea.mx4_linear(x, w, residual=rv, out=ov, x_scale=TS[fmt])
+        assert torch.equal(ov, want)
+        ov.fill_(7.0)
+        assert torch.all(ob == 7.0)
+        tea.mx4_linear(x, w, residual=rv, out=rv, x_scale=TS[fmt])
+        assert torch.equal(rv, want)
+    assert tea.mx4_status() == 0
+
+
 # -------------------------------------------------------- what a call writes --
 
 def _tensor(rows, cols, fmt):
@@ -112,6 +161,25 @@ def test_a_4_bit_result_writes_whole_scale_tiles(rows, n, k, fmt):
     _check_past_rows(q, cb, sb)
     ref = tea.mx4_linear_quant(x, w, out_scale=TS[fmt])
     assert torch.equal(q.codes, ref.codes) and torch.equal(q.scales, ref.scales)
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("rows", [1, 30, 40, 300, 5000])
+def test_a_result_leaves_the_columns_beside_it_alone(rows, dtype):
+    """Results of every width modulo 8 in 16-byte aligned rows of a wider buffer."""
+    x = torch.randn(rows, 300, device="cuda", dtype=torch.bfloat16)
+    for n in (1, 33, 200, 1001, 1002, 1003, 1004, 1005, 1006, 1007, 1008):
+        w = tea.mx4_quantize(torch.randn(n, 300, device="cuda"), "mxfp4")
+        ld = -(-n // 8) * 8 + 16
+        ref = tea.mx4_linear(x, w, dtype=DTYPES[dtype])
+        buf = torch.full((rows, ld), 7.0, device="cuda", dtype=DTYPES[dtype])
+        tea.mx4_linear(x, w, out=buf[:, :n])
+        assert torch.equal(buf[:, :n], ref) and torch.all(buf[:, n:] == 7.0), n
+        res = torch.full((rows, ld), float("nan"), device="cuda", dtype=DTYPES[dtype])
+        res[:, :n] = 0
+        buf[:, :n] = 0
+        tea.mx4_linear(x, w, residual=res[:, :n], out=buf[:, :n])
+        assert torch.equal(buf[:, :n], ref) and torch.all(buf[:, n:] == 7.0), n
 
 
 @pytest.mark.parametrize("fmt", FMTS)

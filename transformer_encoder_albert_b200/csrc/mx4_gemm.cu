@@ -605,8 +605,9 @@ mx4_gemm_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__
 #pragma unroll
                         for (int q = 0; q < 4; ++q)
                             st_shared_u4(tile + stg_off(lane, q), make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]));
-                        // by TMA unless rows past the last one would be written
-                        if (tma_out && (row0 + 32 <= n_rows || n_rows == p.M)) {
+                        // by TMA unless rows past the last one would be written, or columns: a store's
+                        // end is cut off at 16 bytes, and what lies between is written as 0
+                        if (tma_out && (row0 + 32 <= n_rows || n_rows == p.M) && (left >= 32 || tma_out > 1)) {
                             fence_proxy_async_smem();
                             __syncwarp();
                             tma_store_if(lane == 0 && left > 0 && row0 < n_rows, &tmOut, tile, col0, row0);
@@ -669,7 +670,9 @@ cudaError_t launch_tile(const Mx4GemmArgs &a, int num_sms, cudaStream_t s, bool 
     const int es = a.out_type == kElemF32 ? 4 : 2;
     auto ok16 = [&](const void *q, long long ld) { return q && (reinterpret_cast<uintptr_t>(q) & 15) == 0 && ld * es % 16 == 0; };
     CUtensorMap tmOut = tmA, tmRes = tmA;
-    const int tma_res = ok16(a.res, a.ld_res) && a.out_type != kElemF32, tma_out = ok16(a.out, a.ld_out) && a.out_type != kElemF32;
+    const int tma_res = ok16(a.res, a.ld_res) && a.out_type != kElemF32;
+    // (2: a row's end is a multiple of 16 bytes too)
+    const int tma_out = ok16(a.out, a.ld_out) && a.out_type != kElemF32 ? (a.N % 8 == 0 ? 2 : 1) : 0;
     if ((tma_out && make_tmap_tile16(&tmOut, a.out, a.out_type, a.M, a.N, a.ld_out)) ||
         (tma_res && make_tmap_tile16(&tmRes, a.res, a.out_type, a.M, a.N, a.ld_res)))
         return cudaErrorInvalidValue;
