@@ -49,13 +49,6 @@ __device__ __forceinline__ uint32_t cvt_e2m1x8(const float (&v)[8]) {
     return r;
 }
 
-// E2M1 code -> value: sign, 2 exponent bits (bias 1), 1 mantissa bit.
-__device__ __forceinline__ float e2m1_value(uint32_t c) {
-    const uint32_t e = (c >> 1) & 3u, m = c & 1u;
-    const float mag = e == 0 ? 0.5f * m : (1.0f + 0.5f * m) * (float)(1u << (e - 1));
-    return (c & 8u) ? -mag : mag;
-}
-
 __device__ __forceinline__ float e8m0_value(uint32_t byte) {
     // 2^(byte - 127): byte 0 is below fp32's normals, byte 255 is NaN
     return __uint_as_float(byte == 0 ? 0x00400000u : byte == 255u ? 0x7fffffffu : byte << 23);
@@ -119,11 +112,6 @@ __device__ __forceinline__ Mx4Scale mx4_block_scale(uint32_t amax_bits, const Mx
     return s;
 }
 
-template <typename T>
-__device__ __forceinline__ float to_f32(T x) {
-    if constexpr (sizeof(T) == 4) return x;
-    else return static_cast<float>(x);
-}
 template <typename T>
 __device__ __forceinline__ T from_f32(float x) {
     if constexpr (sizeof(T) == 4) return x;
