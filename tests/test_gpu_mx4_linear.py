@@ -323,3 +323,31 @@ print("captured")
 """
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
+
+
+def test_offsets_past_32_bits():
+    """1,100,000 rows of 2048: more than 2^31 values in, out and between; the last rows are those of
+    the same rows alone."""
+    rows, k = 1_100_000, 2048
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.empty(rows, k, device="cuda", dtype=torch.bfloat16).normal_(generator=g)
+    w = tea.mx4_quantize(torch.randn(k, k, device="cuda", generator=g) * 0.02, "mxfp4")
+    part = slice(rows - 300, rows)
+    q, alone = tea.mx4_quantize(x, "mxfp4"), tea.mx4_quantize(x[part], "mxfp4")
+    assert torch.equal(q.codes[part], alone.codes)
+    back = tea.mx4_dequantize(q)
+    assert torch.equal(back[part], tea.mx4_dequantize(alone))
+    del back
+    y = tea.mx4_linear(q, w)
+    assert torch.equal(y[part], tea.mx4_linear(alone, w))
+    r = tea.mx4_linear(x, w, residual=y, out=y)
+    assert torch.equal(r[part], tea.mx4_linear(alone, w, residual=tea.mx4_linear(alone, w)))
+    del y, r
+    gamma, beta = torch.ones(k, device="cuda"), torch.zeros(k, device="cuda")
+    n, n4 = tea.mx4_layer_norm(x, gamma, beta, 1e-5)
+    m, m4 = tea.mx4_layer_norm(x[part], gamma, beta, 1e-5)
+    assert torch.equal(n[part], m) and torch.equal(n4.codes[part], m4.codes)
+    del n
+    u = tea.mx4_linear_quant(n4, w, gelu=True)
+    assert torch.equal(u.codes[part], tea.mx4_linear_quant(m4, w, gelu=True).codes)
+    assert tea.mx4_status() == 0

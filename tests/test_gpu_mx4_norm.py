@@ -95,3 +95,38 @@ def test_rows_of_one_value_give_beta(rows, cols, dtype):
     tol = np.abs(g) * (D + 2) ** 2 * U * U * c.double().abs().numpy()[:, None] / 1e-6 + 2 * U * np.abs(b)
     half = torch.finfo(DTYPES[dtype]).eps / 2
     assert np.all(np.abs(y.double().cpu().numpy() - b) <= tol + half * (np.abs(b) + tol) + (2.0 ** -25 if dtype == "fp16" else 0))
+
+
+@pytest.mark.parametrize("dtype", list(DTYPES))
+@pytest.mark.parametrize("rows,cols", SHAPES)
+def test_normalized_rows_at_any_offset_of_a_wider_buffer(rows, cols, dtype):
+    """y by its C entry in rows of every alignment (gamma, beta too): the same values whatever the
+    kernel's way of moving them allows, nothing beside them, and x's own rows as y."""
+    rng = np.random.default_rng(cols + 1)
+    t = torch.tensor(rng.normal(0, 3, (rows, cols)).astype(np.float32)).to(DTYPES[dtype]).cuda()
+    g, b, tg, tb = _inputs(rng, cols)
+    typ = {"bf16": tea.ALBERT_BF16, "fp16": tea.ALBERT_FP16, "fp32": tea.ALBERT_FP32}[dtype]
+    ref, q = tea.mx4_layer_norm(t, tg, tb, 1e-5, "mxfp4")
+    params = torch.zeros(2, cols + 8, device="cuda")
+    half = torch.finfo(DTYPES[dtype]).eps / 2
+    for off, ld, shift in ((0, -(-cols // 16) * 16 + 16, 0), (8, -(-cols // 8) * 8 + 8, 4), (1, cols + 2, 1), (3, cols + 5, 3)):
+        buf = torch.full((rows * ld + 16,), 7.0, device="cuda", dtype=DTYPES[dtype])
+        y = buf[off:off + rows * ld].view(rows, ld)[:, :cols]
+        pg, pb = params[0, shift:shift + cols], params[1, shift:shift + cols]
+        pg.copy_(tg)
+        pb.copy_(tb)
+        for x in (t, y):
+            if x is y:
+                y.copy_(t)
+            rc = tea.lib().albert_mx4_layer_norm(x.data_ptr(), typ, cols if x is t else ld, pg.data_ptr(), pb.data_ptr(), 1e-5,
+                                                 rows, cols, tea.ALBERT_MXFP4, 1.0, y.data_ptr(), ld, q.codes.data_ptr(),
+                                                 q.scales.data_ptr(), torch.cuda.current_stream().cuda_stream)
+            assert rc == 0
+            # (two kernels may sum in another order: twice the bound of the statistics, and a step)
+            D = 20 + 8 * -(-cols // 2048)
+            yd, rd = y.double(), ref.double()
+            h = ((rd - tb.double()) / tg.double()).abs()
+            tol = 2 * U * (tg.double().abs() * (D + h * (1.5 * D + 12) + 2) + 2 * rd.abs() + tb.double().abs())
+            assert torch.all((yd - rd).abs() <= 2 * tol + 2 * half * rd.abs() + (2.0 ** -24 if dtype == "fp16" else 0))
+        y.fill_(7.0)
+        assert torch.all(buf == 7.0)
