@@ -87,7 +87,10 @@ CLASS_SOURCES = {
     "quant": ["fp8.cu", "sm100_ptx.cuh", "kernels.h"],
     "small": ["forward_small.cu", "sm100_ptx.cuh", "kernels.h"],
     "embed_proj": ["embed_proj.cu", "sm100_ptx.cuh", "kernels.h"],
+    "mx4_rows": ["mx4_quant.cu", "mx4.cuh", "mx4.h", "sm100_ptx.cuh", "kernels.h"],
 }
+# Layer products on narrower operands: their nominal dense rate over bf16's.
+PRODUCT_RATE = {"fp8": (2.0, "E4M3"), "mxfp4": (4.0, "E2M1"), "nvfp4": (4.0, "E2M1")}
 
 
 def source_set(cls: str, seq_len: int = 128) -> str:
@@ -95,6 +98,8 @@ def source_set(cls: str, seq_len: int = 128) -> str:
         return "gemm"
     if cls == "quant_e4m3":
         return "quant"
+    if cls in ("quant_mx4", "layer_norm_mx4"):
+        return "mx4_rows"
     if cls == "small_batch_forward":
         return "small"
     if cls == "embed_proj":
@@ -599,11 +604,12 @@ def measure_workload(args, ctx, name, padded, graph_mode, extras):
     peak = peaks.get("bf16_tflops", FALLBACK_PEAKS["bf16_tflops"])
     peak_sus = peaks.get("bf16_tflops_sustained")
     peak_note = f"{peaks_src} bf16_tflops (burst)"
-    fp8_classes = ("gemm_qkv", "gemm_out_proj_ln", "gemm_ffn_up_gelu", "gemm_ffn_down_ln")
-    if args.dtype == "fp8":
-        # E4M3 products: the measured bf16 peak times the nominal dense fp8 / bf16 ratio (2)
-        peak, peak_sus = 2.0 * peak, (2.0 * peak_sus if peak_sus else None)
-        peak_note = f"{peaks_src} bf16_tflops (burst) x 2, the nominal dense E4M3 / bf16 ratio"
+    layer_classes = ("gemm_qkv", "gemm_out_proj_ln", "gemm_ffn_up_gelu", "gemm_ffn_down_ln")
+    rate, operands = PRODUCT_RATE.get(args.dtype, (1.0, "bf16"))
+    if rate > 1.0:
+        # the measured bf16 peak times the nominal dense ratio of the operands' type
+        peak, peak_sus = rate * peak, (rate * peak_sus if peak_sus else None)
+        peak_note = f"{peaks_src} bf16_tflops (burst) x {rate:.0f}, the nominal dense {operands} / bf16 ratio"
     lenreg = (measure_length_regulation(torch, synth, tea, L, flush, peaks, peaks_src, stream, args.steps)
               if extras else None)
     dom_ms = dom[1] / max(dom[0], 1)
@@ -620,12 +626,22 @@ def measure_workload(args, ctx, name, padded, graph_mode, extras):
                         "peak": hbm, "unit": "GB/s", "bytes_per_launch": qbytes,
                         "peak_source": f"{peaks_src} hbm_gbs"}
         roofline_hbm["frac"] = roofline_hbm["achieved"] / hbm
+    elif dominant in ("quant_mx4", "layer_norm_mx4"):
+        # 768 wide: bf16 rows read (and written, by the LayerNorm), half a byte and a block's
+        # scale byte per value written
+        qbytes = rows * 768 * ((4 if dominant == "layer_norm_mx4" else 2) + 0.5 + 1.0 / (32 if args.dtype == "mxfp4" else 16))
+        hbm = peaks.get("hbm_gbs", FALLBACK_PEAKS["hbm_gbs"])
+        roofline_hbm = {"kernel": dominant, "bound": "hbm", "achieved": qbytes / (dom_ms / 1000.0) / 1e9,
+                        "peak": hbm, "unit": "GB/s", "bytes_per_launch": qbytes,
+                        "peak_source": f"{peaks_src} hbm_gbs"}
+        roofline_hbm["frac"] = roofline_hbm["achieved"] / hbm
     else:
         roofline_hbm = None
-    # E4M3 runs have their own capture (workload label + "_e4m3")
-    traffic, traffic_note = load_traffic(dominant, label + ("_e4m3" if args.dtype == "fp8" else ""), wl.T)
+    # runs on narrower operands have captures of their own (workload label + "_e4m3", "_mxfp4", "_nvfp4")
+    traffic, traffic_note = load_traffic(
+        dominant, label + {"bf16": "", "fp8": "_e4m3"}.get(args.dtype, "_" + args.dtype), wl.T)
     bound = "tensor"
-    dom_peak = peak if (args.dtype == "bf16" or dominant in fp8_classes) else peak / 2.0
+    dom_peak = peak if dominant in layer_classes else peak / rate
     roofline = {"kernel": dominant, "bound": bound, "achieved": achieved, "peak": dom_peak,
                 "unit": "TFLOP/s", "frac": achieved / dom_peak, "traffic": traffic, "traffic_source": traffic_note,
                 "peak_source": f"{peak_note} (the kernel runs {dom_ms * 1000:.0f} us inside a {ms_per_step:.3f} ms step)",
@@ -641,7 +657,8 @@ def measure_workload(args, ctx, name, padded, graph_mode, extras):
         "metric": METRIC, "value": value, "unit": UNIT, "n_gpus": world, "steps": args.steps,
         "warmup": args.warmup, "ms_per_step": ms_per_step, "higher_is_better": True,
         "scaling": "weak", "vs_baseline": None,
-        "dtype": "bf16" if args.dtype == "bf16" else "e4m3 (the four layer GEMMs) + bf16",
+        "dtype": "bf16" if args.dtype == "bf16" else
+                 f"{'e4m3' if args.dtype == 'fp8' else args.dtype} (the four layer GEMMs) + bf16",
         "data": "synthetic (seeded N(0,0.02) weights rounded to bf16, seeded ids and lengths)",
         "config": {"workload": label, "batch": wl.B,
                    "seq_len": wl.T, "lengths": wl.describe(), "valid_tokens_per_step_per_gpu": n_tok,
@@ -699,8 +716,9 @@ def main():
                     help="time replays of the forward captured in a CUDA graph instead of stream launches")
     ap.add_argument("--ncu-forwards", type=int, default=0,
                     help="run this many untimed forwards and exit (for ncu captures); no JSON metric line")
-    ap.add_argument("--dtype", default="bf16", choices=["bf16", "fp8"],
-                    help="fp8: the four layer GEMMs on E4M3 operands with per-row scales")
+    ap.add_argument("--dtype", default="bf16", choices=["bf16", "fp8", "mxfp4", "nvfp4"],
+                    help="fp8: the four layer GEMMs on E4M3 operands with per-row scales; "
+                         "mxfp4, nvfp4: on E2M1 operands with block scales")
     ap.add_argument("--small-batch", default="on", choices=["on", "off"],
                     help="off: batches of at most 128 token rows also take the per-layer kernels")
     ap.add_argument("--all-configs", action="store_true",

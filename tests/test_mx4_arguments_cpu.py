@@ -67,3 +67,10 @@ def test_status_is_asked_on_the_streams_device(monkeypatch):
     stream = types.SimpleNamespace(device=torch.device("cuda", 3), cuda_stream=77)
     assert tea.mx4_status(stream) == 8
     assert log == [("on", "cuda:3"), ("ask", 77), ("off", "cuda:3")]
+
+
+def test_bench_knows_the_4_bit_kernels_classes():
+    import bench
+    for cls in ("quant_mx4", "layer_norm_mx4"):
+        assert bench.source_set(cls) == "mx4_rows" and bench.sources_digest(cls) != bench.sources_digest("attention")
+    assert bench.PRODUCT_RATE["mxfp4"] == bench.PRODUCT_RATE["nvfp4"] == (4.0, "E2M1")
