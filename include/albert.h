@@ -376,7 +376,8 @@ size_t albert_mx4_scales_bytes(int rows, int cols, int fmt);
 int albert_mx4_quantize(const void *x, int x_type, long long ld_x, int rows, int cols, int fmt, float tensor_scale,
                         void *codes, void *scales, void *stream);
 
-/* The values of a 4-bit tensor, rounded once to out_type: out [rows, cols]. */
+/* The values of a 4-bit tensor, rounded to out_type: out [rows, cols].  ALBERT_NVFP4: q * sb is
+ * exact, its product with ts is rounded to fp32 first. */
 int albert_mx4_dequantize(const void *codes, const void *scales, int rows, int cols, int fmt, float tensor_scale,
                           void *out, int out_type, long long ld_out, void *stream);
 

@@ -669,7 +669,8 @@ def mx4_quantize(x, fmt: str = "mxfp4", tensor_scale: float = 1.0, out: Mx4Tenso
 
 
 def mx4_dequantize(t: Mx4Tensor, dtype=None, out=None, stream=None):
-    """The values of a 4-bit matrix, rounded once to `dtype` (default bfloat16)."""
+    """The values of a 4-bit matrix, rounded to `dtype` (default bfloat16); an "nvfp4" matrix's
+    tensor scale is multiplied in fp32."""
     torch = _torch or _mx4_torch()
     dev = t._dev
     if _mx4_away(dev, stream):

@@ -30,10 +30,13 @@
 // Tensor memory holds four scale units (a stage of mxfp4, half a stage of nvfp4, 24
 // columns on pairs).  A unit's columns are written again only after the products that
 // read them have completed: their stage's empty barrier, or the commit in its middle.
-// (With two whole stages of nvfp4 the copies waited for products: 8192^3 250 us, 245 now.)
-// What bounds it: at K = 768 the epilogue (18797 x 2304: 24.2 us, 86.6 MB of results alone
-// are 13 at the copy rate); at 8192^3 the power cap -- the main loop takes 654 (mxfp4) and
-// 705 (nvfp4) cycles a stage where the nominal rate is 512, at 1.6 GHz; 194 and 206 us.
+// (With two whole stages of nvfp4 the copies waited for products: the step took 8192^3, the
+// product alone, from 219 to 217 us.)
+// What bounds it: at K = 768 the epilogue (18797 x 2304: 24.6 us, 86.6 MB of results alone
+// are 13 at the copy rate); at 8192^3 the main loop, which takes 654 (mxfp4) and 705 (nvfp4)
+// cycles a stage where the nominal rate is 512, at the 1.6 GHz that the power cap leaves; 190
+// and 203 us.  Which wait those cycles go to has not been found: a library product of the same
+// operands took 176 us under the same cap.
 // Every wait is bounded; see the bf16 GEMM.
 #include <type_traits>
 

@@ -40,8 +40,8 @@ __device__ __forceinline__ void umma_mx4(uint32_t leader, uint32_t d_tmem, uint6
 
 // Copies one 512-byte scale tile (32 rows of 16 bytes) from shared memory to four
 // tensor-memory columns, repeated in the four 32-lane quadrants; pair form: each
-// CTA's tile at this offset to its own tensor memory.  Executes in order with the
-// products that this thread issues after it.
+// CTA's tile at this offset to its own tensor memory.  Products of another thread that read
+// these columns wait for a commit behind it.
 template <bool PAIR>
 __device__ __forceinline__ void tmem_cp_scales(uint32_t leader, uint32_t taddr, uint64_t s_desc) {
     if constexpr (PAIR)
@@ -52,7 +52,7 @@ __device__ __forceinline__ void tmem_cp_scales(uint32_t leader, uint32_t taddr, 
                      "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr), "l"(s_desc), "r"(leader) : "memory");
 }
 
-// umma_commit / umma_commit_pair (below) of the elected lane.
+// umma_commit / umma_commit_pair (sm100_ptx.cuh) of the elected lane.
 template <bool PAIR>
 __device__ __forceinline__ void umma_commit_elected(uint32_t leader, uint32_t bar, uint16_t cta_mask) {
     if constexpr (PAIR)
@@ -65,7 +65,7 @@ __device__ __forceinline__ void umma_commit_elected(uint32_t leader, uint32_t ba
                      ::"r"(bar), "r"(leader) : "memory");
 }
 
-// tma_load_2d / tma_load_2d_pair of the elected lane.
+// tma_load_2d / tma_load_2d_pair (sm100_ptx.cuh) of the elected lane.
 template <bool PAIR>
 __device__ __forceinline__ void tma_load_elected(uint32_t leader, uint32_t dst, const void *tmap, uint32_t bar, int x, int y) {
     if constexpr (PAIR)

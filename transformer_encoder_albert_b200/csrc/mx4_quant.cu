@@ -974,7 +974,7 @@ template <typename T, bool NV>
 cudaError_t norm_typed(const Mx4NormArgs &a, cudaStream_t s, bool pdl) {
     // A warp per row once the rows fill the machine's warps several times over; a CTA per
     // row for few rows (5 rows of 1000: 4.4 us against 7.9), for rows a warp cannot hold
-    // in half its registers, and for rows without alignment (8192 x 767: 15.9 us against
+    // in half its registers, and for rows without alignment (8192 x 767: 16.9 us against
     // 21); both sides of the other widths at the kernel above.
     static std::atomic<int> c1[64], c3[64], wide[64];
     if (a.q.cols <= 256) return norm_launch<T, NV>(mx4_norm_warp_kernel<T, NV, 1>, c1, kQWarps, kQWarps, a, s, pdl);
