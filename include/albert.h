@@ -381,8 +381,9 @@ int albert_mx4_quantize(const void *x, int x_type, long long ld_x, int rows, int
 int albert_mx4_dequantize(const void *codes, const void *scales, int rows, int cols, int fmt, float tensor_scale,
                           void *out, int out_type, long long ld_out, void *stream);
 
-/* LayerNorm over each row of x (fp32 statistics; gamma, beta [cols] fp32):
- * y [rows, cols] of x_type (may be NULL), and the 4-bit form of the fp32 result. */
+/* LayerNorm over each row of x (fp32 statistics: a row's squared differences from its mean
+ * sum to less than 3e38; gamma, beta [cols] fp32): y [rows, cols] of x_type (may be NULL, or
+ * x's own rows), and the 4-bit form of the fp32 result. */
 int albert_mx4_layer_norm(const void *x, int x_type, long long ld_x, const float *gamma, const float *beta, float eps,
                           int rows, int cols, int fmt, float tensor_scale, void *y, long long ld_y, void *codes,
                           void *scales, void *stream);

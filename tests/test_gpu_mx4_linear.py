@@ -299,6 +299,27 @@ def test_one_of_several_callers_takes_a_recorded_status():
         assert sorted(got) == [0] * 7 + [8]
 
 
+def test_calls_with_a_stream_may_be_captured_on_it():
+    x, g, b = torch.randn(300, 768, device="cuda", dtype=torch.bfloat16), torch.ones(768, device="cuda"), torch.zeros(768, device="cuda")
+    w = tea.mx4_quantize(torch.randn(512, 768, device="cuda") * 0.05, "mxfp4")
+
+    def go(s):
+        y, y4 = tea.mx4_layer_norm(x, g, b, 1e-5, stream=s)
+        h = tea.mx4_linear_quant(y4, w, gelu=True, stream=s)
+        return y, tea.mx4_dequantize(h, stream=s), tea.mx4_linear(x, w, stream=s), tea.mx4_linear(x[:3], w, stream=s)
+
+    ref = go(None)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = go(torch.cuda.current_stream())
+    for _ in range(2):
+        for o in out:
+            o.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, r) for o, r in zip(out, ref))
+
+
 def test_the_first_calls_of_a_process_may_be_captured():
     """Nothing that the entries look up or set up on their first call keeps it out of a graph."""
     import subprocess

@@ -130,3 +130,20 @@ def test_normalized_rows_at_any_offset_of_a_wider_buffer(rows, cols, dtype):
             assert torch.all((yd - rd).abs() <= 2 * tol + 2 * half * rd.abs() + (2.0 ** -24 if dtype == "fp16" else 0))
         y.fill_(7.0)
         assert torch.all(buf == 7.0)
+
+
+@pytest.mark.parametrize("rows,cols", SHAPES)
+def test_rows_with_a_nan_or_an_infinity_are_nan_and_no_others(rows, cols):
+    rows = max(rows, 5)
+    x = torch.randn(rows, cols, device="cuda")
+    x[0, cols // 2] = float("nan")
+    x[1, 0] = float("inf")
+    x[2, cols - 1] = -float("inf")
+    y, q = tea.mx4_layer_norm(x, torch.ones(cols, device="cuda"), torch.zeros(cols, device="cuda"), 1e-5)
+    back = tea.mx4_dequantize(q, dtype=torch.float32)
+    assert torch.isnan(y[:3]).all() and torch.isnan(back[:3]).all()
+    assert torch.isfinite(y[3:]).all() and torch.isfinite(back[3:]).all()
+    # and far beyond fp32's square: beta, not NaN
+    y, _ = tea.mx4_layer_norm(torch.full((2, cols), 1e33, device="cuda") * torch.linspace(-1, 1, cols, device="cuda"),
+                              torch.ones(cols, device="cuda"), torch.full((cols,), 0.5, device="cuda"), 1e-5)
+    assert torch.isfinite(y).all()

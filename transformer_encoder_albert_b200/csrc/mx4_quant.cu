@@ -417,9 +417,10 @@ __device__ __forceinline__ float warp_sums(float a, float b, int lane) {
     for (int o = 8; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     return s;
 }
-// From the means of d^2 and of d: rstd, and -e rstd.  (A variance below 0 is rounding; NaN stays.)
+// From the means of d^2 and of d: rstd, and -e rstd.  (A variance below 0 is rounding; NaN and
+// infinity stay.)
 __device__ __forceinline__ float2 norm_factors(float mean_sq, float e, float eps) {
-    const float var = fmaf(-e, e, mean_sq);
+    const float var = mean_sq < __int_as_float(0x7f800000) ? fmaf(-e, e, mean_sq) : mean_sq;
     const float rstd = rsqrtf((var < 0.f ? 0.f : var) + eps);
     return make_float2(rstd, -e * rstd);
 }
@@ -541,7 +542,7 @@ mx4_norm_warp_kernel(const T *__restrict__ x, long long ld, const float *__restr
 // next row's values load while this one's sums are joined.  WORDS: rows that are not
 // 16-byte aligned, or of a width that is no multiple of 8, come and go by words.  What
 // bounds it over many rows is instructions: 8192 rows of 1000, 2048, 4096 bf16 columns take
-// 9.1, 15.8 and 34.5 us (eight columns a lane: 10.7, 20.9, 43; in the kernel for wider rows
+// 9.1, 15.9 and 35.6 us (eight columns a lane: 10.7, 20.9, 43; in the kernel for wider rows
 // 25, 33, 58), of 1001 by words 16.8 (by values, in that kernel, 30).
 template <int W>
 __device__ __forceinline__ float block_sum(float v, float *red) {
